@@ -16,6 +16,12 @@
  *                       workgroups
  *   idx_insert_quantize, idx_logits_paged_insert (and their _rope forms, with
  *                       the query RoPE): a decode step's calls in fewer launches
+ *   idx_step_map        a step's block-table entries, slots, positions and windows
+ *                       from its request lengths
+ *   idx_norm_rope       per-head norm and RoPE of the indexer's q and k rows
+ *   idx_latent_insert   norm + RoPE of the main cache's latent rows -> paged cache
+ *   idx_attn_paged      attention over the paged latent cache: the tokens of
+ *                       idx_topk's lists, or whole windows
  *   idx_*_fp8           the FP8 (E4M3) indexer cache the MXFP4 one replaces:
  *                       quantize, insert, gather, dense and paged logits,
  *                       and idx_logits_paged_insert_fp8, its decode step's
@@ -97,6 +103,7 @@ typedef enum { IDX_BF16 = 0, IDX_F32 = 1 } idx_dtype;
 #define IDX_TOPK_MAX 2048
 #define IDX_MAX_DECODE_SEQS 65535
 #define IDX_MERGE_MAX_CANDIDATES 8192
+#define IDX_LATENT_ROPE 64         /* rotated values of a latent row */
 
 /* Version of this ABI (major * 100 + minor). */
 int idx_version(void);
@@ -532,6 +539,153 @@ int idx_topk_noalloc(const float* logits, int64_t rows, int64_t logits_row_strid
  * 1 <= k <= 2048, interleave >= 1; global positions must be < 2^31. */
 int idx_topk_merge(const float* values, const int32_t* indices, int world, int64_t rows,
                    int k_in, int interleave, int k, int32_t* out_idx, hipStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Around the indexer: a serving step's bookkeeping, its norms and rotations,
+ * and the attention that reads what idx_topk chose.
+ * ------------------------------------------------------------------------- */
+
+/* idx_step_map -- a serving step's bookkeeping from its request lengths, on the
+ * device (no host round trip, so a captured step follows its requests): the
+ * block-table entries of pages that the step enters, and for each of its rows the
+ * slot, position, sequence and visible window that the other calls take.
+ *   seq_lens, query_lens: [B] int32; request b has seq_lens[b] tokens, the last
+ *     query_lens[b] of them new (0 <= query_lens[b] <= seq_lens[b]; 0: the request
+ *     has no row in this step).  Negative lengths count as 0.
+ *   The step's rows are the requests' new tokens in order: request b's rows begin
+ *   at row sum(query_lens[:b]).  num_rows is how many rows the outputs hold; rows
+ *   behind the last new token are padding, new tokens behind num_rows are dropped.
+ *   block_table: [B, bt_row_stride] int32, bt_pages columns in use; NULL only when
+ *     slot_mapping is NULL too.  With free_pages NULL it is read only.  With free_pages
+ *     it is read up to the pages a request held before the step,
+ *     ceil((seq_lens - query_lens) / page_size), and its entries of the pages that
+ *     the step enters are written: page j of request b becomes
+ *     free_pages[free_start[0] + entered(b') for all b' < b + (j - held(b))], or -1
+ *     past the list's end (so a caller that retries the step writes the same).
+ *   free_pages: [num_free] int32 page ids; free_start: [1] int64, the next unused entry;
+ *     free_next: [1] int64 out = free_start[0] + pages entered by the step; above
+ *     num_free it says how many pages were lacking (without a list: the pages entered).
+ *     It must not be free_start's address.
+ *   columns: IDX_COLUMNS_SEQUENCE: ks = 0, ke = position + 1 (columns of paged logits);
+ *     IDX_COLUMNS_GATHERED: both plus sum(seq_lens[:b]), the request's first row of a
+ *     gathered K (idx_gather, dense logits).  The last column must be < 2^31.
+ *   slot_mapping [num_rows] int64 out: page * page_size + position % page_size, -1 where
+ *     the page is negative or past bt_pages and for padding.
+ *   positions [num_rows] int64, row_seq [num_rows] int32, ks, ke [num_rows] int32 out;
+ *     padding gets position 0, sequence -1 and the empty window 0, 0.
+ *   cu_seq_offsets [B + 1] int64 out: sum(seq_lens[:b]) (idx_gather's offsets), last the total.
+ *   Any output may be NULL.  Page ids' upper bound is not checked: the calls that take
+ *   slots and tables skip what lies outside their cache.
+ * page_size must be 64; 0 <= B <= IDX_MAX_DECODE_SEQS.  With B = 0 the rows are all padding,
+ * cu_seq_offsets[0] = 0 and free_next = free_start. */
+typedef enum { IDX_COLUMNS_SEQUENCE = 0, IDX_COLUMNS_GATHERED = 1 } idx_columns;
+int idx_step_map(const int32_t* seq_lens, const int32_t* query_lens, int B, int32_t* block_table,
+                 int64_t bt_row_stride, int64_t bt_pages, const int32_t* free_pages,
+                 int64_t num_free, const int64_t* free_start, int64_t* free_next, int page_size,
+                 int columns, int64_t num_rows, int64_t* slot_mapping, int64_t* positions,
+                 int32_t* row_seq, int32_t* ks, int32_t* ke, int64_t* cu_seq_offsets,
+                 hipStream_t stream);
+
+/* The norm of a row x of n values, in fp32:
+ *   IDX_NORM_RMS:   y = x * rsqrt(mean(x^2) + eps) * weight + bias
+ *   IDX_NORM_LAYER: y = (x - m) * rsqrt(mean((x - m)^2) + eps) * weight + bias, m = mean(x)
+ *   IDX_NORM_NONE:  y = x (weight, bias and eps are not read). */
+typedef enum { IDX_NORM_NONE = 0, IDX_NORM_RMS = 1, IDX_NORM_LAYER = 2 } idx_norm;
+
+/* idx_heads -- one set of rows of idx_norm_rope (host memory, read during the call only). */
+typedef struct {
+  const void* x;              /* [T, heads, 128]: row (t, h) at x + t*row_stride + h*head_stride */
+  void* out;                  /* the same shape and type, out_row_stride / out_head_stride */
+  int64_t row_stride, head_stride, out_row_stride, out_head_stride;   /* in elements */
+  int heads;
+  int norm;                   /* idx_norm */
+  const float* weight;        /* [128] fp32, 16-byte aligned, or NULL (all ones) */
+  const float* bias;          /* [128] fp32, 16-byte aligned, or NULL (zeros) */
+  float eps;                  /* >= 0 */
+} idx_heads;
+
+/* idx_norm_rope -- per-head norm and rotary position embedding of the indexer's
+ * query and key rows in one pass and one launch: what feeds idx_insert,
+ * idx_quantize and the one-launch decode steps, whose own rotation covers the
+ * query only.
+ *   q, k: one of them may be NULL (or have 0 heads).  Each row is normed over its
+ *     128 values, then its first rope_dim values are rotated as idx_quantize_rope
+ *     does (both pairings, no fused multiply-add; token t takes table row
+ *     positions[t], NULL: row t, which needs table_rows >= T; rows outside the
+ *     table are not rotated), then rounded once to dtype.  fp32 throughout; with
+ *     IDX_NORM_NONE and fp32 rows, idx_quantize of the output gives
+ *     idx_quantize_rope's bytes.
+ *   dtype: IDX_BF16 or IDX_F32, of every x and out.  Pointers 16-byte aligned,
+ *     strides multiples of 8 (bf16) or 4 (fp32), head strides >= 128 where heads
+ *     > 1.  out may be x itself with the same strides; any other overlap, also of
+ *     q's and k's rows with each other's output, is not allowed.
+ *   rope: required (rope_dim 0 rotates nothing). */
+int idx_norm_rope(const idx_heads* q, const idx_heads* k, int dtype, int64_t T,
+                  const idx_rope* rope, hipStream_t stream);
+
+/* idx_latent_insert -- the main cache's rows of a step: each token's latent row is
+ * normed and its positional part rotated, and the row is written to its slot;
+ * the positional part of the query heads is rotated in the same launch.
+ *   Latent cache: num_pages pages of page_size rows of latent + 64 bf16 values, the
+ *     row of slot s = page * page_size + offset at (s * (latent + 64)).  One row serves
+ *     all heads: its `latent` first values are the attention's values, all of them
+ *     its key.  latent is 128, 256 or 512.
+ *   kv: [T, kv_row_stride] of dtype (IDX_BF16 / IDX_F32): `latent` values, RMS-normed
+ *     with weight ([latent] fp32, 16-byte aligned; NULL: all ones; norm IDX_NORM_NONE or
+ *     IDX_NORM_RMS) and then 64 rotated ones, rounded once to bf16.
+ *   slot_mapping: [T] int64; slots outside the cache write nothing; the others must be
+ *     distinct.
+ *   rope: required, rope_dim 64: pairings, tables and positions as for idx_norm_rope.
+ *   q_pe: NULL, or [T, H, 64] of dtype (row (t, h) at q_pe + t*q_row_stride +
+ *     h*q_head_stride): rotated at the token's position and written as bf16 to q_out +
+ *     t*out_row_stride + h*out_head_stride (values 64): with q_out = q + latent the tail
+ *     of idx_attn_paged's query rows.  Rows of tokens without a slot are written too.
+ *   kv, q_pe and q_out 16-byte aligned, strides multiples of 8 (bf16) or 4 (fp32 inputs);
+ *   cache 16-byte aligned; page_size must be 64.  No output may overlap an input. */
+int idx_latent_insert(const void* kv, int dtype, int64_t T, int64_t kv_row_stride, int latent,
+                      int norm, const float* weight, float eps, const idx_rope* rope,
+                      const int64_t* slot_mapping, void* cache, int64_t num_pages, int page_size,
+                      const void* q_pe, int H, int64_t q_row_stride, int64_t q_head_stride,
+                      void* q_out, int64_t out_row_stride, int64_t out_head_stride,
+                      hipStream_t stream);
+
+/* idx_attn_paged -- attention of a step's query rows over the paged latent cache
+ * (idx_latent_insert's), over the tokens of idx_topk's lists or over whole windows:
+ *   s_j = scale * sum_i q[r,h,i] * row_j[i] over the latent + 64 values,
+ *   out[r,h,:] = sum_j softmax_j(s) * row_j[:latent],  lse[r,h] = log sum_j exp(s_j)
+ * over the visible tokens j of row r.  A row that sees none gets out = 0, lse = -inf.
+ *   q:   [rows, H, latent + 64] bf16, row (r, h) at q + r*q_row_stride + h*q_head_stride;
+ *        strides multiples of 8, 16-byte aligned; 1 <= H <= 128; latent 128, 256 or 512.
+ *   cache, num_pages, page_size (64); block_table [B, bt_row_stride] int32 with
+ *        bt_row_stride >= ceil(max_tokens / 64).
+ *   row_seq: [rows] int32, the row's sequence; NULL: rows is a multiple of B and row r
+ *        belongs to sequence r / (rows / B).  Rows whose sequence is outside [0, B) are left
+ *        as they are.
+ *   ks, ke: [rows] int32 (ks NULL: zeros), as idx_topk takes them: column c stands for
+ *        the sequence's token c - ks[r], and the row sees tokens 0 .. ke[r] - ks[r] - 1.
+ *   indices: NULL: the row reads its whole window.  Otherwise [rows, idx_row_stride] int32,
+ *        k columns a row, as idx_topk returns them: a token for each entry whose column lies
+ *        in [ks, ke), in any order; others (-1) are skipped, and an entry that appears twice
+ *        counts twice.
+ *   max_tokens: host-side upper bound of ke - ks: later tokens are not read.  Tokens whose
+ *        page lies outside the cache are skipped.
+ *   out: [rows, H, latent] bf16, strides multiples of 4, 8-byte aligned; lse: [rows, H]
+ *        fp32 or NULL.
+ *   workspace: device memory of at least idx_attn_workspace_bytes(rows, H, latent, k with
+ *        indices, else max_tokens) bytes, 256-byte aligned, as for idx_topk_ws: no
+ *        initialization, scratch after the call, not shared by calls that may run at the
+ *        same time.  May be NULL where that size is 0.
+ * Products are exact, sums and softmax statistics fp32; the softmax weights are rounded to
+ * bf16 for the second product (the statistics, and so lse, take them unrounded), the output
+ * once. */
+size_t idx_attn_workspace_bytes(int64_t rows, int H, int latent, int64_t entries);
+int idx_attn_paged(const void* q, int64_t q_row_stride, int64_t q_head_stride, int64_t rows, int H,
+                   int latent, const void* cache, int64_t num_pages, int page_size,
+                   const int32_t* block_table, int64_t bt_row_stride, int B,
+                   const int32_t* row_seq, const int32_t* ks, const int32_t* ke,
+                   const int32_t* indices, int64_t idx_row_stride, int k, int64_t max_tokens,
+                   float scale, void* out, int64_t out_row_stride, int64_t out_head_stride,
+                   float* lse, void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -9,6 +9,7 @@ PyTorch fallback, and a missing library raises ``MxidxError``.
 Build the library with ``python -m mxfp4_paged_cache_quant_amd.build``.
 """
 
+import collections
 import ctypes
 import os
 
@@ -21,6 +22,8 @@ __all__ = [
     "ROPE_INTERLEAVED", "kpool_insert",
     "quantize_fp8", "insert_fp8", "gather_fp8", "logits_prefill_fp8", "logits_paged_fp8",
     "logits_paged_insert_fp8",
+    "StepMap", "step_map", "norm_rope", "latent_insert", "attn_paged", "attn_workspace_bytes",
+    "attn_workspace", "LATENT_ROPE", "LATENT_DIMS",
     "FP8_ROW_BYTES", "FP8_SCALE_F32", "FP8_SCALE_POW2",
     "HEAD_DIM", "ROW_BYTES", "PAGE_SIZE", "TOPK_MAX", "EXPORTS",
 ]
@@ -36,6 +39,8 @@ TOPK_NOALLOC_MAX_WORKSPACE = 36 << 20
 FP8_ROW_BYTES = 132
 FP8_SCALE_F32, FP8_SCALE_POW2 = 0, 1
 ROPE_NEOX, ROPE_INTERLEAVED = 0, 1
+LATENT_ROPE = 64
+LATENT_DIMS = (128, 256, 512)
 
 IDX_BF16, IDX_F32 = 0, 1
 
@@ -46,12 +51,23 @@ class _Rope(ctypes.Structure):
                 ("table_rows", ctypes.c_int64), ("positions", ctypes.c_void_p),
                 ("rope_dim", ctypes.c_int), ("rope_mode", ctypes.c_int)]
 
+
+class _Heads(ctypes.Structure):
+    """The C ABI's idx_heads block (include/mxidx.h)."""
+    _fields_ = [("x", ctypes.c_void_p), ("out", ctypes.c_void_p),
+                ("row_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("out_row_stride", ctypes.c_int64), ("out_head_stride", ctypes.c_int64),
+                ("heads", ctypes.c_int), ("norm", ctypes.c_int), ("weight", ctypes.c_void_p),
+                ("bias", ctypes.c_void_p), ("eps", ctypes.c_float)]
+
+
 _HERE = os.path.dirname(os.path.abspath(__file__))
 lib_path = os.path.join(_HERE, "libmxidx.so")
 
 _c_void_p = ctypes.c_void_p
 _i64 = ctypes.c_int64
 _int = ctypes.c_int
+_float = ctypes.c_float
 
 # name -> (restype, argtypes); must match include/mxidx.h
 EXPORTS = {
@@ -106,6 +122,18 @@ EXPORTS = {
                                 _c_void_p]),
     "idx_topk_merge": (_int, [_c_void_p, _c_void_p, _int, _i64, _int, _int, _int, _c_void_p,
                               _c_void_p]),
+    "idx_step_map": (_int, [_c_void_p, _c_void_p, _int, _c_void_p, _i64, _i64, _c_void_p, _i64,
+                            _c_void_p, _c_void_p, _int, _int, _i64, _c_void_p, _c_void_p, _c_void_p,
+                            _c_void_p, _c_void_p, _c_void_p, _c_void_p]),
+    "idx_norm_rope": (_int, [_c_void_p, _c_void_p, _int, _i64, _c_void_p, _c_void_p]),
+    "idx_latent_insert": (_int, [_c_void_p, _int, _i64, _i64, _int, _int, _c_void_p, _float,
+                                 _c_void_p, _c_void_p, _c_void_p, _i64, _int, _c_void_p, _int, _i64,
+                                 _i64, _c_void_p, _i64, _i64, _c_void_p]),
+    "idx_attn_workspace_bytes": (ctypes.c_size_t, [_i64, _int, _int, _i64]),
+    "idx_attn_paged": (_int, [_c_void_p, _i64, _i64, _i64, _int, _int, _c_void_p, _i64, _int,
+                              _c_void_p, _i64, _int, _c_void_p, _c_void_p, _c_void_p, _c_void_p,
+                              _i64, _int, _i64, _float, _c_void_p, _i64, _i64, _c_void_p, _c_void_p,
+                              ctypes.c_size_t, _c_void_p]),
 }
 
 
@@ -860,3 +888,315 @@ def topk_merge(values, indices, interleave, k, out=None, stream=None):
     _check(lib().idx_topk_merge(_ptr(values), _ptr(indices), world, rows, k_in, interleave, k,
                                 _ptr(out), _stream(stream)), "idx_topk_merge")
     return out
+
+
+# ---------------------------------------------------------------------------
+# a serving step around the indexer
+# ---------------------------------------------------------------------------
+
+_NORMS = {"none": 0, "rms": 1, "layer": 2}
+_MODES = {"neox": ROPE_NEOX, "interleaved": ROPE_INTERLEAVED}
+_COLUMNS = {"sequence": 0, "gathered": 1}
+
+
+def _code(table, value, name):
+    try:
+        return table[value]
+    except (KeyError, TypeError):
+        raise MxidxError(f"{name} must be one of {sorted(table)}, got {value!r}") from None
+
+
+def _on(device, t, name, dtype, shape=None):
+    """t: a tensor of that type on that device, contiguous with that shape where one is given."""
+    if not t.is_cuda or t.device != device:
+        raise MxidxError(f"{name} must be a device tensor on {device}, got {t.device}")
+    if t.dtype != dtype:
+        raise MxidxError(f"{name} must be {dtype}, got {t.dtype}")
+    if shape is not None and (tuple(t.shape) != shape or not t.is_contiguous()):
+        raise MxidxError(f"{name} must be contiguous of shape {shape}, got {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _call(name, device, stream, *args):
+    """One call of the library with `device` current, on `stream` (None: that device's
+    current stream)."""
+    torch = _torch()
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    elif stream.device != device:
+        raise MxidxError(f"{name}: the stream belongs to {stream.device}, the tensors to {device}")
+    fn = getattr(lib(), name)
+    if torch.cuda.current_device() == device.index:
+        status = fn(*args, stream.cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, stream.cuda_stream)
+    if status != 0:
+        _check(status, name)
+
+
+def _empty(stream, shape, dtype, device):
+    """A new tensor whose memory belongs to the call's stream."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _device_of(t, name):
+    if not t.is_cuda:
+        raise MxidxError(f"{name} must be a device tensor")
+    return t.device
+
+
+def _rope_args(device, cos, sin, rope_dim, mode, positions, tokens):
+    """The checked idx_rope block of a call on `device` (host memory; the tensors must outlive it)."""
+    torch = _torch()
+    rows = cos.shape[0]
+    half = int(rope_dim) // 2
+    cp = _on(device, cos, "cos", torch.float32, (rows, half))
+    sp = _on(device, sin, "sin", torch.float32, (rows, half))
+    pp = None if positions is None else _on(device, positions, "positions", torch.int64, (tokens,))
+    return _Rope(cp, sp, rows, pp, int(rope_dim), _code(_MODES, mode, "mode"))
+
+
+StepMap = collections.namedtuple("StepMap", ["slot_mapping", "positions", "row_seq", "ks", "ke",
+                                             "cu_seq_offsets", "free_next"])
+
+
+def step_map(seq_lens, query_lens, block_table, num_rows, free_pages=None, free_start=None,
+             free_next=None, columns="sequence", slot_mapping=None, positions=None, row_seq=None,
+             ks=None, ke=None, cu_seq_offsets=None, stream=None):
+    """A step's bookkeeping from its request lengths, in one launch: returns StepMap.
+
+    seq_lens / query_lens i32 [B]: each request's tokens and how many of them are new; the step's
+    rows are the new tokens in order, padded to ``num_rows``.  With ``free_pages`` (i32) and
+    ``free_start`` (i64 [1]) the pages that the step enters are taken from that list and
+    written into ``block_table`` [B, pages]; ``free_next`` (i64 [1]) says where the list
+    goes on.  ``columns``: "sequence" (paged logits) or "gathered" (rows of gather / dense
+    logits).  Padding rows get slot -1, position 0, sequence -1 and an empty window."""
+    torch = _torch()
+    device = _device_of(seq_lens, "seq_lens")
+    i32, i64 = torch.int32, torch.int64
+    B, rows = seq_lens.numel(), int(num_rows)
+    if rows < 0:
+        raise MxidxError("num_rows must not be negative")
+    sp = _on(device, seq_lens, "seq_lens", i32, (B,))
+    qp = _on(device, query_lens, "query_lens", i32, (B,))
+    bp = _on(device, block_table, "block_table", i32)
+    if block_table.dim() != 2 or block_table.shape[0] != B or \
+            (block_table.numel() and block_table.shape[1] > 1 and block_table.stride(1) != 1):
+        raise MxidxError("block_table must be [B, pages] with unit inner stride")
+    pages = block_table.shape[1]
+    stride = block_table.stride(0) if B > 1 else max(pages, 1)
+    fp = ip = None
+    free = 0
+    if free_pages is not None:
+        if free_start is None:
+            raise MxidxError("free_pages needs free_start")
+        free = free_pages.numel()
+        ip = _on(device, free_start, "free_start", i64, (1,))
+        # an empty list has no address of its own, and is still a list
+        fp = _on(device, free_pages, "free_pages", i32, (free,)) or ip
+    elif free_start is not None:
+        raise MxidxError("free_start needs free_pages")
+
+    def out(t, name, dtype, n):
+        if t is None:
+            return _empty(stream, n, dtype, device)
+        _on(device, t, name, dtype, (n,))
+        return t
+
+    slot_mapping = out(slot_mapping, "slot_mapping", i64, rows)
+    positions = out(positions, "positions", i64, rows)
+    row_seq = out(row_seq, "row_seq", i32, rows)
+    ks, ke = out(ks, "ks", i32, rows), out(ke, "ke", i32, rows)
+    cu_seq_offsets = out(cu_seq_offsets, "cu_seq_offsets", i64, B + 1)
+    free_next = out(free_next, "free_next", i64, 1)
+    _call("idx_step_map", device, stream, sp, qp, B, bp, stride, pages, fp, free, ip,
+          free_next.data_ptr(), PAGE_SIZE, _code(_COLUMNS, columns, "columns"), rows,
+          slot_mapping.data_ptr(), positions.data_ptr(), row_seq.data_ptr(), ks.data_ptr(),
+          ke.data_ptr(), cu_seq_offsets.data_ptr())
+    return StepMap(slot_mapping, positions, row_seq, ks, ke, cu_seq_offsets, free_next)
+
+
+def _heads_block(device, stream, x, out, norm, weight, bias, eps, name, tokens, dtype):
+    """(idx_heads block, out) of x [T, H, 128] or [T, 128]."""
+    torch = _torch()
+    _on(device, x, name, dtype)
+    if x.dim() not in (2, 3) or x.shape[-1] != HEAD_DIM or x.shape[0] != tokens:
+        raise MxidxError(f"{name} must be [{tokens}, H, {HEAD_DIM}] or [{tokens}, {HEAD_DIM}]")
+    if out is None:
+        out = _empty(stream, x.shape, dtype, device)
+    _on(device, out, f"{name}_out", dtype)
+    if out.shape != x.shape:
+        raise MxidxError(f"{name}_out must have {name}'s shape")
+    heads = x.shape[1] if x.dim() == 3 else 1
+    if tokens and heads:
+        if x.stride(-1) != 1 or out.stride(-1) != 1:
+            raise MxidxError(f"{name} and {name}_out must have a contiguous last dim")
+        if out.data_ptr() == x.data_ptr() and out.stride() != x.stride():
+            raise MxidxError(f"{name}_out may be {name} itself only with the same strides")
+    params = []
+    for what, p in (("weight", weight), ("bias", bias)):
+        params.append(None if p is None else
+                      _on(device, p, f"{name}_{what}", torch.float32, (HEAD_DIM,)))
+    xh = x.stride(1) if x.dim() == 3 else HEAD_DIM
+    oh = out.stride(1) if x.dim() == 3 else HEAD_DIM
+    return _Heads(x.data_ptr(), out.data_ptr(), x.stride(0), xh, out.stride(0), oh, heads,
+                  _code(_NORMS, norm, f"{name}_norm"), params[0], params[1], eps), out
+
+
+def norm_rope(q, k, cos, sin, rope_dim, mode="neox", positions=None, q_norm="none", q_weight=None,
+              q_bias=None, k_norm="layer", k_weight=None, k_bias=None, eps=1e-6, q_out=None,
+              k_out=None, stream=None):
+    """Per-head norm ("none", "rms", "layer"; fp32 weight / bias [128] or None) and RoPE on the
+    first ``rope_dim`` dims of the indexer's rows, in one launch: q [T, H, 128] and k
+    [T, 128] or [T, Hk, 128], bf16 or fp32, either of them None; cos / sin / positions /
+    mode as for quantize_rope.  Returns (q_out, k_out), of the inputs' type; an output may
+    be its input."""
+    first = q if q is not None else k
+    if first is None:
+        raise MxidxError("norm_rope needs q or k")
+    torch = _torch()
+    device = _device_of(first, "q" if q is not None else "k")
+    dtype = first.dtype
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise MxidxError("q and k must be bfloat16 or float32")
+    T = first.shape[0]
+    rope = _rope_args(device, cos, sin, rope_dim, mode, positions, T)
+    qb = kb = None
+    if q is not None:
+        qb, q_out = _heads_block(device, stream, q, q_out, q_norm, q_weight, q_bias, eps, "q", T, dtype)
+    if k is not None:
+        kb, k_out = _heads_block(device, stream, k, k_out, k_norm, k_weight, k_bias, eps, "k", T, dtype)
+    _call("idx_norm_rope", device, stream, None if qb is None else ctypes.addressof(qb),
+          None if kb is None else ctypes.addressof(kb), IDX_BF16 if dtype == torch.bfloat16 else IDX_F32,
+          T, ctypes.addressof(rope))
+    return (None if q is None else q_out), (None if k is None else k_out)
+
+
+def _latent_cache(device, cache):
+    """(address, num_pages, latent) of a latent cache."""
+    torch = _torch()
+    cp = _on(device, cache, "cache", torch.bfloat16)
+    if cache.dim() != 3 or cache.shape[1] != PAGE_SIZE or not cache.is_contiguous() or \
+            cache.shape[2] - LATENT_ROPE not in LATENT_DIMS:
+        raise MxidxError("cache must be a contiguous bfloat16 [num_pages, 64, latent + 64], latent "
+                         f"one of {LATENT_DIMS}")
+    return cp, cache.shape[0], cache.shape[2] - LATENT_ROPE
+
+
+def latent_insert(kv, slot_mapping, cache, cos, sin, mode="neox", positions=None, norm="rms",
+                  weight=None, eps=1e-6, q_pe=None, q_out=None, stream=None):
+    """Latent rows kv [T, latent + 64] (bf16 / fp32) into the latent cache [num_pages, 64,
+    latent + 64] bf16: the latent part RMS-normed (``norm`` "rms", fp32 ``weight`` [latent] or
+    None; or "none"), the last 64 values rotated (cos / sin fp32 [table_rows, 32]), slots < 0
+    skipped.  ``q_pe`` [T, H, 64]: the query's positional part, rotated into ``q_out``
+    [T, H, 64] bf16 (``q[..., latent:]`` of attn_paged's query, say) in the same launch.
+    Returns cache, or (cache, q_out) with q_pe."""
+    torch = _torch()
+    device = _device_of(kv, "kv")
+    dtype = kv.dtype
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise MxidxError("kv must be bfloat16 or float32")
+    cp, num_pages, latent = _latent_cache(device, cache)
+    if kv.dim() != 2 or kv.shape[1] != latent + LATENT_ROPE or (kv.shape[0] and kv.stride(1) != 1):
+        raise MxidxError(f"kv must be [T, {latent + LATENT_ROPE}] with a contiguous last dim")
+    T = kv.shape[0]
+    mp = _on(device, slot_mapping, "slot_mapping", torch.int64, (T,))
+    wp = None if weight is None else _on(device, weight, "weight", torch.float32, (latent,))
+    rope = _rope_args(device, cos, sin, LATENT_ROPE, mode, positions, T)
+    qp = op = None
+    H = qs = qh = os_ = oh = 0
+    if q_pe is not None:
+        qp = _on(device, q_pe, "q_pe", dtype)
+        if q_pe.dim() != 3 or q_pe.shape[0] != T or q_pe.shape[2] != LATENT_ROPE:
+            raise MxidxError(f"q_pe must be [{T}, H, {LATENT_ROPE}]")
+        if q_out is None:
+            q_out = _empty(stream, q_pe.shape, torch.bfloat16, device)
+        op = _on(device, q_out, "q_out", torch.bfloat16)
+        if q_out.shape != q_pe.shape:
+            raise MxidxError("q_out must have q_pe's shape")
+        if q_pe.numel() and (q_pe.stride(2) != 1 or q_out.stride(2) != 1):
+            raise MxidxError("q_pe and q_out must have a contiguous last dim")
+        H, qs, qh = q_pe.shape[1], q_pe.stride(0), q_pe.stride(1)
+        os_, oh = q_out.stride(0), q_out.stride(1)
+    elif q_out is not None:
+        raise MxidxError("q_out needs q_pe")
+    _call("idx_latent_insert", device, stream, kv.data_ptr(),
+          IDX_BF16 if dtype == torch.bfloat16 else IDX_F32, T, kv.stride(0), latent,
+          _code({"none": 0, "rms": 1}, norm, "norm"), wp, eps, ctypes.addressof(rope), mp, cp,
+          num_pages, PAGE_SIZE, qp, H, qs, qh, op, os_, oh)
+    return cache if q_pe is None else (cache, q_out)
+
+
+def attn_workspace_bytes(rows, heads, latent, entries):
+    """Workspace bytes of attn_paged; entries: k with indices, else max_tokens (0: no workspace)."""
+    return int(lib().idx_attn_workspace_bytes(rows, heads, latent, entries))
+
+
+def attn_workspace(rows, heads, latent, entries, device="cuda"):
+    """A workspace for attn_paged: reusable, not by calls that may run at the same time."""
+    torch = _torch()
+    return torch.empty(max(attn_workspace_bytes(rows, heads, latent, entries), 1),
+                       dtype=torch.uint8, device=device)
+
+
+def attn_paged(q, cache, block_table, ke, scale, indices=None, ks=None, row_seq=None,
+               max_tokens=None, out=None, lse=None, workspace=None, stream=None):
+    """Attention of query rows q [rows, H, latent + 64] (bf16) over the latent cache: returns
+    (out bf16 [rows, H, latent], lse fp32 [rows, H]).
+
+    Row r sees its sequence's tokens 0 .. ke[r] - ks[r] - 1 (ks None: 0), all of them or those
+    of ``indices`` (int32 [rows, k] columns in [ks, ke), topk's output; -1 skipped).
+    ``row_seq`` i32 [rows]: the row's sequence (None: rows / B rows each, in order); rows of no
+    sequence stay as they are.  ``max_tokens`` bounds ke - ks (None: what block_table holds).
+    ``workspace``: attn_workspace's, allocated here when it is not given."""
+    torch = _torch()
+    device = _device_of(q, "q")
+    cp, num_pages, latent = _latent_cache(device, cache)
+    qp = _on(device, q, "q", torch.bfloat16)
+    if q.dim() != 3 or q.shape[2] != latent + LATENT_ROPE or (q.numel() and q.stride(2) != 1):
+        raise MxidxError(f"q must be [rows, H, {latent + LATENT_ROPE}] with a contiguous last dim")
+    rows, H = q.shape[0], q.shape[1]
+    i32 = torch.int32
+    bp = _on(device, block_table, "block_table", i32)
+    if block_table.dim() != 2 or (block_table.numel() and block_table.shape[1] > 1 and block_table.stride(1) != 1):
+        raise MxidxError("block_table must be [B, pages] with unit inner stride")
+    B, pages = block_table.shape
+    stride = block_table.stride(0) if B > 1 else max(pages, 1)
+    if max_tokens is None:
+        max_tokens = pages * PAGE_SIZE
+    elif max_tokens > pages * PAGE_SIZE:
+        raise MxidxError("block_table has fewer pages than max_tokens needs")
+    ep = _on(device, ke, "ke", i32, (rows,))
+    kp = None if ks is None else _on(device, ks, "ks", i32, (rows,))
+    rp = None if row_seq is None else _on(device, row_seq, "row_seq", i32, (rows,))
+    ip, istride, k = None, 0, 0
+    if indices is not None:
+        ip = _on(device, indices, "indices", i32)
+        if indices.dim() != 2 or indices.shape[0] != rows or \
+                (indices.numel() and indices.shape[1] > 1 and indices.stride(1) != 1):
+            raise MxidxError("indices must be [rows, k] with unit inner stride")
+        k, istride = indices.shape[1], indices.stride(0)
+        ip = ip or ep      # a list of no columns has no address of its own, and is still a list
+    if out is None:
+        out = _empty(stream, (rows, H, latent), torch.bfloat16, device)
+    op = _on(device, out, "out", torch.bfloat16)
+    if tuple(out.shape) != (rows, H, latent) or (out.numel() and out.stride(2) != 1):
+        raise MxidxError(f"out must be [{rows}, {H}, {latent}] with a contiguous last dim")
+    if lse is None:
+        lse = _empty(stream, (rows, H), torch.float32, device)
+    lp = _on(device, lse, "lse", torch.float32, (rows, H))
+    if workspace is None:
+        need = attn_workspace_bytes(rows, H, latent, k if indices is not None else max_tokens)
+        if need:
+            workspace = _empty(stream, need, torch.uint8, device)
+    wp = None if workspace is None else _on(device, workspace, "workspace", torch.uint8)
+    wb = 0 if workspace is None else workspace.numel()
+    _call("idx_attn_paged", device, stream, qp, q.stride(0), q.stride(1), rows, H, latent, cp,
+          num_pages, PAGE_SIZE, bp, stride, B, rp, kp, ep, ip, istride, k, max_tokens, scale, op,
+          out.stride(0), out.stride(1), lp, wp, wb)
+    return out, lse

@@ -553,4 +553,172 @@ int idx_topk_noalloc(const float* logits, int64_t rows, int64_t logits_row_strid
                                              stream));
 }
 
+int idx_step_map(const int32_t* seq_lens, const int32_t* query_lens, int B, int32_t* block_table,
+                 int64_t bt_row_stride, int64_t bt_pages, const int32_t* free_pages,
+                 int64_t num_free, const int64_t* free_start, int64_t* free_next, int page_size,
+                 int columns, int64_t num_rows, int64_t* slot_mapping, int64_t* positions,
+                 int32_t* row_seq, int32_t* ks, int32_t* ke, int64_t* cu_seq_offsets,
+                 hipStream_t stream) {
+  if (page_size != IDX_PAGE_SIZE || B < 0 || B > IDX_MAX_DECODE_SEQS || num_rows < 0 ||
+      num_rows > 0x7fffffffLL || num_free < 0 || bt_pages < 0 || bt_row_stride < bt_pages)
+    return IDX_ERR_ARG;
+  if (columns != IDX_COLUMNS_SEQUENCE && columns != IDX_COLUMNS_GATHERED) return IDX_ERR_ARG;
+  if (B > 0) {
+    if (!seq_lens || !aligned(seq_lens, 4) || !query_lens || !aligned(query_lens, 4))
+      return IDX_ERR_ARG;
+    if (slot_mapping && bt_pages > 0 && !block_table) return IDX_ERR_ARG;
+  }
+  // a list of no pages is still a list: its pages are all lacking
+  if (free_pages ? !free_start || !aligned(free_start, 8) : num_free > 0) return IDX_ERR_ARG;
+  if (free_next && (!aligned(free_next, 8) || free_next == free_start)) return IDX_ERR_ARG;
+  if (!aligned(block_table, 4) || !aligned(free_pages, 4) || !aligned(slot_mapping, 8) ||
+      !aligned(positions, 8) || !aligned(row_seq, 4) || !aligned(ks, 4) || !aligned(ke, 4) ||
+      !aligned(cu_seq_offsets, 8))
+    return IDX_ERR_ARG;
+  if (num_rows == 0 && !free_next && !cu_seq_offsets) return IDX_OK;
+  int st = gate_current();
+  if (st != IDX_OK) return st;
+  const mxidx::StepMapArgs a{seq_lens,   query_lens, B,         columns == IDX_COLUMNS_GATHERED,
+                             block_table, bt_row_stride, bt_pages, free_pages, num_free, free_start,
+                             free_next,  num_rows,   slot_mapping, positions, row_seq, ks, ke,
+                             cu_seq_offsets};
+  return launched(mxidx::launch_step_map(a, stream));
+}
+
+// `count` rows of `width` values: a stride that steps over whole, aligned rows.
+static bool stride_ok(int64_t stride, int64_t count, int width, int align) {
+  return count <= 1 || (stride >= width && stride % align == 0);
+}
+
+static int check_heads(const idx_heads* s, int dtype, int64_t T) {
+  if (s->heads < 0 || s->norm < IDX_NORM_NONE || s->norm > IDX_NORM_LAYER) return IDX_ERR_ARG;
+  if (s->heads == 0 || T == 0) return IDX_OK;
+  const int al = dtype == IDX_BF16 ? 8 : 4;
+  if (!s->x || !aligned(s->x, 16) || !s->out || !aligned(s->out, 16)) return IDX_ERR_ARG;
+  if (!stride_ok(s->row_stride, T, IDX_HEAD_DIM, al) ||
+      !stride_ok(s->head_stride, s->heads, IDX_HEAD_DIM, al) ||
+      !stride_ok(s->out_row_stride, T, IDX_HEAD_DIM, al) ||
+      !stride_ok(s->out_head_stride, s->heads, IDX_HEAD_DIM, al))
+    return IDX_ERR_ARG;
+  if (s->norm != IDX_NORM_NONE &&
+      (!aligned(s->weight, 16) || !aligned(s->bias, 16) || !(s->eps >= 0.f)))
+    return IDX_ERR_ARG;
+  return IDX_OK;
+}
+
+static mxidx::HeadsSpec heads_spec(const idx_heads* s) {
+  if (!s) return mxidx::HeadsSpec{};
+  const bool on = s->norm != IDX_NORM_NONE;
+  return mxidx::HeadsSpec{s->x,     s->out,  s->row_stride, s->head_stride, s->out_row_stride,
+                          s->out_head_stride, s->heads, s->norm, on ? s->weight : nullptr,
+                          on ? s->bias : nullptr, s->eps};
+}
+
+int idx_norm_rope(const idx_heads* q, const idx_heads* k, int dtype, int64_t T,
+                  const idx_rope* rope, hipStream_t stream) {
+  int st = check_rope(rope);
+  if (st != IDX_OK) return st;
+  if (dtype != IDX_BF16 && dtype != IDX_F32) return IDX_ERR_ARG;
+  if (T < 0 || T > ((int64_t)1 << 40)) return IDX_ERR_ARG;
+  if (q && (st = check_heads(q, dtype, T)) != IDX_OK) return st;
+  if (k && (st = check_heads(k, dtype, T)) != IDX_OK) return st;
+  const int64_t heads = (int64_t)(q ? q->heads : 0) + (k ? k->heads : 0);
+  if (heads > (1 << 20)) return IDX_ERR_ARG;
+  if (T == 0 || heads == 0) return IDX_OK;
+  if (rope->rope_dim > 0 && !rope->positions && rope->table_rows < T) return IDX_ERR_ARG;
+  if ((st = gate_current()) != IDX_OK) return st;
+  return launched(mxidx::launch_norm_rope(heads_spec(q), heads_spec(k), dtype == IDX_F32, T,
+                                          rope_spec(rope), stream));
+}
+
+static bool latent_ok(int latent) { return latent == 128 || latent == 256 || latent == 512; }
+
+int idx_latent_insert(const void* kv, int dtype, int64_t T, int64_t kv_row_stride, int latent,
+                      int norm, const float* weight, float eps, const idx_rope* rope,
+                      const int64_t* slot_mapping, void* cache, int64_t num_pages, int page_size,
+                      const void* q_pe, int H, int64_t q_row_stride, int64_t q_head_stride,
+                      void* q_out, int64_t out_row_stride, int64_t out_head_stride,
+                      hipStream_t stream) {
+  int st = check_rope(rope);
+  if (st != IDX_OK) return st;
+  if (rope->rope_dim != IDX_LATENT_ROPE) return IDX_ERR_ARG;
+  if (dtype != IDX_BF16 && dtype != IDX_F32) return IDX_ERR_ARG;
+  if (!latent_ok(latent) || page_size != IDX_PAGE_SIZE || num_pages < 0 ||
+      num_pages > ((int64_t)1 << 40) || T < 0 || H < 0)
+    return IDX_ERR_ARG;
+  // the grid is one workgroup for 4 tokens and one for 32 query rows
+  if (T > (1 << 28) || (q_pe && T * H > ((int64_t)1 << 30))) return IDX_ERR_ARG;
+  if (norm != IDX_NORM_NONE && norm != IDX_NORM_RMS) return IDX_ERR_ARG;
+  if (T == 0) return IDX_OK;
+  const int al = dtype == IDX_BF16 ? 8 : 4;
+  if (!kv || !aligned(kv, 16) || !stride_ok(kv_row_stride, T, latent + IDX_LATENT_ROPE, al))
+    return IDX_ERR_ARG;
+  if (norm == IDX_NORM_RMS && (!aligned(weight, 16) || !(eps >= 0.f))) return IDX_ERR_ARG;
+  if (!slot_mapping || !aligned(slot_mapping, 8)) return IDX_ERR_ARG;
+  if (num_pages > 0 && (!cache || !aligned(cache, 16))) return IDX_ERR_ARG;
+  if (!rope->positions && rope->table_rows < T) return IDX_ERR_ARG;
+  const bool has_q = q_pe && H > 0;
+  if (has_q && (!aligned(q_pe, 16) || !q_out || !aligned(q_out, 16) ||
+                !stride_ok(q_row_stride, T, IDX_LATENT_ROPE, al) ||
+                !stride_ok(q_head_stride, H, IDX_LATENT_ROPE, al) ||
+                !stride_ok(out_row_stride, T, IDX_LATENT_ROPE, 8) ||
+                !stride_ok(out_head_stride, H, IDX_LATENT_ROPE, 8)))
+    return IDX_ERR_ARG;
+  if ((st = gate_current()) != IDX_OK) return st;
+  const mxidx::LatentSpec a{kv, T, kv_row_stride, norm, norm == IDX_NORM_RMS ? weight : nullptr,
+                            eps, slot_mapping, cache, num_pages * IDX_PAGE_SIZE,
+                            has_q ? q_pe : nullptr, H, q_row_stride, q_head_stride, q_out,
+                            out_row_stride, out_head_stride};
+  return launched(mxidx::launch_latent_insert(a, dtype == IDX_F32, latent, rope_spec(rope), stream));
+}
+
+// What the two calls below share: sizes that the kernels' grid and indexes take.
+static bool attn_sizes_ok(int64_t rows, int H, int latent, int64_t max_tokens) {
+  return rows >= 0 && H >= 1 && H <= IDX_MAX_HEADS && rows <= 0x7fffffffLL / IDX_MAX_HEADS &&
+         latent_ok(latent) && max_tokens >= 0 && max_tokens <= 0x7fffffffLL - IDX_PAGE_SIZE;
+}
+
+size_t idx_attn_workspace_bytes(int64_t rows, int H, int latent, int64_t entries) {
+  if (!attn_sizes_ok(rows, H, latent, entries)) return 0;
+  return (size_t)mxidx::attn_workspace_bytes(rows, H, latent, entries);
+}
+
+int idx_attn_paged(const void* q, int64_t q_row_stride, int64_t q_head_stride, int64_t rows, int H,
+                   int latent, const void* cache, int64_t num_pages, int page_size,
+                   const int32_t* block_table, int64_t bt_row_stride, int B,
+                   const int32_t* row_seq, const int32_t* ks, const int32_t* ke,
+                   const int32_t* indices, int64_t idx_row_stride, int k, int64_t max_tokens,
+                   float scale, void* out, int64_t out_row_stride, int64_t out_head_stride,
+                   float* lse, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  if (!attn_sizes_ok(rows, H, latent, max_tokens) || page_size != IDX_PAGE_SIZE || num_pages < 0 ||
+      num_pages > ((int64_t)1 << 40) || B < 0)
+    return IDX_ERR_ARG;
+  if (rows == 0 || B == 0) return IDX_OK;     // no row belongs to a sequence
+  const int64_t pages_per_seq = (max_tokens + IDX_PAGE_SIZE - 1) / IDX_PAGE_SIZE;
+  if (bt_row_stride < pages_per_seq) return IDX_ERR_ARG;
+  if (!row_seq && rows % B != 0) return IDX_ERR_ARG;
+  if (!q || !aligned(q, 16) || !stride_ok(q_row_stride, rows, latent + IDX_LATENT_ROPE, 8) ||
+      !stride_ok(q_head_stride, H, latent + IDX_LATENT_ROPE, 8))
+    return IDX_ERR_ARG;
+  if (!out || !aligned(out, 8) || !stride_ok(out_row_stride, rows, latent, 4) ||
+      !stride_ok(out_head_stride, H, latent, 4))
+    return IDX_ERR_ARG;
+  if (!ke || !aligned(ke, 4) || !aligned(ks, 4) || !aligned(row_seq, 4) || !aligned(lse, 4))
+    return IDX_ERR_ARG;
+  if (indices && (k < 0 || !aligned(indices, 4) || !stride_ok(idx_row_stride, rows, k, 1)))
+    return IDX_ERR_ARG;
+  if (max_tokens > 0 && (!block_table || !aligned(block_table, 4))) return IDX_ERR_ARG;
+  if (num_pages > 0 && (!cache || !aligned(cache, 16))) return IDX_ERR_ARG;
+  const size_t need = idx_attn_workspace_bytes(rows, H, latent, indices ? k : max_tokens);
+  if (need > 0 && (!workspace || !aligned(workspace, 256) || workspace_bytes < need))
+    return IDX_ERR_ARG;
+  int st = gate_current();
+  if (st != IDX_OK) return st;
+  const mxidx::AttnArgs a{q, q_row_stride, q_head_stride, rows, H, cache, num_pages, block_table,
+                          bt_row_stride, B, row_seq, row_seq ? 1 : rows / B, ks, ke, indices,
+                          idx_row_stride, k, max_tokens, scale, out, out_row_stride,
+                          out_head_stride, lse};
+  return launched(mxidx::launch_attn_paged(a, latent, workspace, stream));
+}
+
 }  // extern "C"

@@ -139,4 +139,89 @@ constexpr int64_t kNoAllocScratchBytes = 36ll << 20;
 hipError_t launch_topk_noalloc(const float* logits, int64_t rows, int64_t ld, const int32_t* ks,
                                const int32_t* ke, int k, int32_t* out_idx, hipStream_t stream);
 
+// A step's bookkeeping from its request lengths (step_map.hip); pointers as in
+// idx_step_map, outputs may be null.
+struct StepMapArgs {
+  const int32_t* seq_lens;
+  const int32_t* query_lens;
+  int B;
+  bool gathered;
+  int32_t* block_table;
+  int64_t bt_row_stride, bt_pages;
+  const int32_t* free_pages;
+  int64_t num_free;
+  const int64_t* free_start;
+  int64_t* free_next;
+  int64_t num_rows;
+  int64_t* slot_mapping;
+  int64_t* positions;
+  int32_t* row_seq;
+  int32_t* ks;
+  int32_t* ke;
+  int64_t* cu_seq_offsets;
+};
+hipError_t launch_step_map(const StepMapArgs& a, hipStream_t stream);
+
+// Per-head norm and rotation (norm_rope.hip).
+enum { kNormNone = 0, kNormRms = 1, kNormLayer = 2 };
+struct HeadsSpec {
+  const void* x;
+  void* out;
+  int64_t row_stride, head_stride, out_row_stride, out_head_stride;
+  int heads, norm;
+  const float* weight;
+  const float* bias;
+  float eps;
+};
+hipError_t launch_norm_rope(const HeadsSpec& q, const HeadsSpec& k, bool f32, int64_t T,
+                            const RopeSpec& rope, hipStream_t stream);
+
+// Latent rows normed, rotated and written to the paged latent cache (bf16 rows of
+// latent + 64 values); q_pe null: no query rows.
+struct LatentSpec {
+  const void* kv;
+  int64_t T, kv_row_stride;
+  int norm;
+  const float* weight;
+  float eps;
+  const int64_t* slot_mapping;
+  void* cache;
+  int64_t num_slots;
+  const void* q_pe;
+  int H;
+  int64_t q_row_stride, q_head_stride;
+  void* q_out;
+  int64_t out_row_stride, out_head_stride;
+};
+hipError_t launch_latent_insert(const LatentSpec& a, bool f32, int latent, const RopeSpec& rope,
+                                hipStream_t stream);
+
+// Attention over the paged latent cache (attn_paged.hip); pointers as in
+// idx_attn_paged.  row_seq null: row r belongs to sequence r / rows_per_seq.
+struct AttnArgs {
+  const void* q;
+  int64_t q_row_stride, q_head_stride, rows;
+  int H;
+  const void* cache;
+  int64_t num_pages;
+  const int32_t* block_table;
+  int64_t bt_row_stride;
+  int B;
+  const int32_t* row_seq;
+  int64_t rows_per_seq;
+  const int32_t* ks;
+  const int32_t* ke;
+  const int32_t* indices;
+  int64_t idx_row_stride;
+  int k;
+  int64_t max_tokens;
+  float scale;
+  void* out;
+  int64_t out_row_stride, out_head_stride;
+  float* lse;
+};
+// Workspace bytes for rows whose windows (or lists) hold up to `entries` tokens.
+int64_t attn_workspace_bytes(int64_t rows, int H, int latent, int64_t entries);
+hipError_t launch_attn_paged(const AttnArgs& a, int latent, void* workspace, hipStream_t stream);
+
 }  // namespace mxidx
