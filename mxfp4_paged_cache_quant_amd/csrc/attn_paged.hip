@@ -4,9 +4,37 @@
 //   out[r,h,:] = sum_j exp(s_j - m) * row_j[:n] / l,  l = sum_j exp(s_j - m),
 //   lse[r,h] = m + log l,  m = max_j s_j.
 //
-// One pass over the tokens with the running maximum and sum: a new maximum scales what
-// was summed so far by exp(m_old - m_new).  One workgroup per (row, head); its four waves
-// take every fourth token each, 64 lanes sharing a row's values, and join at the end.
+// One pass over the tokens with the running maximum and sum (in powers of two): a
+// new maximum scales what was summed so far by 2^(m_old - m_new).
+//
+// Work mapping: one workgroup takes HG * 16 heads of one query row over one share of
+// the row's tokens, 64 tokens (a tile) at a time.  A wave holds 16 heads: their query
+// in registers and their output sums, HG waves the heads and TH waves the tile's
+// token parts.  All products run on the 16x16x32 bf16 MFMA in the transposed form:
+//   S^T = K Q^T   A = 16 tokens of the tile, B = the wave's 16 heads
+//   O^T = V^T P^T A = 16 of the n values over 32 tokens, B = the weights
+// so a lane holds one head throughout: the weights leave the first product in the
+// registers where the second takes them (lane group g: tokens 4g..4g+3 of two 16-token
+// parts), and the running maximum and sum are one register each.
+//
+// A row serves as key and, in its first n values, as value, so each cached row is
+// read once into LDS (two tiles, the next one's loads in flight behind the current
+// one's products).  The copies go straight from the cache rows to LDS in 16-byte
+// chunks; chunk c of token t lands at place c ^ swz(t) of the row, which spreads both
+// the keys' reads (16 tokens, one chunk) and the values' transposing reads (16 tokens,
+// two neighbouring chunks) over all banks.
+//
+// Places of a tile that hold no visible token read a visible token's row instead and
+// get weight 0, so nothing that a masked place holds reaches a sum; a tile with no
+// visible token is skipped.
+//
+// The weights are rounded to bf16 for the second product (relative error 2^-8 at most,
+// as the cached values' own); l and lse take them unrounded.
+//
+// Few rows: the tokens are split over workgroups, each leaving its unscaled sums with
+// m and l in the workspace, and a second launch joins them.
+#include <type_traits>
+
 #include "common.hpp"
 #include "launch.hpp"
 
@@ -14,105 +42,424 @@ namespace mxidx {
 namespace {
 
 constexpr int kRopeWidth = 64;
-constexpr int kWaves = 4;
+constexpr int kTile = 64;                  // tokens per tile: a lane each
+constexpr int kCus = 256;
 
-__device__ __forceinline__ float bf16_to_f32(uint16_t u) { return __uint_as_float((uint32_t)u << 16); }
+typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
+typedef __bf16 v4bf __attribute__((ext_vector_type(4)));
+typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
+typedef short v4s __attribute__((ext_vector_type(4)));
+typedef short v8s __attribute__((ext_vector_type(8)));
+#define MXIDX_LDS __attribute__((address_space(3)))
+#define MXIDX_GLOBAL __attribute__((address_space(1)))
 
-__device__ __forceinline__ uint16_t f32_to_bf16(float x) {
-  return __builtin_bit_cast(uint16_t, (__bf16)x);
+__device__ __forceinline__ v4f mfma_bf16(v8s a, v8s b, v4f c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, a),
+                                                 __builtin_bit_cast(v8bf, b), c, 0, 0, 0);
 }
 
-// The cache row of entry j of query row r, or -1 where there is none.
-__device__ __forceinline__ int64_t token_row(const AttnArgs& a, int64_t r, int64_t j, int seq,
-                                             int64_t ks, int64_t window) {
-  int64_t p = j;
-  if (a.indices) p = (int64_t)a.indices[r * a.idx_row_stride + j] - ks;
-  if (p < 0 || p >= window) return -1;
-  const int page = a.block_table[seq * a.bt_row_stride + p / kPage];
-  if (page < 0 || page >= a.num_pages) return -1;
-  return (int64_t)page * kPage + p % kPage;
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  const v2bf r = {(__bf16)a, (__bf16)b};
+  return __builtin_bit_cast(uint32_t, r);
 }
+
+// LDS place of a 16-byte chunk: chunk c of token t's row is stored at c ^ swz(t).
+// Latent rows are multiples of 256 bytes, so their banks repeat every 16 chunks and
+// swz runs over 16 values, tokens 0..7 on even ones (a transposing read takes chunk
+// pairs of 8 tokens at a time); the 128-byte positional rows alternate between two
+// halves of the banks, and 8 values over token pairs do.
+template <int kChunks>
+__device__ __forceinline__ int swz(int t) {
+  if constexpr (kChunks >= 16) return ((t & 7) << 1) | ((t >> 3) & 1);
+  return (t >> 1) & 7;
+}
+
+struct Row {                               // a query row's window
+  int seq;
+  int64_t ks, window;
+};
+
+// False when the row belongs to no sequence.
+__device__ __forceinline__ bool row_of(const AttnArgs& a, int64_t r, Row& o) {
+  o.seq = a.row_seq ? a.row_seq[r] : (int)(r / a.rows_per_seq);
+  if (o.seq < 0 || o.seq >= a.B) return false;
+  o.ks = a.ks ? a.ks[r] : 0;
+  o.window = min(max((int64_t)a.ke[r] - o.ks, (int64_t)0), a.max_tokens);
+  return true;
+}
+
+// A lane's token of a tile, in the three steps that the pipeline takes apart: the
+// list entry, its page, its cache row.
+struct Token {
+  int64_t p;                               // token of the sequence, -1: none
+  int page;
+};
+
+__device__ __forceinline__ int64_t token_entry(const AttnArgs& a, int64_t r, const Row& row,
+                                               int64_t e) {
+  if (!a.indices) return e < row.window ? e : -1;
+  if (e >= a.k) return -1;
+  const int64_t p = (int64_t)a.indices[r * a.idx_row_stride + e] - row.ks;
+  return p >= 0 && p < row.window ? p : -1;
+}
+
+__device__ __forceinline__ int token_page(const AttnArgs& a, const Row& row, int64_t p) {
+  return p < 0 ? -1 : a.block_table[row.seq * a.bt_row_stride + p / kPage];
+}
+
+// Partial sums of the split form: for each (row, split) HP x n output sums, then
+// (m, l) of each head; HP = heads rounded up to the workgroups' heads.
+struct Parts {
+  float* o;
+  float* ml;
+  int splits, heads;
+};
+
+template <int kLatent, int HG, int TH>
+__global__ __launch_bounds__(HG * TH * kWave) void attn_kernel(AttnArgs a, Parts parts) {
+  constexpr int kRow = kLatent + kRopeWidth;
+  constexpr int kWaves = HG * TH;
+  constexpr int kTokens = kTile / TH;                  // of a tile, per wave
+  constexpr int NT = kTokens / 16;                     // 16-token parts of those
+  constexpr int KS = kRow / 32, KL = kLatent / 32;     // contraction steps, latent ones
+  constexpr int NV = kLatent / 16;                     // 16-value parts of the output
+  constexpr int LC = kLatent / 8;                      // 16-byte chunks of a latent row
+  constexpr int kLatentBytes = kTile * kLatent * 2, kTileBytes = kTile * kRow * 2;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kTileBytes];
+  static_assert(2 * kTileBytes <= 160 * 1024, "two tiles fit the LDS");
+  static_assert((TH - 1) * HG * 16 * kLatent * 4 <= 2 * kTileBytes, "the waves' join fits them");
+  __shared__ float join_ml[TH > 1 ? TH * HG * 16 * 2 : 1];
+
+  const int lane = threadIdx.x & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int hg = wave % HG, th = wave / HG;
+  const int g = lane >> 4, n = lane & 15;
+  const int groups = parts.heads / (HG * 16);
+  const int group = blockIdx.x % groups;
+  const int split = (blockIdx.x / groups) % parts.splits;
+  const int64_t r = blockIdx.x / groups / parts.splits;
+  Row row;
+  if (!row_of(a, r, row)) return;
+  const int64_t entries = a.indices ? a.k : row.window;
+  const int64_t tiles = (entries + kTile - 1) / kTile;
+  const int64_t t0 = tiles * split / parts.splits, t1 = tiles * (split + 1) / parts.splits;
+  const int head = group * HG * 16 + hg * 16 + n;      // this lane's head
+
+  // the wave's query: step s holds values 32s + 8g .. +7 of this lane's head
+  v8s q[KS];
+  {
+    const uint16_t* p = static_cast<const uint16_t*>(a.q) + r * a.q_row_stride +
+                        (int64_t)min(head, a.H - 1) * a.q_head_stride + 8 * g;
+#pragma unroll
+    for (int s = 0; s < KS; ++s) q[s] = *reinterpret_cast<const v8s*>(p + 32 * s);
+  }
+  v4f o[NV];
+#pragma unroll
+  for (int v = 0; v < NV; ++v) o[v] = v4f{0.f, 0.f, 0.f, 0.f};
+  float m = neg_inf(), l = 0.f;                        // l: this lane's tokens only
+  const float scale2 = a.scale * 1.4426950408889634f;  // scores in powers of two
+
+  // Copies the tile's rows: lane i holds the cache row of token i, this wave copies
+  // tokens kTile/kWaves at a time, 64 chunks an instruction.
+  auto stage = [&](uint8_t* buf, int64_t cache_row) {
+    constexpr int kMine = kTile / kWaves;
+    const int first = wave * kMine;
+    const char* base = static_cast<const char*>(a.cache);
+    const uint64_t bytes = (uint64_t)cache_row * (kRow * 2);
+    const uint32_t lo = (uint32_t)bytes, hi = (uint32_t)(bytes >> 32);
+    auto copy = [&](auto chunks_c, uint8_t* dst, int offset) {
+      constexpr int C = chunks_c;                      // chunks of a row
+      constexpr int kPer = C >= kWave ? 1 : kWave / C; // rows of an instruction
+      static_assert(C <= kWave && kMine % kPer == 0, "whole instructions");
+      const int sub = lane / C, place = lane % C;
+#pragma unroll
+      for (int i = 0; i < kMine; i += kPer) {
+        const int t = first + i + sub;
+        const uint32_t l32 = (uint32_t)__shfl((int)lo, t), h32 = (uint32_t)__shfl((int)hi, t);
+        const char* src = base + (((uint64_t)h32 << 32) | l32) + offset + ((place ^ swz<C>(t)) << 4);
+        __builtin_amdgcn_global_load_lds((const MXIDX_GLOBAL void*)src,
+                                         (MXIDX_LDS void*)(dst + (first + i) * C * 16), 16, 0, 0);
+      }
+    };
+    copy(std::integral_constant<int, LC>{}, buf, 0);
+    copy(std::integral_constant<int, 8>{}, buf + kLatentBytes, kLatent * 2);
+  };
+  // The lanes' cache rows of a tile; places of no token take the first visible one's.
+  auto rows_of = [&](const Token& t, uint64_t& mask) -> int64_t {
+    const bool ok = t.p >= 0 && t.page >= 0 && t.page < a.num_pages;
+    mask = __ballot(ok);
+    const int64_t mine = (int64_t)t.page * kPage + t.p % kPage;
+    const int from = ok || mask == 0 ? lane : __builtin_ctzll(mask);
+    const uint32_t lo = (uint32_t)__shfl((int)(uint32_t)mine, from);
+    const uint32_t hi = (uint32_t)__shfl((int)(uint32_t)((uint64_t)mine >> 32), from);
+    return (int64_t)(((uint64_t)hi << 32) | lo);
+  };
+
+  auto compute = [&](const uint8_t* buf, uint64_t mask) {
+    const uint8_t* pos = buf + kLatentBytes;
+    const int base = th * kTokens;
+    v4f s[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) s[t] = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < KS; ++k) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const int tok = base + 16 * t + n;
+        const uint8_t* p = k < KL ? buf + tok * (kLatent * 2) + (((4 * k + g) ^ swz<LC>(tok)) << 4)
+                                  : pos + tok * (kRopeWidth * 2) + (((4 * (k - KL) + g) ^ swz<8>(tok)) << 4);
+        s[t] = mfma_bf16(*reinterpret_cast<const v8s*>(p), q[k], s[t]);
+      }
+    }
+    // s[t][i]: token base + 16t + 4g + i of this lane's head
+    float top = neg_inf();
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[t][i] *= scale2;
+    if (mask != ~0ull) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const uint32_t bits = (uint32_t)(mask >> (base + 16 * t + 4 * g));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[t][i] = (bits >> i) & 1 ? s[t][i] : neg_inf();
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) top = fmaxf(top, s[t][i]);
+    top = fmaxf(top, __shfl_xor(top, 16));
+    top = fmaxf(top, __shfl_xor(top, 32));
+    const float m2 = fmaxf(m, top);
+    if (__any(m2 > m)) {
+      const float f = m2 > m ? __builtin_amdgcn_exp2f(m - m2) : 1.f;
+      l *= f;
+#pragma unroll
+      for (int v = 0; v < NV; ++v) o[v] *= f;
+      m = m2;
+    }
+    const float ref = m == neg_inf() ? 0.f : m;        // no token yet: every weight 0
+    uint32_t w[NT][2];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      float p[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        p[i] = __builtin_amdgcn_exp2f(s[t][i] - ref);
+        l += p[i];
+      }
+      w[t][0] = pack2(p[0], p[1]);
+      w[t][1] = pack2(p[2], p[3]);
+    }
+    // values: lane 4j + c of a 16-lane group reads tokens 4g + j, values 4c..4c+3, and
+    // gets tokens 4g..4g+3 of value n
+    auto values = [&](int t, int v) -> v4s {
+      const int tok = base + 16 * t + 4 * g + (n >> 2);
+      const int chunk = (2 * v + ((n >> 1) & 1)) ^ swz<LC>(tok);
+      return __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+          (MXIDX_LDS v4s*)(buf + tok * (kLatent * 2) + (chunk << 4) + 8 * (n & 1)));
+    };
+    if constexpr (NT == 1) {
+      const v4s b = __builtin_bit_cast(v4s, uint2{w[0][0], w[0][1]});
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+        o[v] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(values(0, v), b, o[v], 0, 0, 0);
+    } else {
+#pragma unroll
+      for (int t = 0; t < NT; t += 2) {
+        const v8s b = __builtin_bit_cast(v8s, uint4{w[t][0], w[t][1], w[t + 1][0], w[t + 1][1]});
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+          const v4s x = values(t, v), y = values(t + 1, v);
+          o[v] = mfma_bf16(__builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7), b, o[v]);
+        }
+      }
+    }
+  };
+
+  // the pipeline: the tile computed, the next one's rows on their way to LDS, the one
+  // behind it looking up its pages and the one behind that its list entries
+  if (t0 < t1) {
+    auto entry = [&](int64_t t) { return t < t1 ? token_entry(a, r, row, t * kTile + lane) : -1; };
+    Token now, next;
+    now.p = entry(t0);
+    next.p = entry(t0 + 1);
+    now.page = token_page(a, row, now.p);
+    uint64_t mask;
+    int64_t rows = rows_of(now, mask);
+    if (mask) stage(lds, rows);
+    next.page = token_page(a, row, next.p);
+    int64_t far = entry(t0 + 2);
+    for (int64_t t = t0; t < t1; ++t) {
+      uint8_t* cur = lds + ((t - t0) & 1) * kTileBytes;
+      uint8_t* nxt = lds + ((t - t0 + 1) & 1) * kTileBytes;
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      __syncthreads();
+      uint64_t next_mask = 0;
+      if (t + 1 < t1) {
+        rows = rows_of(next, next_mask);
+        if (next_mask) stage(nxt, rows);
+        next.p = far;
+        next.page = token_page(a, row, far);
+        far = entry(t + 3);
+      }
+      if (mask) compute(cur, mask);
+      mask = next_mask;
+    }
+  }
+
+  l += __shfl_xor(l, 16);
+  l += __shfl_xor(l, 32);
+  if constexpr (TH > 1) {
+    // the token parts' sums joined in LDS: part th > 0 leaves its own, part 0 takes them
+    float* lo = reinterpret_cast<float*>(lds);
+    if (g == 0) {
+      join_ml[(th * HG + hg) * 32 + 2 * n] = m;
+      join_ml[(th * HG + hg) * 32 + 2 * n + 1] = l;
+    }
+    __syncthreads();                                   // the last tile's reads are done
+    if (th > 0) {
+      float* dst = lo + ((th - 1) * HG + hg) * 16 * kLatent + 4 * lane;
+#pragma unroll
+      for (int v = 0; v < NV; ++v) *reinterpret_cast<v4f*>(dst + v * 256) = o[v];
+    }
+    __syncthreads();
+    if (th > 0) return;
+    float top = m;
+#pragma unroll
+    for (int t = 1; t < TH; ++t) top = fmaxf(top, join_ml[(t * HG + hg) * 32 + 2 * n]);
+    const float ref = top == neg_inf() ? 0.f : top;
+    float f = __builtin_amdgcn_exp2f(m - ref);
+    l *= f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) o[v] *= f;
+#pragma unroll
+    for (int t = 1; t < TH; ++t) {
+      f = __builtin_amdgcn_exp2f(join_ml[(t * HG + hg) * 32 + 2 * n] - ref);
+      l += f * join_ml[(t * HG + hg) * 32 + 2 * n + 1];
+      const float* src = lo + ((t - 1) * HG + hg) * 16 * kLatent + 4 * lane;
+#pragma unroll
+      for (int v = 0; v < NV; ++v) o[v] += f * *reinterpret_cast<const v4f*>(src + v * 256);
+    }
+    m = top;
+  }
+
+  // o[v][i]: value 16v + 4g + i of this lane's head
+  if (parts.splits > 1) {
+    const int64_t at = (r * parts.splits + split) * parts.heads + head;
+    if (g == 0) *reinterpret_cast<float2*>(parts.ml + 2 * at) = make_float2(m, l);
+    if (__all(l == 0.f)) return;
+    float* dst = parts.o + at * kLatent + 4 * g;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) *reinterpret_cast<v4f*>(dst + 16 * v) = o[v];
+    return;
+  }
+  if (head >= a.H) return;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  uint16_t* out = static_cast<uint16_t*>(a.out) + r * a.out_row_stride +
+                  (int64_t)head * a.out_head_stride + 4 * g;
+#pragma unroll
+  for (int v = 0; v < NV; ++v)
+    *reinterpret_cast<uint2*>(out + 16 * v) =
+        l == 0.f ? make_uint2(0, 0)
+                 : make_uint2(pack2(o[v][0] * inv, o[v][1] * inv), pack2(o[v][2] * inv, o[v][3] * inv));
+  if (a.lse && g == 0)
+    a.lse[r * a.H + head] = l == 0.f ? neg_inf() : m * 0.6931471805599453f + logf(l);
+}
+
+// The splits' sums of one (row, head), kLatent / 4 lanes: 4 values each.
+template <int kLatent>
+__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, Parts parts) {
+  constexpr int W = kLatent / 4;
+  const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) / W;
+  const int i = threadIdx.x % W;
+  const int64_t r = at / a.H;
+  const int head = (int)(at % a.H);
+  Row row;
+  if (r >= a.rows || !row_of(a, r, row)) return;
+  const int64_t first = r * parts.splits * parts.heads + head;
+  float top = neg_inf();
+  for (int s = 0; s < parts.splits; ++s)
+    top = fmaxf(top, parts.ml[2 * (first + (int64_t)s * parts.heads)]);
+  v4f o = {0.f, 0.f, 0.f, 0.f};
+  float l = 0.f;
+  for (int s = 0; s < parts.splits; ++s) {
+    const int64_t p = first + (int64_t)s * parts.heads;
+    const float2 ml = *reinterpret_cast<const float2*>(parts.ml + 2 * p);
+    if (ml.y == 0.f) continue;                         // nothing seen: no sums written
+    const float f = __builtin_amdgcn_exp2f(ml.x - top);
+    l += f * ml.y;
+    o += f * *reinterpret_cast<const v4f*>(parts.o + p * kLatent + 4 * i);
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + r * a.out_row_stride +
+                            (int64_t)head * a.out_head_stride + 4 * i) =
+      make_uint2(pack2(o[0] * inv, o[1] * inv), pack2(o[2] * inv, o[3] * inv));
+  if (a.lse && i == 0)
+    a.lse[r * a.H + head] = l == 0.f ? neg_inf() : top * 0.6931471805599453f + logf(l);
+}
+
+struct Plan {
+  int group_heads;        // heads of a workgroup
+  int heads;              // H rounded up to whole groups
+  int splits;
+};
+
+Plan plan_of(int64_t rows, int H, int64_t entries) {
+  Plan p;
+  p.group_heads = H <= 16 ? 16 : H <= 32 ? 32 : H <= 64 ? 64 : 128;
+  p.heads = (H + p.group_heads - 1) / p.group_heads * p.group_heads;
+  const int64_t units = rows * (p.heads / p.group_heads);
+  const int64_t tiles = (entries + kTile - 1) / kTile;
+  int64_t s = units > 0 ? kCus / units : 1;
+  s = s < tiles ? s : tiles;
+  p.splits = (int)(s > 1 ? s : 1);
+  return p;
+}
+
+int64_t align256(int64_t x) { return (x + 255) / 256 * 256; }
+
+int64_t ml_bytes(int64_t rows, const Plan& p) { return align256(rows * p.splits * p.heads * 8); }
 
 template <int kLatent>
-__global__ __launch_bounds__(kWaves * kWave) void attn_simple_kernel(AttnArgs a) {
-  constexpr int kRow = kLatent + kRopeWidth;
-  constexpr int kPer = kRow / kWave, kOut = kLatent / kWave;
-  __shared__ float part[kWaves][kLatent];
-  __shared__ float part_m[kWaves], part_l[kWaves];
-  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
-  const int64_t r = blockIdx.x / a.H;
-  const int h = (int)(blockIdx.x % a.H);
-  const int seq = a.row_seq ? a.row_seq[r] : (int)(r / a.rows_per_seq);
-  if (seq < 0 || seq >= a.B) return;
-  const int64_t ks = a.ks ? a.ks[r] : 0;
-  const int64_t window = min(max((int64_t)a.ke[r] - ks, (int64_t)0), a.max_tokens);
-  const int64_t entries = a.indices ? a.k : window;
-
-  const uint16_t* q = static_cast<const uint16_t*>(a.q) + r * a.q_row_stride + h * a.q_head_stride;
-  float qv[kPer];
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) qv[i] = bf16_to_f32(q[lane + i * kWave]);
-  float m = neg_inf(), l = 0.f, o[kOut];
-#pragma unroll
-  for (int i = 0; i < kOut; ++i) o[i] = 0.f;
-  for (int64_t j = wave; j < entries; j += kWaves) {
-    const int64_t row = token_row(a, r, j, seq, ks, window);
-    if (row < 0) continue;
-    const uint16_t* c = static_cast<const uint16_t*>(a.cache) + row * kRow;
-    float kv[kPer], s = 0.f;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) kv[i] = bf16_to_f32(c[lane + i * kWave]);
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) s += qv[i] * kv[i];
-#pragma unroll
-    for (int x = 1; x < kWave; x <<= 1) s += __shfl_xor(s, x);
-    s *= a.scale;
-    const float m2 = fmaxf(m, s);
-    const float old = m2 == m ? 1.f : expf(m - m2), p = s == m2 ? 1.f : expf(s - m2);
-    l = l * old + p;
-#pragma unroll
-    for (int i = 0; i < kOut; ++i) o[i] = o[i] * old + p * kv[i];
-    m = m2;
+hipError_t launch(const AttnArgs& a, void* workspace, hipStream_t stream) {
+  const Plan p = plan_of(a.rows, a.H, a.indices ? a.k : a.max_tokens);
+  Parts parts{nullptr, nullptr, p.splits, p.heads};
+  if (p.splits > 1) {
+    parts.ml = static_cast<float*>(workspace);
+    parts.o = reinterpret_cast<float*>(static_cast<char*>(workspace) + ml_bytes(a.rows, p));
   }
-#pragma unroll
-  for (int i = 0; i < kOut; ++i) part[wave][lane + i * kWave] = o[i];
-  if (lane == 0) {
-    part_m[wave] = m;
-    part_l[wave] = l;
+  const dim3 grid((uint32_t)(a.rows * (p.heads / p.group_heads) * p.splits));
+  switch (p.group_heads) {
+    case 16: hipLaunchKernelGGL((attn_kernel<kLatent, 1, 4>), grid, dim3(256), 0, stream, a, parts); break;
+    case 32: hipLaunchKernelGGL((attn_kernel<kLatent, 2, 2>), grid, dim3(256), 0, stream, a, parts); break;
+    case 64: hipLaunchKernelGGL((attn_kernel<kLatent, 4, 2>), grid, dim3(512), 0, stream, a, parts); break;
+    default: hipLaunchKernelGGL((attn_kernel<kLatent, 8, 1>), grid, dim3(512), 0, stream, a, parts); break;
   }
-  __syncthreads();
-  if (wave != 0) return;
-  float mm = neg_inf(), ll = 0.f, f[kWaves];
-#pragma unroll
-  for (int w = 0; w < kWaves; ++w) mm = fmaxf(mm, part_m[w]);
-#pragma unroll
-  for (int w = 0; w < kWaves; ++w) {
-    f[w] = part_l[w] == 0.f ? 0.f : expf(part_m[w] - mm);
-    ll += f[w] * part_l[w];
-  }
-  uint16_t* out = static_cast<uint16_t*>(a.out) + r * a.out_row_stride + h * a.out_head_stride;
-#pragma unroll
-  for (int i = 0; i < kOut; ++i) {
-    float v = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) v += f[w] * part[w][lane + i * kWave];
-    out[lane + i * kWave] = f32_to_bf16(ll == 0.f ? 0.f : v / ll);
-  }
-  if (a.lse && lane == 0) a.lse[r * a.H + h] = ll == 0.f ? neg_inf() : mm + logf(ll);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || p.splits == 1) return e;
+  constexpr int W = kLatent / 4;
+  const int64_t threads = a.rows * a.H * W;
+  hipLaunchKernelGGL(attn_join_kernel<kLatent>, dim3((uint32_t)((threads + 255) / 256)), dim3(256), 0,
+                     stream, a, parts);
+  return hipGetLastError();
 }
 
 }  // namespace
 
-int64_t attn_workspace_bytes(int64_t, int, int, int64_t) { return 0; }
+int64_t attn_workspace_bytes(int64_t rows, int H, int latent, int64_t entries) {
+  const Plan p = plan_of(rows, H, entries);
+  if (p.splits == 1) return 0;
+  return ml_bytes(rows, p) + rows * p.splits * p.heads * latent * 4;
+}
 
-hipError_t launch_attn_paged(const AttnArgs& a, int latent, void*, hipStream_t stream) {
-  const dim3 grid((uint32_t)(a.rows * a.H)), block(kWaves * kWave);
+hipError_t launch_attn_paged(const AttnArgs& a, int latent, void* workspace, hipStream_t stream) {
   switch (latent) {
-    case 128: hipLaunchKernelGGL(attn_simple_kernel<128>, grid, block, 0, stream, a); break;
-    case 256: hipLaunchKernelGGL(attn_simple_kernel<256>, grid, block, 0, stream, a); break;
-    default: hipLaunchKernelGGL(attn_simple_kernel<512>, grid, block, 0, stream, a); break;
+    case 128: return launch<128>(a, workspace, stream);
+    case 256: return launch<256>(a, workspace, stream);
+    default: return launch<512>(a, workspace, stream);
   }
-  return hipGetLastError();
 }
 
 }  // namespace mxidx
