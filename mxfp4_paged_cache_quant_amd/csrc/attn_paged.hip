@@ -44,6 +44,7 @@ namespace {
 constexpr int kRopeWidth = 64;
 constexpr int kTile = 64;                  // tokens per tile: a lane each
 constexpr int kCus = 256;
+constexpr float kSlack = 8.f;               // weights stay below 2^8 of the reference's
 
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 typedef __bf16 v4bf __attribute__((ext_vector_type(4)));
@@ -76,7 +77,8 @@ __device__ __forceinline__ int swz(int t) {
 
 struct Row {                               // a query row's window
   int seq;
-  int64_t ks, window;
+  int64_t ks;
+  int window;
 };
 
 // False when the row belongs to no sequence.
@@ -84,26 +86,20 @@ __device__ __forceinline__ bool row_of(const AttnArgs& a, int64_t r, Row& o) {
   o.seq = a.row_seq ? a.row_seq[r] : (int)(r / a.rows_per_seq);
   if (o.seq < 0 || o.seq >= a.B) return false;
   o.ks = a.ks ? a.ks[r] : 0;
-  o.window = min(max((int64_t)a.ke[r] - o.ks, (int64_t)0), a.max_tokens);
+  o.window = (int)min(max((int64_t)a.ke[r] - o.ks, (int64_t)0), a.max_tokens);
   return true;
 }
 
-// A lane's token of a tile, in the three steps that the pipeline takes apart: the
-// list entry, its page, its cache row.
-struct Token {
-  int64_t p;                               // token of the sequence, -1: none
-  int page;
-};
-
-__device__ __forceinline__ int64_t token_entry(const AttnArgs& a, int64_t r, const Row& row,
-                                               int64_t e) {
+// A lane's token of a tile, in the steps that the pipeline takes apart: the token of
+// the sequence (-1: none), its page, and then its cache row.
+__device__ __forceinline__ int token_entry(const AttnArgs& a, int64_t r, const Row& row, int e) {
   if (!a.indices) return e < row.window ? e : -1;
   if (e >= a.k) return -1;
   const int64_t p = (int64_t)a.indices[r * a.idx_row_stride + e] - row.ks;
-  return p >= 0 && p < row.window ? p : -1;
+  return p >= 0 && p < row.window ? (int)p : -1;
 }
 
-__device__ __forceinline__ int token_page(const AttnArgs& a, const Row& row, int64_t p) {
+__device__ __forceinline__ int token_page(const AttnArgs& a, const Row& row, int p) {
   return p < 0 ? -1 : a.block_table[row.seq * a.bt_row_stride + p / kPage];
 }
 
@@ -115,12 +111,13 @@ struct Parts {
   int splits, heads;
 };
 
-template <int kLatent, int HG, int TH>
-__global__ __launch_bounds__(HG * TH * kWave) void attn_kernel(AttnArgs a, Parts parts) {
+template <int kLatent, int HG, int MT, int TH>
+__global__ __launch_bounds__(HG * TH * kWave, 1) void attn_kernel(AttnArgs a, Parts parts) {
   constexpr int kRow = kLatent + kRopeWidth;
   constexpr int kWaves = HG * TH;
+  constexpr int kHeads = HG * MT * 16;                 // of the workgroup
   constexpr int kTokens = kTile / TH;                  // of a tile, per wave
-  constexpr int NT = kTokens / 16;                     // 16-token parts of those
+  constexpr int NT = kTokens < 32 ? 1 : 2;             // 16-token parts of a step
   constexpr int KS = kRow / 32, KL = kLatent / 32;     // contraction steps, latent ones
   constexpr int NV = kLatent / 16;                     // 16-value parts of the output
   constexpr int LC = kLatent / 8;                      // 16-byte chunks of a latent row
@@ -128,35 +125,42 @@ __global__ __launch_bounds__(HG * TH * kWave) void attn_kernel(AttnArgs a, Parts
   __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kTileBytes];
   static_assert(2 * kTileBytes <= 160 * 1024, "two tiles fit the LDS");
   static_assert((TH - 1) * HG * 16 * kLatent * 4 <= 2 * kTileBytes, "the waves' join fits them");
-  __shared__ float join_ml[TH > 1 ? TH * HG * 16 * 2 : 1];
+  __shared__ float join_ml[TH > 1 ? TH * kHeads * 2 : 1];
 
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int hg = wave % HG, th = wave / HG;
   const int g = lane >> 4, n = lane & 15;
-  const int groups = parts.heads / (HG * 16);
+  const int groups = parts.heads / kHeads;
   const int group = blockIdx.x % groups;
   const int split = (blockIdx.x / groups) % parts.splits;
   const int64_t r = blockIdx.x / groups / parts.splits;
   Row row;
   if (!row_of(a, r, row)) return;
-  const int64_t entries = a.indices ? a.k : row.window;
-  const int64_t tiles = (entries + kTile - 1) / kTile;
-  const int64_t t0 = tiles * split / parts.splits, t1 = tiles * (split + 1) / parts.splits;
-  const int head = group * HG * 16 + hg * 16 + n;      // this lane's head
+  const int entries = a.indices ? a.k : row.window;
+  const int tiles = (entries + kTile - 1) / kTile;
+  const int t0 = (int)((int64_t)tiles * split / parts.splits);
+  const int t1 = (int)((int64_t)tiles * (split + 1) / parts.splits);
+  const int head0 = group * kHeads + hg * MT * 16 + n; // this lane's heads: head0 + 16u
 
-  // the wave's query: step s holds values 32s + 8g .. +7 of this lane's head
-  v8s q[KS];
-  {
+  // the wave's query: step s holds values 32s + 8g .. +7 of a head
+  v8s q[MT][KS];
+#pragma unroll
+  for (int u = 0; u < MT; ++u) {
     const uint16_t* p = static_cast<const uint16_t*>(a.q) + r * a.q_row_stride +
-                        (int64_t)min(head, a.H - 1) * a.q_head_stride + 8 * g;
+                        (int64_t)min(head0 + 16 * u, a.H - 1) * a.q_head_stride + 8 * g;
 #pragma unroll
-    for (int s = 0; s < KS; ++s) q[s] = *reinterpret_cast<const v8s*>(p + 32 * s);
+    for (int s = 0; s < KS; ++s) q[u][s] = *reinterpret_cast<const v8s*>(p + 32 * s);
   }
-  v4f o[NV];
+  v4f o[MT][NV];
+  float m[MT], l[MT];                                  // l: this lane's tokens only
 #pragma unroll
-  for (int v = 0; v < NV; ++v) o[v] = v4f{0.f, 0.f, 0.f, 0.f};
-  float m = neg_inf(), l = 0.f;                        // l: this lane's tokens only
+  for (int u = 0; u < MT; ++u) {
+#pragma unroll
+    for (int v = 0; v < NV; ++v) o[u][v] = v4f{0.f, 0.f, 0.f, 0.f};
+    m[u] = neg_inf();
+    l[u] = 0.f;
+  }
   const float scale2 = a.scale * 1.4426950408889634f;  // scores in powers of two
 
   // Copies the tile's rows: lane i holds the cache row of token i, this wave copies
@@ -185,94 +189,130 @@ __global__ __launch_bounds__(HG * TH * kWave) void attn_kernel(AttnArgs a, Parts
     copy(std::integral_constant<int, 8>{}, buf + kLatentBytes, kLatent * 2);
   };
   // The lanes' cache rows of a tile; places of no token take the first visible one's.
-  auto rows_of = [&](const Token& t, uint64_t& mask) -> int64_t {
-    const bool ok = t.p >= 0 && t.page >= 0 && t.page < a.num_pages;
+  auto rows_of = [&](int p, int page, uint64_t& mask) -> int64_t {
+    const bool ok = p >= 0 && page >= 0 && page < a.num_pages;
     mask = __ballot(ok);
-    const int64_t mine = (int64_t)t.page * kPage + t.p % kPage;
+    const int64_t mine = (int64_t)page * kPage + p % kPage;
     const int from = ok || mask == 0 ? lane : __builtin_ctzll(mask);
     const uint32_t lo = (uint32_t)__shfl((int)(uint32_t)mine, from);
     const uint32_t hi = (uint32_t)__shfl((int)(uint32_t)((uint64_t)mine >> 32), from);
     return (int64_t)(((uint64_t)hi << 32) | lo);
   };
 
-  auto compute = [&](const uint8_t* buf, uint64_t mask) {
-    const uint8_t* pos = buf + kLatentBytes;
-    const int base = th * kTokens;
-    v4f s[NT];
+  // LDS addresses of the operands, from a tile's first byte: the places of the chunks
+  // differ between steps by constants xored into few bits (swz), so one register for
+  // each kind of row is kept and the rest recomputed
+  const int n_key = n * (kLatent * 2) + ((g ^ swz<LC>(n)) << 4);
+  const int n_pos = kLatentBytes + n * (kRopeWidth * 2) + ((g ^ swz<8>(n)) << 4);
+  const int vt = 4 * g + (n >> 2);
+  const int n_val = vt * (kLatent * 2) + ((((n >> 1) & 1) ^ swz<LC>(vt)) << 4) + 8 * (n & 1);
+
+  // kTokens tokens of a tile against the wave's heads, 16 * NT at a time
+  auto compute = [&](MXIDX_LDS const uint8_t* buf, uint64_t mask) {
+#pragma unroll 1
+    for (int base = th * kTokens; base < (th + 1) * kTokens; base += 16 * NT) {
+      MXIDX_LDS const uint8_t* latent = buf + base * (kLatent * 2);
+      int key = (int)(uintptr_t)(latent + n_key);
+      int pos = (int)(uintptr_t)(buf + base * (kRopeWidth * 2) + n_pos);
+      int val = (int)(uintptr_t)(latent + n_val);
+      asm volatile("" : "+v"(key), "+v"(pos), "+v"(val));
+      v4f s[MT][NT];
 #pragma unroll
-    for (int t = 0; t < NT; ++t) s[t] = v4f{0.f, 0.f, 0.f, 0.f};
+      for (int u = 0; u < MT; ++u)
 #pragma unroll
-    for (int k = 0; k < KS; ++k) {
+        for (int t = 0; t < NT; ++t) s[u][t] = v4f{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        const int tok = base + 16 * t + n;
-        const uint8_t* p = k < KL ? buf + tok * (kLatent * 2) + (((4 * k + g) ^ swz<LC>(tok)) << 4)
-                                  : pos + tok * (kRopeWidth * 2) + (((4 * (k - KL) + g) ^ swz<8>(tok)) << 4);
-        s[t] = mfma_bf16(*reinterpret_cast<const v8s*>(p), q[k], s[t]);
+      for (int k = 0; k < KS; ++k) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          // chunk 4k + g: bits 0..3 xored with swz, the rest added
+          const int at = k < KL ? (key ^ ((k & 3) << 6)) + (k >> 2) * 256 + t * 16 * (kLatent * 2)
+                                : (pos ^ ((k - KL) << 6)) + t * 16 * (kRopeWidth * 2);
+          const v8s x = *(MXIDX_LDS const v8s*)(uintptr_t)at;
+#pragma unroll
+          for (int u = 0; u < MT; ++u) s[u][t] = mfma_bf16(x, q[u][k], s[u][t]);
+        }
       }
-    }
-    // s[t][i]: token base + 16t + 4g + i of this lane's head
-    float top = neg_inf();
+      // s[u][t][i]: token base + 16t + 4g + i, head head0 + 16u
+      float f[MT];
+      bool grow = false;
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
+      for (int u = 0; u < MT; ++u) {
+        float top = neg_inf();
 #pragma unroll
-      for (int i = 0; i < 4; ++i) s[t][i] *= scale2;
-    if (mask != ~0ull) {
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        const uint32_t bits = (uint32_t)(mask >> (base + 16 * t + 4 * g));
+          for (int i = 0; i < 4; ++i) s[u][t][i] *= scale2;
+        if (mask != ~0ull) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s[t][i] = (bits >> i) & 1 ? s[t][i] : neg_inf();
+          for (int t = 0; t < NT; ++t) {
+            const uint32_t bits = (uint32_t)(mask >> (base + 16 * t + 4 * g));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[u][t][i] = (bits >> i) & 1 ? s[u][t][i] : neg_inf();
+          }
+        }
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) top = fmaxf(top, s[u][t][i]);
+        top = fmaxf(top, __shfl_xor(top, 16));
+        top = fmaxf(top, __shfl_xor(top, 32));
+        // the reference is raised only where weights would pass 2^kSlack: what was summed
+        // so far is seldom rescaled
+        f[u] = 1.f;
+        if (m[u] == neg_inf()) {
+          m[u] = top;                                  // nothing summed yet
+        } else if (top > m[u] + kSlack) {
+          f[u] = __builtin_amdgcn_exp2f(m[u] - top);
+          m[u] = top;
+          grow = true;
+        }
       }
-    }
+      if (__any(grow)) {
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
+        for (int u = 0; u < MT; ++u) {
+          l[u] *= f[u];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) top = fmaxf(top, s[t][i]);
-    top = fmaxf(top, __shfl_xor(top, 16));
-    top = fmaxf(top, __shfl_xor(top, 32));
-    const float m2 = fmaxf(m, top);
-    if (__any(m2 > m)) {
-      const float f = m2 > m ? __builtin_amdgcn_exp2f(m - m2) : 1.f;
-      l *= f;
-#pragma unroll
-      for (int v = 0; v < NV; ++v) o[v] *= f;
-      m = m2;
-    }
-    const float ref = m == neg_inf() ? 0.f : m;        // no token yet: every weight 0
-    uint32_t w[NT][2];
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      float p[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        p[i] = __builtin_amdgcn_exp2f(s[t][i] - ref);
-        l += p[i];
+          for (int v = 0; v < NV; ++v) o[u][v] *= f[u];
+        }
       }
-      w[t][0] = pack2(p[0], p[1]);
-      w[t][1] = pack2(p[2], p[3]);
-    }
-    // values: lane 4j + c of a 16-lane group reads tokens 4g + j, values 4c..4c+3, and
-    // gets tokens 4g..4g+3 of value n
-    auto values = [&](int t, int v) -> v4s {
-      const int tok = base + 16 * t + 4 * g + (n >> 2);
-      const int chunk = (2 * v + ((n >> 1) & 1)) ^ swz<LC>(tok);
-      return __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-          (MXIDX_LDS v4s*)(buf + tok * (kLatent * 2) + (chunk << 4) + 8 * (n & 1)));
-    };
-    if constexpr (NT == 1) {
-      const v4s b = __builtin_bit_cast(v4s, uint2{w[0][0], w[0][1]});
+      uint32_t w[MT][NT][2];
 #pragma unroll
-      for (int v = 0; v < NV; ++v)
-        o[v] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(values(0, v), b, o[v], 0, 0, 0);
-    } else {
+      for (int u = 0; u < MT; ++u) {
+        const float ref = m[u] == neg_inf() ? 0.f : m[u];   // no token yet: every weight 0
 #pragma unroll
-      for (int t = 0; t < NT; t += 2) {
-        const v8s b = __builtin_bit_cast(v8s, uint4{w[t][0], w[t][1], w[t + 1][0], w[t + 1][1]});
+        for (int t = 0; t < NT; ++t) {
+          float p[4];
 #pragma unroll
-        for (int v = 0; v < NV; ++v) {
-          const v4s x = values(t, v), y = values(t + 1, v);
-          o[v] = mfma_bf16(__builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7), b, o[v]);
+          for (int i = 0; i < 4; ++i) {
+            p[i] = __builtin_amdgcn_exp2f(s[u][t][i] - ref);
+            l[u] += p[i];
+          }
+          w[u][t][0] = pack2(p[0], p[1]);
+          w[u][t][1] = pack2(p[2], p[3]);
+        }
+      }
+      // values: lane 4j + c of a 16-lane group reads tokens 4g + j, values 4c..4c+3, and
+      // gets tokens 4g..4g+3 of value n
+      auto values = [&](int t, int v) -> v4s {
+        const int at = (val ^ ((v & 7) << 5)) + (v >> 3) * 256 + t * 16 * (kLatent * 2);
+        return __builtin_amdgcn_ds_read_tr16_b64_v4i16((MXIDX_LDS v4s*)(uintptr_t)at);
+      };
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        if constexpr (NT == 1) {
+          const v4s x = values(0, v);
+#pragma unroll
+          for (int u = 0; u < MT; ++u)
+            o[u][v] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(
+                x, __builtin_bit_cast(v4s, uint2{w[u][0][0], w[u][0][1]}), o[u][v], 0, 0, 0);
+        } else {
+          const v4s x = values(0, v), y = values(1, v);
+          const v8s xy = __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
+#pragma unroll
+          for (int u = 0; u < MT; ++u)
+            o[u][v] = mfma_bf16(xy, __builtin_bit_cast(v8s, uint4{w[u][0][0], w[u][0][1], w[u][NT - 1][0],
+                                                                  w[u][NT - 1][1]}), o[u][v]);
         }
       }
     }
@@ -281,91 +321,107 @@ __global__ __launch_bounds__(HG * TH * kWave) void attn_kernel(AttnArgs a, Parts
   // the pipeline: the tile computed, the next one's rows on their way to LDS, the one
   // behind it looking up its pages and the one behind that its list entries
   if (t0 < t1) {
-    auto entry = [&](int64_t t) { return t < t1 ? token_entry(a, r, row, t * kTile + lane) : -1; };
-    Token now, next;
-    now.p = entry(t0);
-    next.p = entry(t0 + 1);
-    now.page = token_page(a, row, now.p);
+    auto entry = [&](int t) { return t < t1 ? token_entry(a, r, row, t * kTile + lane) : -1; };
+    int next = entry(t0 + 1);
     uint64_t mask;
-    int64_t rows = rows_of(now, mask);
-    if (mask) stage(lds, rows);
-    next.page = token_page(a, row, next.p);
-    int64_t far = entry(t0 + 2);
-    for (int64_t t = t0; t < t1; ++t) {
-      uint8_t* cur = lds + ((t - t0) & 1) * kTileBytes;
-      uint8_t* nxt = lds + ((t - t0 + 1) & 1) * kTileBytes;
+    {
+      const int now = entry(t0);
+      const int64_t rows = rows_of(now, token_page(a, row, now), mask);
+      if (mask) stage(lds, rows);
+    }
+    int page = token_page(a, row, next);
+    int far = entry(t0 + 2);
+    for (int t = t0; t < t1; ++t) {
+      const int cur = ((t - t0) & 1) * kTileBytes;
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
       __syncthreads();
       uint64_t next_mask = 0;
       if (t + 1 < t1) {
-        rows = rows_of(next, next_mask);
-        if (next_mask) stage(nxt, rows);
-        next.p = far;
-        next.page = token_page(a, row, far);
+        const int64_t rows = rows_of(next, page, next_mask);
+        if (next_mask) stage(lds + (kTileBytes - cur), rows);
+        next = far;
+        page = token_page(a, row, far);
         far = entry(t + 3);
       }
-      if (mask) compute(cur, mask);
+      if (mask) compute((MXIDX_LDS const uint8_t*)lds + cur, mask);
       mask = next_mask;
     }
   }
 
-  l += __shfl_xor(l, 16);
-  l += __shfl_xor(l, 32);
+#pragma unroll
+  for (int u = 0; u < MT; ++u) {
+    l[u] += __shfl_xor(l[u], 16);
+    l[u] += __shfl_xor(l[u], 32);
+  }
   if constexpr (TH > 1) {
-    // the token parts' sums joined in LDS: part th > 0 leaves its own, part 0 takes them
+    // the token parts' sums joined in LDS, 16 heads at a time: part th > 0 leaves its
+    // own, part 0 takes them
     float* lo = reinterpret_cast<float*>(lds);
-    if (g == 0) {
-      join_ml[(th * HG + hg) * 32 + 2 * n] = m;
-      join_ml[(th * HG + hg) * 32 + 2 * n + 1] = l;
-    }
-    __syncthreads();                                   // the last tile's reads are done
-    if (th > 0) {
-      float* dst = lo + ((th - 1) * HG + hg) * 16 * kLatent + 4 * lane;
 #pragma unroll
-      for (int v = 0; v < NV; ++v) *reinterpret_cast<v4f*>(dst + v * 256) = o[v];
+    for (int u = 0; u < MT; ++u) {
+      const int slot = (th * HG + hg) * MT * 16 + 16 * u + n;
+      if (g == 0) {
+        join_ml[2 * slot] = m[u];
+        join_ml[2 * slot + 1] = l[u];
+      }
     }
-    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < MT; ++u) {
+      __syncthreads();                                 // the last reads are done
+      if (th > 0) {
+        float* dst = lo + ((th - 1) * HG + hg) * 16 * kLatent + 4 * lane;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) *reinterpret_cast<v4f*>(dst + v * 256) = o[u][v];
+      }
+      __syncthreads();
+      if (th > 0) continue;
+      float top = m[u];
+#pragma unroll
+      for (int t = 1; t < TH; ++t)
+        top = fmaxf(top, join_ml[2 * ((t * HG + hg) * MT * 16 + 16 * u + n)]);
+      const float ref = top == neg_inf() ? 0.f : top;
+      float f = __builtin_amdgcn_exp2f(m[u] - ref);
+      l[u] *= f;
+#pragma unroll
+      for (int v = 0; v < NV; ++v) o[u][v] *= f;
+#pragma unroll
+      for (int t = 1; t < TH; ++t) {
+        const int slot = (t * HG + hg) * MT * 16 + 16 * u + n;
+        f = __builtin_amdgcn_exp2f(join_ml[2 * slot] - ref);
+        l[u] += f * join_ml[2 * slot + 1];
+        const float* src = lo + ((t - 1) * HG + hg) * 16 * kLatent + 4 * lane;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) o[u][v] += f * *reinterpret_cast<const v4f*>(src + v * 256);
+      }
+      m[u] = top;
+    }
     if (th > 0) return;
-    float top = m;
-#pragma unroll
-    for (int t = 1; t < TH; ++t) top = fmaxf(top, join_ml[(t * HG + hg) * 32 + 2 * n]);
-    const float ref = top == neg_inf() ? 0.f : top;
-    float f = __builtin_amdgcn_exp2f(m - ref);
-    l *= f;
-#pragma unroll
-    for (int v = 0; v < NV; ++v) o[v] *= f;
-#pragma unroll
-    for (int t = 1; t < TH; ++t) {
-      f = __builtin_amdgcn_exp2f(join_ml[(t * HG + hg) * 32 + 2 * n] - ref);
-      l += f * join_ml[(t * HG + hg) * 32 + 2 * n + 1];
-      const float* src = lo + ((t - 1) * HG + hg) * 16 * kLatent + 4 * lane;
-#pragma unroll
-      for (int v = 0; v < NV; ++v) o[v] += f * *reinterpret_cast<const v4f*>(src + v * 256);
-    }
-    m = top;
   }
 
-  // o[v][i]: value 16v + 4g + i of this lane's head
-  if (parts.splits > 1) {
-    const int64_t at = (r * parts.splits + split) * parts.heads + head;
-    if (g == 0) *reinterpret_cast<float2*>(parts.ml + 2 * at) = make_float2(m, l);
-    if (__all(l == 0.f)) return;
-    float* dst = parts.o + at * kLatent + 4 * g;
+  // o[u][v][i]: value 16v + 4g + i of head head0 + 16u
 #pragma unroll
-    for (int v = 0; v < NV; ++v) *reinterpret_cast<v4f*>(dst + 16 * v) = o[v];
-    return;
+  for (int u = 0; u < MT; ++u) {
+    const int head = head0 + 16 * u;
+    if (parts.splits > 1) {
+      const int64_t at = (r * parts.splits + split) * parts.heads + head;
+      if (g == 0) *reinterpret_cast<float2*>(parts.ml + 2 * at) = make_float2(m[u], l[u]);
+      if (__all(l[u] == 0.f)) continue;
+      float* dst = parts.o + at * kLatent + 4 * g;
+#pragma unroll
+      for (int v = 0; v < NV; ++v) *reinterpret_cast<v4f*>(dst + 16 * v) = o[u][v];
+      continue;
+    }
+    if (head >= a.H) continue;
+    const float inv = l[u] == 0.f ? 0.f : 1.f / l[u];
+    uint16_t* out = static_cast<uint16_t*>(a.out) + r * a.out_row_stride +
+                    (int64_t)head * a.out_head_stride + 4 * g;
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+      *reinterpret_cast<uint2*>(out + 16 * v) =
+          make_uint2(pack2(o[u][v][0] * inv, o[u][v][1] * inv), pack2(o[u][v][2] * inv, o[u][v][3] * inv));
+    if (a.lse && g == 0)
+      a.lse[r * a.H + head] = l[u] == 0.f ? neg_inf() : m[u] * 0.6931471805599453f + logf(l[u]);
   }
-  if (head >= a.H) return;
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  uint16_t* out = static_cast<uint16_t*>(a.out) + r * a.out_row_stride +
-                  (int64_t)head * a.out_head_stride + 4 * g;
-#pragma unroll
-  for (int v = 0; v < NV; ++v)
-    *reinterpret_cast<uint2*>(out + 16 * v) =
-        l == 0.f ? make_uint2(0, 0)
-                 : make_uint2(pack2(o[v][0] * inv, o[v][1] * inv), pack2(o[v][2] * inv, o[v][3] * inv));
-  if (a.lse && g == 0)
-    a.lse[r * a.H + head] = l == 0.f ? neg_inf() : m * 0.6931471805599453f + logf(l);
 }
 
 // The splits' sums of one (row, head), kLatent / 4 lanes: 4 values each.
@@ -432,10 +488,10 @@ hipError_t launch(const AttnArgs& a, void* workspace, hipStream_t stream) {
   }
   const dim3 grid((uint32_t)(a.rows * (p.heads / p.group_heads) * p.splits));
   switch (p.group_heads) {
-    case 16: hipLaunchKernelGGL((attn_kernel<kLatent, 1, 4>), grid, dim3(256), 0, stream, a, parts); break;
-    case 32: hipLaunchKernelGGL((attn_kernel<kLatent, 2, 2>), grid, dim3(256), 0, stream, a, parts); break;
-    case 64: hipLaunchKernelGGL((attn_kernel<kLatent, 4, 2>), grid, dim3(512), 0, stream, a, parts); break;
-    default: hipLaunchKernelGGL((attn_kernel<kLatent, 8, 1>), grid, dim3(512), 0, stream, a, parts); break;
+    case 16: hipLaunchKernelGGL((attn_kernel<kLatent, 1, 1, 4>), grid, dim3(256), 0, stream, a, parts); break;
+    case 32: hipLaunchKernelGGL((attn_kernel<kLatent, 2, 1, 2>), grid, dim3(256), 0, stream, a, parts); break;
+    case 64: hipLaunchKernelGGL((attn_kernel<kLatent, 4, 1, 2>), grid, dim3(512), 0, stream, a, parts); break;
+    default: hipLaunchKernelGGL((attn_kernel<kLatent, 8, 1, 1>), grid, dim3(512), 0, stream, a, parts); break;
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;
