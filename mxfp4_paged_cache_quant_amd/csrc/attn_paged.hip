@@ -33,8 +33,6 @@
 //
 // Few rows: the tokens are split over workgroups, each leaving its unscaled sums with
 // m and l in the workspace, and a second launch joins them.
-#include <type_traits>
-
 #include "common.hpp"
 #include "launch.hpp"
 
@@ -44,6 +42,7 @@ namespace {
 constexpr int kRopeWidth = 64;
 constexpr int kTile = 64;                  // tokens per tile: a lane each
 constexpr int kCus = 256;
+constexpr int kAhead = 3;                  // operand steps in flight from LDS
 constexpr float kSlack = 8.f;               // weights stay below 2^8 of the reference's
 
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
@@ -75,6 +74,14 @@ __device__ __forceinline__ int swz(int t) {
   return (t >> 1) & 7;
 }
 
+// The lane number, computed anew where it is called: nothing derived from it can be
+// kept in registers from one call to the next.
+__device__ __forceinline__ int fresh_lane() {
+  int zero = 0;
+  asm volatile("" : "+v"(zero));
+  return (int)__builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, (uint32_t)zero));
+}
+
 struct Row {                               // a query row's window
   int seq;
   int64_t ks;
@@ -83,24 +90,28 @@ struct Row {                               // a query row's window
 
 // False when the row belongs to no sequence.
 __device__ __forceinline__ bool row_of(const AttnArgs& a, int64_t r, Row& o) {
-  o.seq = a.row_seq ? a.row_seq[r] : (int)(r / a.rows_per_seq);
+  o.seq = a.row_seq ? a.row_seq[r] : (int)((uint32_t)r / (uint32_t)a.rows_per_seq);
   if (o.seq < 0 || o.seq >= a.B) return false;
   o.ks = a.ks ? a.ks[r] : 0;
   o.window = (int)min(max((int64_t)a.ke[r] - o.ks, (int64_t)0), a.max_tokens);
   return true;
 }
 
-// A lane's token of a tile, in the steps that the pipeline takes apart: the token of
-// the sequence (-1: none), its page, and then its cache row.
-__device__ __forceinline__ int token_entry(const AttnArgs& a, int64_t r, const Row& row, int e) {
-  if (!a.indices) return e < row.window ? e : -1;
-  if (e >= a.k) return -1;
-  const int64_t p = (int64_t)a.indices[r * a.idx_row_stride + e] - row.ks;
-  return p >= 0 && p < row.window ? (int)p : -1;
+// A lane's token of a tile, in the steps that the pipeline takes apart so that none
+// waits for its load at once: the list entry (of a window: the place itself), the token
+// of the sequence (-1: none), its page, and then its cache row.  Loads of places
+// without a token read a token's that is there.
+__device__ __forceinline__ int list_entry(const AttnArgs& a, int64_t r, int e) {
+  return a.indices ? a.indices[r * a.idx_row_stride + min(e, a.k - 1)] : e;
+}
+
+__device__ __forceinline__ int token_of(const AttnArgs& a, const Row& row, int entry, int e) {
+  const int64_t p = a.indices ? (int64_t)entry - row.ks : entry;
+  return p >= 0 && p < row.window && (!a.indices || e < a.k) ? (int)p : -1;
 }
 
 __device__ __forceinline__ int token_page(const AttnArgs& a, const Row& row, int p) {
-  return p < 0 ? -1 : a.block_table[row.seq * a.bt_row_stride + p / kPage];
+  return a.block_table[row.seq * a.bt_row_stride + max(p, 0) / kPage];
 }
 
 // Partial sums of the split form: for each (row, split) HP x n output sums, then
@@ -109,7 +120,44 @@ struct Parts {
   float* o;
   float* ml;
   int splits, heads;
+  int pages;              // of the cache, at most 2^31 - 1: all that a table names
+  uint32_t cache_bytes;   // the cache's size below 4 GiB (small_cache)
+  bool small_cache;
 };
+
+// 16 bytes a lane to LDS, at dst + 16 * lane.
+__device__ __forceinline__ void copy16(__amdgpu_buffer_rsrc_t rs, MXIDX_LDS uint8_t* dst, int offset) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (MXIDX_LDS void*)dst, 16, offset, 0, 0, 0);
+}
+
+// Copies C 16-byte chunks, from byte `offset` on, of each of kMine rows of a tile to
+// LDS: token t = first .. first + kMine - 1 from the cache row whose byte lane t holds
+// (lo, hi).  Rows that fill less than an instruction share one where 32-bit offsets
+// reach the whole cache, and take one each where they do not.
+template <int C, int kMine, int kRowBytes>
+__device__ __forceinline__ void copy_rows(const char* base, const Parts& parts, MXIDX_LDS uint8_t* dst,
+                                          int first, int lo, int hi, int offset, int ln) {
+  constexpr int kPer = C >= kWave ? 1 : kWave / C;
+  static_assert(C <= kWave && kMine % kPer == 0, "whole instructions");
+  if (kPer > 1 && parts.small_cache) {
+    const __amdgpu_buffer_rsrc_t rs = buffer_rsrc(base, (int)parts.cache_bytes);
+#pragma unroll
+    for (int i = 0; i < kMine; i += kPer) {
+      const int t = first + i + ln / C;
+      copy16(rs, dst + (first + i) * C * 16, __shfl(lo, t) + offset + (((ln % C) ^ swz<C>(t)) << 4));
+    }
+  } else if (kPer == 1 || ln < C) {
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+      const int t = first + i;
+      const uint32_t l32 = (uint32_t)__builtin_amdgcn_readlane(lo, t);
+      const uint32_t h32 = (uint32_t)__builtin_amdgcn_readlane(hi, t);
+      copy16(buffer_rsrc(base + (((uint64_t)h32 << 32) | l32), kRowBytes), dst + t * C * 16,
+             offset + ((ln ^ swz<C>(t)) << 4));
+      __builtin_amdgcn_sched_barrier(0);               // one row's descriptor at a time
+    }
+  }
+}
 
 template <int kLatent, int HG, int MT, int TH>
 __global__ __launch_bounds__(HG * TH * kWave, 1) void attn_kernel(AttnArgs a, Parts parts) {
@@ -122,25 +170,32 @@ __global__ __launch_bounds__(HG * TH * kWave, 1) void attn_kernel(AttnArgs a, Pa
   constexpr int NV = kLatent / 16;                     // 16-value parts of the output
   constexpr int LC = kLatent / 8;                      // 16-byte chunks of a latent row
   constexpr int kLatentBytes = kTile * kLatent * 2, kTileBytes = kTile * kRow * 2;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kTileBytes];
+  // Two arrays, and the loop below unrolled over them: the compiler then sees that a
+  // tile's reads do not touch the one being copied, and does not wait for its copies.
+  __shared__ __attribute__((aligned(1024))) uint8_t tile0[kTileBytes];
+  __shared__ __attribute__((aligned(1024))) uint8_t tile1[kTileBytes];
   static_assert(2 * kTileBytes <= 160 * 1024, "two tiles fit the LDS");
-  static_assert((TH - 1) * HG * 16 * kLatent * 4 <= 2 * kTileBytes, "the waves' join fits them");
+  constexpr int kJoin = 16 * kLatent * 4;              // a wave's 16 heads, joined at the end
+  constexpr int kJoin0 = kTileBytes / kJoin;           // of them in the first tile
+  static_assert((TH - 1) * HG <= 2 * kJoin0, "the waves' join fits the tiles");
   __shared__ float join_ml[TH > 1 ? TH * kHeads * 2 : 1];
 
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int hg = wave % HG, th = wave / HG;
   const int g = lane >> 4, n = lane & 15;
-  const int groups = parts.heads / kHeads;
-  const int group = blockIdx.x % groups;
-  const int split = (blockIdx.x / groups) % parts.splits;
-  const int64_t r = blockIdx.x / groups / parts.splits;
+  const uint32_t groups = (uint32_t)parts.heads / kHeads, unit = blockIdx.x / groups;
+  const int group = (int)(blockIdx.x - unit * groups);
+  const uint32_t r32 = unit / (uint32_t)parts.splits;
+  const int split = (int)(unit - r32 * (uint32_t)parts.splits);
+  const int64_t r = r32;
   Row row;
   if (!row_of(a, r, row)) return;
-  const int entries = a.indices ? a.k : row.window;
+  const int entries = row.window == 0 ? 0 : a.indices ? a.k : row.window;
   const int tiles = (entries + kTile - 1) / kTile;
-  const int t0 = (int)((int64_t)tiles * split / parts.splits);
-  const int t1 = (int)((int64_t)tiles * (split + 1) / parts.splits);
+  const int share = tiles / parts.splits, more = tiles - share * parts.splits;
+  const int t0 = split * share + min(split, more);     // the first `more` splits take one more
+  const int t1 = t0 + share + (split < more ? 1 : 0);
   const int head0 = group * kHeads + hg * MT * 16 + n; // this lane's heads: head0 + 16u
 
   // the wave's query: step s holds values 32s + 8g .. +7 of a head
@@ -163,76 +218,72 @@ __global__ __launch_bounds__(HG * TH * kWave, 1) void attn_kernel(AttnArgs a, Pa
   }
   const float scale2 = a.scale * 1.4426950408889634f;  // scores in powers of two
 
-  // Copies the tile's rows: lane i holds the cache row of token i, this wave copies
-  // tokens kTile/kWaves at a time, 64 chunks an instruction.
-  auto stage = [&](uint8_t* buf, int64_t cache_row) {
+  // Copies the tile's rows, kTile/kWaves by each wave: lane i holds the cache row of
+  // token i.  By buffer loads: the compiler counts them apart from the LDS reads, which
+  // it would drain at every use behind global_load_lds's.  Nothing of it is kept over the
+  // products: they take all registers, and a spilled one would be waited for behind the
+  // copies.
+  auto stage = [&](MXIDX_LDS uint8_t* buf, int64_t cache_row) __attribute__((always_inline)) {
     constexpr int kMine = kTile / kWaves;
     const int first = wave * kMine;
     const char* base = static_cast<const char*>(a.cache);
     const uint64_t bytes = (uint64_t)cache_row * (kRow * 2);
-    const uint32_t lo = (uint32_t)bytes, hi = (uint32_t)(bytes >> 32);
-    auto copy = [&](auto chunks_c, uint8_t* dst, int offset) {
-      constexpr int C = chunks_c;                      // chunks of a row
-      constexpr int kPer = C >= kWave ? 1 : kWave / C; // rows of an instruction
-      static_assert(C <= kWave && kMine % kPer == 0, "whole instructions");
-      const int sub = lane / C, place = lane % C;
-#pragma unroll
-      for (int i = 0; i < kMine; i += kPer) {
-        const int t = first + i + sub;
-        const uint32_t l32 = (uint32_t)__shfl((int)lo, t), h32 = (uint32_t)__shfl((int)hi, t);
-        const char* src = base + (((uint64_t)h32 << 32) | l32) + offset + ((place ^ swz<C>(t)) << 4);
-        __builtin_amdgcn_global_load_lds((const MXIDX_GLOBAL void*)src,
-                                         (MXIDX_LDS void*)(dst + (first + i) * C * 16), 16, 0, 0);
-      }
-    };
-    copy(std::integral_constant<int, LC>{}, buf, 0);
-    copy(std::integral_constant<int, 8>{}, buf + kLatentBytes, kLatent * 2);
+    const int lo = (int)(uint32_t)bytes, hi = (int)(uint32_t)(bytes >> 32);
+    const int ln = fresh_lane();
+    copy_rows<LC, kMine, kRow * 2>(base, parts, buf, first, lo, hi, 0, ln);
+    copy_rows<8, kMine, kRow * 2>(base, parts, buf + kLatentBytes, first, lo, hi, kLatent * 2, ln);
   };
   // The lanes' cache rows of a tile; places of no token take the first visible one's.
   auto rows_of = [&](int p, int page, uint64_t& mask) -> int64_t {
-    const bool ok = p >= 0 && page >= 0 && page < a.num_pages;
+    const bool ok = p >= 0 && page >= 0 && page < parts.pages;
     mask = __ballot(ok);
     const int64_t mine = (int64_t)page * kPage + p % kPage;
-    const int from = ok || mask == 0 ? lane : __builtin_ctzll(mask);
+    const int from = ok || mask == 0 ? fresh_lane() : __builtin_ctzll(mask);
     const uint32_t lo = (uint32_t)__shfl((int)(uint32_t)mine, from);
     const uint32_t hi = (uint32_t)__shfl((int)(uint32_t)((uint64_t)mine >> 32), from);
     return (int64_t)(((uint64_t)hi << 32) | lo);
   };
 
-  // LDS addresses of the operands, from a tile's first byte: the places of the chunks
-  // differ between steps by constants xored into few bits (swz), so one register for
-  // each kind of row is kept and the rest recomputed
-  const int n_key = n * (kLatent * 2) + ((g ^ swz<LC>(n)) << 4);
-  const int n_pos = kLatentBytes + n * (kRopeWidth * 2) + ((g ^ swz<8>(n)) << 4);
-  const int vt = 4 * g + (n >> 2);
-  const int n_val = vt * (kLatent * 2) + ((((n >> 1) & 1) ^ swz<LC>(vt)) << 4) + 8 * (n & 1);
-
   // kTokens tokens of a tile against the wave's heads, 16 * NT at a time
-  auto compute = [&](MXIDX_LDS const uint8_t* buf, uint64_t mask) {
+  auto compute = [&](MXIDX_LDS const uint8_t* buf, uint64_t mask) __attribute__((always_inline)) {
+    int stop = (th + 1) * kTokens;
+    asm volatile("" : "+s"(stop));                     // stays a loop
 #pragma unroll 1
-    for (int base = th * kTokens; base < (th + 1) * kTokens; base += 16 * NT) {
-      MXIDX_LDS const uint8_t* latent = buf + base * (kLatent * 2);
-      int key = (int)(uintptr_t)(latent + n_key);
-      int pos = (int)(uintptr_t)(buf + base * (kRopeWidth * 2) + n_pos);
-      int val = (int)(uintptr_t)(latent + n_val);
-      asm volatile("" : "+v"(key), "+v"(pos), "+v"(val));
+    for (int base = th * kTokens; base < stop; base += 16 * NT) {
+      // LDS offsets of the operands in the tile: the places of the chunks differ between
+      // steps by constants xored into few bits (swz), so one register for each kind of
+      // row does
+      const int ln = fresh_lane(), n = ln & 15, g = ln >> 4;
+      const int key = base * (kLatent * 2) + n * (kLatent * 2) + ((g ^ swz<LC>(n)) << 4);
+      const int pos = kLatentBytes + base * (kRopeWidth * 2) + n * (kRopeWidth * 2) + ((g ^ swz<8>(n)) << 4);
       v4f s[MT][NT];
 #pragma unroll
       for (int u = 0; u < MT; ++u)
 #pragma unroll
         for (int t = 0; t < NT; ++t) s[u][t] = v4f{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int k = 0; k < KS; ++k) {
+      // keys: kAhead steps are on their way while one is used
+      auto keys = [&](int k, v8s (&x)[NT]) __attribute__((always_inline)) {
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
           // chunk 4k + g: bits 0..3 xored with swz, the rest added
           const int at = k < KL ? (key ^ ((k & 3) << 6)) + (k >> 2) * 256 + t * 16 * (kLatent * 2)
                                 : (pos ^ ((k - KL) << 6)) + t * 16 * (kRopeWidth * 2);
-          const v8s x = *(MXIDX_LDS const v8s*)(uintptr_t)at;
-#pragma unroll
-          for (int u = 0; u < MT; ++u) s[u][t] = mfma_bf16(x, q[u][k], s[u][t]);
+          x[t] = *(MXIDX_LDS const v8s*)(buf + at);
         }
+      };
+      v8s x[kAhead][NT];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) keys(k, x[k]);
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int u = 0; u < MT; ++u) s[u][t] = mfma_bf16(x[k % kAhead][t], q[u][k], s[u][t]);
+        if (k + kAhead < KS) keys(k + kAhead, x[k % kAhead]);
       }
+      __builtin_amdgcn_sched_barrier(0);
       // s[u][t][i]: token base + 16t + 4g + i, head head0 + 16u
       float f[MT];
       bool grow = false;
@@ -246,7 +297,7 @@ __global__ __launch_bounds__(HG * TH * kWave, 1) void attn_kernel(AttnArgs a, Pa
         if (mask != ~0ull) {
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
-            const uint32_t bits = (uint32_t)(mask >> (base + 16 * t + 4 * g));
+            const uint32_t bits = (uint32_t)(mask >> (base + 16 * t + 4 * (fresh_lane() >> 4)));
 #pragma unroll
             for (int i = 0; i < 4; ++i) s[u][t][i] = (bits >> i) & 1 ? s[u][t][i] : neg_inf();
           }
@@ -294,57 +345,72 @@ __global__ __launch_bounds__(HG * TH * kWave, 1) void attn_kernel(AttnArgs a, Pa
       }
       // values: lane 4j + c of a 16-lane group reads tokens 4g + j, values 4c..4c+3, and
       // gets tokens 4g..4g+3 of value n
-      auto values = [&](int t, int v) -> v4s {
-        const int at = (val ^ ((v & 7) << 5)) + (v >> 3) * 256 + t * 16 * (kLatent * 2);
-        return __builtin_amdgcn_ds_read_tr16_b64_v4i16((MXIDX_LDS v4s*)(uintptr_t)at);
+      const int vl = fresh_lane(), vn = vl & 15, vt = 4 * (vl >> 4) + (vn >> 2);
+      const int val = base * (kLatent * 2) + vt * (kLatent * 2) +
+                      ((((vn >> 1) & 1) ^ swz<LC>(vt)) << 4) + 8 * (vn & 1);
+      v4s y[kAhead][NT];
+      auto values = [&](int v, v4s (&r)[NT]) __attribute__((always_inline)) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+          r[t] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((MXIDX_LDS v4s*)(
+              buf + (val ^ ((v & 7) << 5)) + (v >> 3) * 256 + t * 16 * (kLatent * 2)));
       };
 #pragma unroll
+      for (int v = 0; v < kAhead; ++v) values(v, y[v]);
+#pragma unroll
       for (int v = 0; v < NV; ++v) {
+        __builtin_amdgcn_sched_barrier(0);
+        const v4s(&z)[NT] = y[v % kAhead];
         if constexpr (NT == 1) {
-          const v4s x = values(0, v);
 #pragma unroll
           for (int u = 0; u < MT; ++u)
             o[u][v] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(
-                x, __builtin_bit_cast(v4s, uint2{w[u][0][0], w[u][0][1]}), o[u][v], 0, 0, 0);
+                z[0], __builtin_bit_cast(v4s, uint2{w[u][0][0], w[u][0][1]}), o[u][v], 0, 0, 0);
         } else {
-          const v4s x = values(0, v), y = values(1, v);
-          const v8s xy = __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
+          const v8s zz = __builtin_shufflevector(z[0], z[NT - 1], 0, 1, 2, 3, 4, 5, 6, 7);
 #pragma unroll
           for (int u = 0; u < MT; ++u)
-            o[u][v] = mfma_bf16(xy, __builtin_bit_cast(v8s, uint4{w[u][0][0], w[u][0][1], w[u][NT - 1][0],
+            o[u][v] = mfma_bf16(zz, __builtin_bit_cast(v8s, uint4{w[u][0][0], w[u][0][1], w[u][NT - 1][0],
                                                                   w[u][NT - 1][1]}), o[u][v]);
         }
+        if (v + kAhead < NV) values(v + kAhead, y[v % kAhead]);
       }
+      __builtin_amdgcn_sched_barrier(0);
     }
   };
 
   // the pipeline: the tile computed, the next one's rows on their way to LDS, the one
   // behind it looking up its pages and the one behind that its list entries
   if (t0 < t1) {
-    auto entry = [&](int t) { return t < t1 ? token_entry(a, r, row, t * kTile + lane) : -1; };
-    int next = entry(t0 + 1);
+    auto place = [&](int t) { return t * kTile + fresh_lane(); };
+    auto entry = [&](int t) { return list_entry(a, r, place(min(t, t1 - 1))); };
     uint64_t mask;
     {
-      const int now = entry(t0);
+      const int now = token_of(a, row, entry(t0), place(t0));
       const int64_t rows = rows_of(now, token_page(a, row, now), mask);
-      if (mask) stage(lds, rows);
+      if (mask) stage((MXIDX_LDS uint8_t*)tile0, rows);
     }
+    int next = token_of(a, row, entry(t0 + 1), place(t0 + 1));
     int page = token_page(a, row, next);
     int far = entry(t0 + 2);
-    for (int t = t0; t < t1; ++t) {
-      const int cur = ((t - t0) & 1) * kTileBytes;
+    // tile t from `cur`, tile t + 1 on its way to `nxt`
+    auto step = [&](int t, MXIDX_LDS uint8_t* cur, MXIDX_LDS uint8_t* nxt) __attribute__((always_inline)) {
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
       __syncthreads();
       uint64_t next_mask = 0;
       if (t + 1 < t1) {
         const int64_t rows = rows_of(next, page, next_mask);
-        if (next_mask) stage(lds + (kTileBytes - cur), rows);
-        next = far;
-        page = token_page(a, row, far);
+        if (next_mask) stage(nxt, rows);
+        next = token_of(a, row, far, place(t + 2));
+        page = token_page(a, row, next);
         far = entry(t + 3);
       }
-      if (mask) compute((MXIDX_LDS const uint8_t*)lds + cur, mask);
+      if (mask) compute(cur, mask);
       mask = next_mask;
+    };
+    for (int t = t0; t < t1; t += 2) {
+      step(t, (MXIDX_LDS uint8_t*)tile0, (MXIDX_LDS uint8_t*)tile1);
+      if (t + 1 < t1) step(t + 1, (MXIDX_LDS uint8_t*)tile1, (MXIDX_LDS uint8_t*)tile0);
     }
   }
 
@@ -356,7 +422,9 @@ __global__ __launch_bounds__(HG * TH * kWave, 1) void attn_kernel(AttnArgs a, Pa
   if constexpr (TH > 1) {
     // the token parts' sums joined in LDS, 16 heads at a time: part th > 0 leaves its
     // own, part 0 takes them
-    float* lo = reinterpret_cast<float*>(lds);
+    auto place = [&](int i) {                          // of the i-th leaving wave
+      return reinterpret_cast<float*>(i < kJoin0 ? tile0 + i * kJoin : tile1 + (i - kJoin0) * kJoin) + 4 * lane;
+    };
 #pragma unroll
     for (int u = 0; u < MT; ++u) {
       const int slot = (th * HG + hg) * MT * 16 + 16 * u + n;
@@ -369,7 +437,7 @@ __global__ __launch_bounds__(HG * TH * kWave, 1) void attn_kernel(AttnArgs a, Pa
     for (int u = 0; u < MT; ++u) {
       __syncthreads();                                 // the last reads are done
       if (th > 0) {
-        float* dst = lo + ((th - 1) * HG + hg) * 16 * kLatent + 4 * lane;
+        float* dst = place((th - 1) * HG + hg);
 #pragma unroll
         for (int v = 0; v < NV; ++v) *reinterpret_cast<v4f*>(dst + v * 256) = o[u][v];
       }
@@ -389,7 +457,7 @@ __global__ __launch_bounds__(HG * TH * kWave, 1) void attn_kernel(AttnArgs a, Pa
         const int slot = (t * HG + hg) * MT * 16 + 16 * u + n;
         f = __builtin_amdgcn_exp2f(join_ml[2 * slot] - ref);
         l[u] += f * join_ml[2 * slot + 1];
-        const float* src = lo + ((t - 1) * HG + hg) * 16 * kLatent + 4 * lane;
+        const float* src = place((t - 1) * HG + hg);
 #pragma unroll
         for (int v = 0; v < NV; ++v) o[u][v] += f * *reinterpret_cast<const v4f*>(src + v * 256);
       }
@@ -430,8 +498,8 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, Parts parts)
   constexpr int W = kLatent / 4;
   const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) / W;
   const int i = threadIdx.x % W;
-  const int64_t r = at / a.H;
-  const int head = (int)(at % a.H);
+  const int64_t r = (uint32_t)at / (uint32_t)a.H;      // rows * H < 2^31
+  const int head = (int)(at - r * a.H);
   Row row;
   if (r >= a.rows || !row_of(a, r, row)) return;
   const int64_t first = r * parts.splits * parts.heads + head;
@@ -481,7 +549,10 @@ int64_t ml_bytes(int64_t rows, const Plan& p) { return align256(rows * p.splits 
 template <int kLatent>
 hipError_t launch(const AttnArgs& a, void* workspace, hipStream_t stream) {
   const Plan p = plan_of(a.rows, a.H, a.indices ? a.k : a.max_tokens);
-  Parts parts{nullptr, nullptr, p.splits, p.heads};
+  const int64_t cache_bytes = a.num_pages * kPage * (kLatent + kRopeWidth) * 2;
+  const bool small = cache_bytes < (1ll << 32);
+  Parts parts{nullptr, nullptr, p.splits, p.heads, (int)(a.num_pages < 0x7fffffff ? a.num_pages : 0x7fffffff),
+              small ? (uint32_t)cache_bytes : 0, small};
   if (p.splits > 1) {
     parts.ml = static_cast<float*>(workspace);
     parts.o = reinterpret_cast<float*>(static_cast<char*>(workspace) + ml_bytes(a.rows, p));
