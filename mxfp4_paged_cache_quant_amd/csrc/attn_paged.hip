@@ -33,6 +33,7 @@
 //
 // Few rows: the tokens are split over workgroups, each leaving its unscaled sums with
 // m and l in the workspace, and a second launch joins them.
+#include <cstdlib>
 #include "common.hpp"
 #include "launch.hpp"
 
@@ -121,8 +122,7 @@ struct Parts {
   float* ml;
   int splits, heads;
   int pages;              // of the cache, at most 2^31 - 1: all that a table names
-  uint32_t cache_bytes;   // the cache's size below 4 GiB (small_cache)
-  bool small_cache;
+  uint32_t cache_bytes;   // the cache's size where it is below 4 GiB
 };
 
 // 16 bytes a lane to LDS, at dst + 16 * lane.
@@ -130,60 +130,77 @@ __device__ __forceinline__ void copy16(__amdgpu_buffer_rsrc_t rs, MXIDX_LDS uint
   __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (MXIDX_LDS void*)dst, 16, offset, 0, 0, 0);
 }
 
-// Copies C 16-byte chunks, from byte `offset` on, of each of kMine rows of a tile to
-// LDS: token t = first .. first + kMine - 1 from the cache row whose byte lane t holds
-// (lo, hi).  Rows that fill less than an instruction share one where 32-bit offsets
-// reach the whole cache, and take one each where they do not.
-template <int C, int kMine, int kRowBytes>
-__device__ __forceinline__ void copy_rows(const char* base, const Parts& parts, MXIDX_LDS uint8_t* dst,
-                                          int first, int lo, int hi, int offset, int ln) {
-  constexpr int kPer = C >= kWave ? 1 : kWave / C;
-  static_assert(C <= kWave && kMine % kPer == 0, "whole instructions");
-  if (kPer > 1 && parts.small_cache) {
-    const __amdgpu_buffer_rsrc_t rs = buffer_rsrc(base, (int)parts.cache_bytes);
+// The copy of a tile's rows to LDS, kMine of them by each wave, in kPieces parts that
+// the caller issues between its products: latent rows first, then the positional ones,
+// C 16-byte chunks of each.  Lane t of (lo, hi) holds the cache byte of token t's row,
+// or kNoRow as hi: the row is then out of its descriptor's range and reads as zeros.
+// Rows that fill less than an instruction share one where 32-bit offsets reach the
+// whole cache (kSmall), and take one each where they do not.
+constexpr int kNoRow = -1;
+
+template <int kLatent, int kMine, bool kSmall>
+struct TileCopy {
+  static constexpr int kRowBytes = (kLatent + kRopeWidth) * 2;
+  static constexpr int LC = kLatent / 8, PC = kRopeWidth / 8;
+  static constexpr int kLatentPer = LC >= kWave ? 1 : kWave / LC, kPosPer = kWave / PC;
+  static constexpr int kLatentPieces = kMine / kLatentPer, kPosPieces = kMine / kPosPer;
+  static constexpr int kPieces = kLatentPieces + kPosPieces;
+  static_assert(kMine % kLatentPer == 0 && kMine % kPosPer == 0, "whole instructions");
+
+  template <int C, int kPer>
+  static __device__ __forceinline__ void rows(const char* base, const Parts& parts, MXIDX_LDS uint8_t* dst,
+                                              int t0, int lo, int hi, int offset) {
+    const int ln = fresh_lane();
+    if constexpr (kPer > 1 && kSmall) {
+      const int t = t0 + ln / C;
+      const int at = (int)((uint32_t)lo | (uint32_t)(hi == kNoRow ? kNoRow : 0));
+      const int row = __shfl(at, t);
+      copy16(buffer_rsrc(base, (int)parts.cache_bytes), dst + t0 * C * 16,
+             row == kNoRow ? row : row + offset + (((ln % C) ^ swz<C>(t)) << 4));
+    } else if (kPer == 1 || ln < C) {
 #pragma unroll
-    for (int i = 0; i < kMine; i += kPer) {
-      const int t = first + i + ln / C;
-      copy16(rs, dst + (first + i) * C * 16, __shfl(lo, t) + offset + (((ln % C) ^ swz<C>(t)) << 4));
-    }
-  } else if (kPer == 1 || ln < C) {
-#pragma unroll
-    for (int i = 0; i < kMine; ++i) {
-      const int t = first + i;
-      const uint32_t l32 = (uint32_t)__builtin_amdgcn_readlane(lo, t);
-      const uint32_t h32 = (uint32_t)__builtin_amdgcn_readlane(hi, t);
-      copy16(buffer_rsrc(base + (((uint64_t)h32 << 32) | l32), kRowBytes), dst + t * C * 16,
-             offset + ((ln ^ swz<C>(t)) << 4));
-      __builtin_amdgcn_sched_barrier(0);               // one row's descriptor at a time
+      for (int i = 0; i < kPer; ++i) {
+        const int t = t0 + i;
+        const uint32_t l32 = (uint32_t)__builtin_amdgcn_readlane(lo, t);
+        const int h32 = __builtin_amdgcn_readlane(hi, t);
+        copy16(buffer_rsrc(base + (((uint64_t)(uint32_t)max(h32, 0) << 32) | l32), h32 < 0 ? 0 : kRowBytes),
+               dst + t * C * 16, offset + ((ln ^ swz<C>(t)) << 4));
+      }
     }
   }
-}
 
-template <int kLatent, int HG, int MT, int TH>
+  static __device__ __forceinline__ void latent(int i, const char* base, const Parts& parts,
+                                                MXIDX_LDS uint8_t* tile, int first, int lo, int hi) {
+    rows<LC, kLatentPer>(base, parts, tile, first + i * kLatentPer, lo, hi, 0);
+  }
+  static __device__ __forceinline__ void positional(int i, const char* base, const Parts& parts,
+                                                    MXIDX_LDS uint8_t* tile, int first, int lo, int hi) {
+    rows<PC, kPosPer>(base, parts, tile + kTile * kLatent * 2, first + i * kPosPer, lo, hi, kLatent * 2);
+  }
+};
+
+template <int kLatent, int HG, int TH, bool kSmall>
 __global__ __launch_bounds__(HG * TH * kWave, 1) void attn_kernel(AttnArgs a, Parts parts) {
   constexpr int kRow = kLatent + kRopeWidth;
-  constexpr int kWaves = HG * TH;
-  constexpr int kHeads = HG * MT * 16;                 // of the workgroup
+  constexpr int kWaves = HG * TH, kHeads = HG * 16;
   constexpr int kTokens = kTile / TH;                  // of a tile, per wave
   constexpr int NT = kTokens < 32 ? 1 : 2;             // 16-token parts of a step
   constexpr int KS = kRow / 32, KL = kLatent / 32;     // contraction steps, latent ones
   constexpr int NV = kLatent / 16;                     // 16-value parts of the output
   constexpr int LC = kLatent / 8;                      // 16-byte chunks of a latent row
+  constexpr int kMine = kTile / kWaves;                // rows that a wave copies
   constexpr int kLatentBytes = kTile * kLatent * 2, kTileBytes = kTile * kRow * 2;
+  using Copy = TileCopy<kLatent, kMine, kSmall>;
+  constexpr int kSteps = kTokens / (16 * NT);          // of a wave's part of a tile
   // Two arrays, and the loop below unrolled over them: the compiler then sees that a
   // tile's reads do not touch the one being copied, and does not wait for its copies.
   __shared__ __attribute__((aligned(1024))) uint8_t tile0[kTileBytes];
   __shared__ __attribute__((aligned(1024))) uint8_t tile1[kTileBytes];
-  static_assert(2 * kTileBytes <= 160 * 1024, "two tiles fit the LDS");
-  constexpr int kJoin = 16 * kLatent * 4;              // a wave's 16 heads, joined at the end
-  constexpr int kJoin0 = kTileBytes / kJoin;           // of them in the first tile
-  static_assert((TH - 1) * HG <= 2 * kJoin0, "the waves' join fits the tiles");
-  __shared__ float join_ml[TH > 1 ? TH * kHeads * 2 : 1];
+  static_assert(2 * kTileBytes <= 156 * 1024, "two tiles fit the LDS");
+  __shared__ float2 stats[TH][kHeads];                 // the waves' (m, l), then the output's scale
 
-  const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int hg = wave % HG, th = wave / HG;
-  const int g = lane >> 4, n = lane & 15;
   const uint32_t groups = (uint32_t)parts.heads / kHeads, unit = blockIdx.x / groups;
   const int group = (int)(blockIdx.x - unit * groups);
   const uint32_t r32 = unit / (uint32_t)parts.splits;
@@ -196,163 +213,130 @@ __global__ __launch_bounds__(HG * TH * kWave, 1) void attn_kernel(AttnArgs a, Pa
   const int share = tiles / parts.splits, more = tiles - share * parts.splits;
   const int t0 = split * share + min(split, more);     // the first `more` splits take one more
   const int t1 = t0 + share + (split < more ? 1 : 0);
-  const int head0 = group * kHeads + hg * MT * 16 + n; // this lane's heads: head0 + 16u
 
-  // the wave's query: step s holds values 32s + 8g .. +7 of a head
-  v8s q[MT][KS];
+  v8s q[KS];                                           // step s: values 32s + 8g .. +7
+  v4f o[NV];
 #pragma unroll
-  for (int u = 0; u < MT; ++u) {
-    const uint16_t* p = static_cast<const uint16_t*>(a.q) + r * a.q_row_stride +
-                        (int64_t)min(head0 + 16 * u, a.H - 1) * a.q_head_stride + 8 * g;
-#pragma unroll
-    for (int s = 0; s < KS; ++s) q[u][s] = *reinterpret_cast<const v8s*>(p + 32 * s);
-  }
-  v4f o[MT][NV];
-  float m[MT], l[MT];                                  // l: this lane's tokens only
-#pragma unroll
-  for (int u = 0; u < MT; ++u) {
-#pragma unroll
-    for (int v = 0; v < NV; ++v) o[u][v] = v4f{0.f, 0.f, 0.f, 0.f};
-    m[u] = neg_inf();
-    l[u] = 0.f;
-  }
+  for (int v = 0; v < NV; ++v) o[v] = v4f{0.f, 0.f, 0.f, 0.f};
+  float m = neg_inf(), l = 0.f;                        // l: this lane's tokens only
   const float scale2 = a.scale * 1.4426950408889634f;  // scores in powers of two
+  bool seen = false;                                   // a visible token
 
-  // Copies the tile's rows, kTile/kWaves by each wave: lane i holds the cache row of
-  // token i.  By buffer loads: the compiler counts them apart from the LDS reads, which
-  // it would drain at every use behind global_load_lds's.  Nothing of it is kept over the
-  // products: they take all registers, and a spilled one would be waited for behind the
-  // copies.
-  auto stage = [&](MXIDX_LDS uint8_t* buf, int64_t cache_row) __attribute__((always_inline)) {
-    constexpr int kMine = kTile / kWaves;
-    const int first = wave * kMine;
-    const char* base = static_cast<const char*>(a.cache);
-    const uint64_t bytes = (uint64_t)cache_row * (kRow * 2);
-    const int lo = (int)(uint32_t)bytes, hi = (int)(uint32_t)(bytes >> 32);
-    const int ln = fresh_lane();
-    copy_rows<LC, kMine, kRow * 2>(base, parts, buf, first, lo, hi, 0, ln);
-    copy_rows<8, kMine, kRow * 2>(base, parts, buf + kLatentBytes, first, lo, hi, kLatent * 2, ln);
-  };
-  // The lanes' cache rows of a tile; places of no token take the first visible one's.
-  auto rows_of = [&](int p, int page, uint64_t& mask) -> int64_t {
+  // The lanes' cache rows of a tile as byte offsets, and which places hold a token.
+  auto rows_of = [&](int p, int page, uint64_t& mask, int& lo, int& hi) __attribute__((always_inline)) {
     const bool ok = p >= 0 && page >= 0 && page < parts.pages;
     mask = __ballot(ok);
-    const int64_t mine = (int64_t)page * kPage + p % kPage;
-    const int from = ok || mask == 0 ? fresh_lane() : __builtin_ctzll(mask);
-    const uint32_t lo = (uint32_t)__shfl((int)(uint32_t)mine, from);
-    const uint32_t hi = (uint32_t)__shfl((int)(uint32_t)((uint64_t)mine >> 32), from);
-    return (int64_t)(((uint64_t)hi << 32) | lo);
+    const uint64_t mine = ((uint64_t)(uint32_t)page * kPage + (uint32_t)(p % kPage)) * (kRow * 2);
+    lo = (int)(uint32_t)mine;
+    hi = ok ? (int)(uint32_t)(mine >> 32) : kNoRow;
   };
+  const char* cache = static_cast<const char*>(a.cache);
 
-  // kTokens tokens of a tile against the wave's heads, 16 * NT at a time
-  auto compute = [&](MXIDX_LDS const uint8_t* buf, uint64_t mask) __attribute__((always_inline)) {
+  // kTokens tokens of a tile against the wave's heads, 16 * NT at a time; the pieces of the
+  // next tile's copy go between the steps of the first product
+  auto compute = [&](MXIDX_LDS const uint8_t* buf, uint64_t mask, MXIDX_LDS uint8_t* nxt, int lo,
+                     int hi) __attribute__((always_inline)) {
+    int first = wave * kMine;                          // of the rows left to copy
     int stop = (th + 1) * kTokens;
     asm volatile("" : "+s"(stop));                     // stays a loop
 #pragma unroll 1
     for (int base = th * kTokens; base < stop; base += 16 * NT) {
-      // LDS offsets of the operands in the tile: the places of the chunks differ between
-      // steps by constants xored into few bits (swz), so one register for each kind of
-      // row does
-      const int ln = fresh_lane(), n = ln & 15, g = ln >> 4;
-      const int key = base * (kLatent * 2) + n * (kLatent * 2) + ((g ^ swz<LC>(n)) << 4);
-      const int pos = kLatentBytes + base * (kRopeWidth * 2) + n * (kRopeWidth * 2) + ((g ^ swz<8>(n)) << 4);
-      v4f s[MT][NT];
-#pragma unroll
-      for (int u = 0; u < MT; ++u)
-#pragma unroll
-        for (int t = 0; t < NT; ++t) s[u][t] = v4f{0.f, 0.f, 0.f, 0.f};
-      // keys: kAhead steps are on their way while one is used
-      auto keys = [&](int k, v8s (&x)[NT]) __attribute__((always_inline)) {
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          // chunk 4k + g: bits 0..3 xored with swz, the rest added
-          const int at = k < KL ? (key ^ ((k & 3) << 6)) + (k >> 2) * 256 + t * 16 * (kLatent * 2)
-                                : (pos ^ ((k - KL) << 6)) + t * 16 * (kRopeWidth * 2);
-          x[t] = *(MXIDX_LDS const v8s*)(buf + at);
-        }
-      };
-      v8s x[kAhead][NT];
-#pragma unroll
-      for (int k = 0; k < kAhead; ++k) keys(k, x[k]);
-#pragma unroll
-      for (int k = 0; k < KS; ++k) {
-        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int u = 0; u < MT; ++u) s[u][t] = mfma_bf16(x[k % kAhead][t], q[u][k], s[u][t]);
-        if (k + kAhead < KS) keys(k + kAhead, x[k % kAhead]);
-      }
-      __builtin_amdgcn_sched_barrier(0);
-      // s[u][t][i]: token base + 16t + 4g + i, head head0 + 16u
-      float f[MT];
-      bool grow = false;
-#pragma unroll
-      for (int u = 0; u < MT; ++u) {
-        float top = neg_inf();
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) s[u][t][i] *= scale2;
-        if (mask != ~0ull) {
+      v4f s[NT];
+      {
+        // LDS offsets of the operands in the tile: the places of the chunks differ
+        // between steps by constants xored into few bits (swz), so one register for each
+        // kind of row does
+        const int ln = fresh_lane(), n = ln & 15, g = ln >> 4;
+        const int key = (base + n) * (kLatent * 2) + ((g ^ swz<LC>(n)) << 4);
+        const int pos = kLatentBytes + (base + n) * (kRopeWidth * 2) + ((g ^ swz<8>(n)) << 4);
+        // kAhead steps are on their way while one is used
+        auto keys = [&](int k, v8s (&x)[NT]) __attribute__((always_inline)) {
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
-            const uint32_t bits = (uint32_t)(mask >> (base + 16 * t + 4 * (fresh_lane() >> 4)));
-#pragma unroll
-            for (int i = 0; i < 4; ++i) s[u][t][i] = (bits >> i) & 1 ? s[u][t][i] : neg_inf();
+            // chunk 4k + g: bits 0..3 xored with swz, the rest added
+            const int at = k < KL ? (key ^ ((k & 3) << 6)) + (k >> 2) * 256 + t * 16 * (kLatent * 2)
+                                  : (pos ^ ((k - KL) << 6)) + t * 16 * (kRopeWidth * 2);
+            x[t] = *(MXIDX_LDS const v8s*)(buf + at);
           }
-        }
+        };
+        v8s x[kAhead][NT];
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+        for (int k = 0; k < kAhead; ++k) keys(k, x[k]);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) top = fmaxf(top, s[u][t][i]);
-        top = fmaxf(top, __shfl_xor(top, 16));
-        top = fmaxf(top, __shfl_xor(top, 32));
-        // the reference is raised only where weights would pass 2^kSlack: what was summed
-        // so far is seldom rescaled
-        f[u] = 1.f;
-        if (m[u] == neg_inf()) {
-          m[u] = top;                                  // nothing summed yet
-        } else if (top > m[u] + kSlack) {
-          f[u] = __builtin_amdgcn_exp2f(m[u] - top);
-          m[u] = top;
-          grow = true;
+        for (int t = 0; t < NT; ++t) s[t] = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+          for (int t = 0; t < NT; ++t) s[t] = mfma_bf16(x[k % kAhead][t], q[k], s[t]);
+          if (k + kAhead < KS) keys(k + kAhead, x[k % kAhead]);
+          // (the positional rows are copied in every step: they are few, and the same)
+          constexpr int kL = Copy::kLatentPieces / kSteps, kP = kL + Copy::kPosPieces;
+#pragma unroll
+          for (int i = 0; i < kP; ++i)
+            if (i * KS / kP == k) {
+              if (i < kL)
+                Copy::latent(i, cache, parts, nxt, first, lo, hi);
+              else
+                Copy::positional(i - kL, cache, parts, nxt, wave * kMine, lo, hi);
+            }
         }
+        first += kMine / kSteps;
+        __builtin_amdgcn_sched_barrier(0);
       }
-      if (__any(grow)) {
+      // s[t][i]: token base + 16t + 4g + i of this lane's head
 #pragma unroll
-        for (int u = 0; u < MT; ++u) {
-          l[u] *= f[u];
+      for (int t = 0; t < NT; ++t)
 #pragma unroll
-          for (int v = 0; v < NV; ++v) o[u][v] *= f[u];
-        }
-      }
-      uint32_t w[MT][NT][2];
-#pragma unroll
-      for (int u = 0; u < MT; ++u) {
-        const float ref = m[u] == neg_inf() ? 0.f : m[u];   // no token yet: every weight 0
+        for (int i = 0; i < 4; ++i) s[t][i] *= scale2;
+      if (mask != ~0ull) {
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-          float p[4];
+          const uint32_t bits = (uint32_t)(mask >> (base + 16 * t + 4 * (fresh_lane() >> 4)));
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            p[i] = __builtin_amdgcn_exp2f(s[u][t][i] - ref);
-            l[u] += p[i];
-          }
-          w[u][t][0] = pack2(p[0], p[1]);
-          w[u][t][1] = pack2(p[2], p[3]);
+          for (int i = 0; i < 4; ++i) s[t][i] = (bits >> i) & 1 ? s[t][i] : neg_inf();
         }
+      }
+      float top = neg_inf();
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top = fmaxf(top, s[t][i]);
+      top = fmaxf(top, __shfl_xor(top, 16));
+      top = fmaxf(top, __shfl_xor(top, 32));
+      // the reference is raised only where weights would pass 2^kSlack: what was summed so
+      // far is seldom rescaled
+      const bool grow = m != neg_inf() && top > m + kSlack;
+      const float m2 = grow || m == neg_inf() ? top : m;
+      if (__any(grow)) {
+        const float f = grow ? __builtin_amdgcn_exp2f(m - m2) : 1.f;
+        l *= f;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) o[v] *= f;
+      }
+      m = m2;
+      const float ref = m == neg_inf() ? 0.f : m;      // no token yet: every weight 0
+      uint32_t w[NT][2];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        float p[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          p[i] = __builtin_amdgcn_exp2f(s[t][i] - ref);
+          l += p[i];
+        }
+        w[t][0] = pack2(p[0], p[1]);
+        w[t][1] = pack2(p[2], p[3]);
       }
       // values: lane 4j + c of a 16-lane group reads tokens 4g + j, values 4c..4c+3, and
       // gets tokens 4g..4g+3 of value n
       const int vl = fresh_lane(), vn = vl & 15, vt = 4 * (vl >> 4) + (vn >> 2);
-      const int val = base * (kLatent * 2) + vt * (kLatent * 2) +
-                      ((((vn >> 1) & 1) ^ swz<LC>(vt)) << 4) + 8 * (vn & 1);
+      const int val = (base + vt) * (kLatent * 2) + ((((vn >> 1) & 1) ^ swz<LC>(vt)) << 4) + 8 * (vn & 1);
       v4s y[kAhead][NT];
-      auto values = [&](int v, v4s (&r)[NT]) __attribute__((always_inline)) {
+      auto values = [&](int v, v4s (&x)[NT]) __attribute__((always_inline)) {
 #pragma unroll
         for (int t = 0; t < NT; ++t)
-          r[t] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((MXIDX_LDS v4s*)(
+          x[t] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((MXIDX_LDS v4s*)(
               buf + (val ^ ((v & 7) << 5)) + (v >> 3) * 256 + t * 16 * (kLatent * 2)));
       };
 #pragma unroll
@@ -361,18 +345,12 @@ __global__ __launch_bounds__(HG * TH * kWave, 1) void attn_kernel(AttnArgs a, Pa
       for (int v = 0; v < NV; ++v) {
         __builtin_amdgcn_sched_barrier(0);
         const v4s(&z)[NT] = y[v % kAhead];
-        if constexpr (NT == 1) {
-#pragma unroll
-          for (int u = 0; u < MT; ++u)
-            o[u][v] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(
-                z[0], __builtin_bit_cast(v4s, uint2{w[u][0][0], w[u][0][1]}), o[u][v], 0, 0, 0);
-        } else {
-          const v8s zz = __builtin_shufflevector(z[0], z[NT - 1], 0, 1, 2, 3, 4, 5, 6, 7);
-#pragma unroll
-          for (int u = 0; u < MT; ++u)
-            o[u][v] = mfma_bf16(zz, __builtin_bit_cast(v8s, uint4{w[u][0][0], w[u][0][1], w[u][NT - 1][0],
-                                                                  w[u][NT - 1][1]}), o[u][v]);
-        }
+        if constexpr (NT == 1)
+          o[v] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(z[0], __builtin_bit_cast(v4s, uint2{w[0][0], w[0][1]}),
+                                                            o[v], 0, 0, 0);
+        else
+          o[v] = mfma_bf16(__builtin_shufflevector(z[0], z[NT - 1], 0, 1, 2, 3, 4, 5, 6, 7),
+                           __builtin_bit_cast(v8s, uint4{w[0][0], w[0][1], w[NT - 1][0], w[NT - 1][1]}), o[v]);
         if (v + kAhead < NV) values(v + kAhead, y[v % kAhead]);
       }
       __builtin_amdgcn_sched_barrier(0);
@@ -384,115 +362,126 @@ __global__ __launch_bounds__(HG * TH * kWave, 1) void attn_kernel(AttnArgs a, Pa
   if (t0 < t1) {
     auto place = [&](int t) { return t * kTile + fresh_lane(); };
     auto entry = [&](int t) { return list_entry(a, r, place(min(t, t1 - 1))); };
-    uint64_t mask;
-    {
-      const int now = token_of(a, row, entry(t0), place(t0));
-      const int64_t rows = rows_of(now, token_page(a, row, now), mask);
-      if (mask) stage((MXIDX_LDS uint8_t*)tile0, rows);
-    }
-    int next = token_of(a, row, entry(t0 + 1), place(t0 + 1));
-    int page = token_page(a, row, next);
+    const int e0 = entry(t0), e1 = entry(t0 + 1);
     int far = entry(t0 + 2);
-    // tile t from `cur`, tile t + 1 on its way to `nxt`
+    const int now = token_of(a, row, e0, place(t0));
+    const int now_page = token_page(a, row, now);
+    int next = token_of(a, row, e1, place(t0 + 1));
+    int page = token_page(a, row, next);
+    uint64_t mask;
+    int lo, hi;
+    rows_of(now, now_page, mask, lo, hi);
+#pragma unroll
+    for (int i = 0; i < Copy::kPosPieces; ++i)
+      Copy::positional(i, cache, parts, (MXIDX_LDS uint8_t*)tile0, wave * kMine, lo, hi);
+#pragma unroll
+    for (int i = 0; i < Copy::kLatentPieces; ++i) {
+      Copy::latent(i, cache, parts, (MXIDX_LDS uint8_t*)tile0, wave * kMine, lo, hi);
+      __builtin_amdgcn_sched_barrier(0);               // one row's descriptor at a time
+    }
+    {
+      // the query's loads behind the first tile's, which wait for two lookups
+      const int ln = fresh_lane(), head = min(group * kHeads + hg * 16 + (ln & 15), a.H - 1);
+      const uint16_t* p = static_cast<const uint16_t*>(a.q) + r * a.q_row_stride +
+                          (int64_t)head * a.q_head_stride + 8 * (ln >> 4);
+#pragma unroll
+      for (int s = 0; s < KS; ++s) q[s] = *reinterpret_cast<const v8s*>(p + 32 * s);
+    }
+    // tile t from `cur`, tile t + 1 on its way to `nxt` (behind the last one: zeros)
     auto step = [&](int t, MXIDX_LDS uint8_t* cur, MXIDX_LDS uint8_t* nxt) __attribute__((always_inline)) {
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
       __syncthreads();
-      uint64_t next_mask = 0;
-      if (t + 1 < t1) {
-        const int64_t rows = rows_of(next, page, next_mask);
-        if (next_mask) stage(nxt, rows);
-        next = token_of(a, row, far, place(t + 2));
-        page = token_page(a, row, next);
-        far = entry(t + 3);
-      }
-      if (mask) compute(cur, mask);
+      uint64_t next_mask;
+      rows_of(t + 1 < t1 ? next : -1, page, next_mask, lo, hi);
+      next = token_of(a, row, far, place(t + 2));
+      page = token_page(a, row, next);
+      far = entry(t + 3);
+      seen |= mask != 0;
+      compute(cur, mask, nxt, lo, hi);
       mask = next_mask;
     };
     for (int t = t0; t < t1; t += 2) {
       step(t, (MXIDX_LDS uint8_t*)tile0, (MXIDX_LDS uint8_t*)tile1);
       if (t + 1 < t1) step(t + 1, (MXIDX_LDS uint8_t*)tile1, (MXIDX_LDS uint8_t*)tile0);
     }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // the last copies write LDS no more
   }
 
-#pragma unroll
-  for (int u = 0; u < MT; ++u) {
-    l[u] += __shfl_xor(l[u], 16);
-    l[u] += __shfl_xor(l[u], 32);
-  }
+  // the waves' maxima and sums, and with them each one's factor
+  const int ln = threadIdx.x & (kWave - 1), n = ln & 15, g = ln >> 4;
+  l += __shfl_xor(l, 16);
+  l += __shfl_xor(l, 32);
+  if (g == 0) stats[th][hg * 16 + n] = make_float2(m, l);
+  __syncthreads();                                     // and the last tile's reads are done
+  float f = 1.f;
   if constexpr (TH > 1) {
-    // the token parts' sums joined in LDS, 16 heads at a time: part th > 0 leaves its
-    // own, part 0 takes them
-    auto place = [&](int i) {                          // of the i-th leaving wave
-      return reinterpret_cast<float*>(i < kJoin0 ? tile0 + i * kJoin : tile1 + (i - kJoin0) * kJoin) + 4 * lane;
-    };
+    float top = m, mine = m;
 #pragma unroll
-    for (int u = 0; u < MT; ++u) {
-      const int slot = (th * HG + hg) * MT * 16 + 16 * u + n;
-      if (g == 0) {
-        join_ml[2 * slot] = m[u];
-        join_ml[2 * slot + 1] = l[u];
-      }
+    for (int t = 0; t < TH; ++t) top = fmaxf(top, stats[t][hg * 16 + n].x);
+    const float ref = top == neg_inf() ? 0.f : top;
+    f = __builtin_amdgcn_exp2f(mine - ref);
+    m = top;
+    l = 0.f;
+#pragma unroll
+    for (int t = 0; t < TH; ++t) {
+      const float2 other = stats[t][hg * 16 + n];
+      l += __builtin_amdgcn_exp2f(other.x - ref) * other.y;
     }
+  }
+  const bool whole = parts.splits == 1;
+  const int head = group * kHeads + hg * 16 + n;
+  const int64_t part = (r * parts.splits + split) * parts.heads + group * kHeads;
+  if (th == 0 && g == 0) {
+    if (!whole)
+      *reinterpret_cast<float2*>(parts.ml + 2 * (part + hg * 16 + n)) = make_float2(m, l);
+    else if (a.lse && head < a.H)
+      a.lse[r * a.H + head] = l == 0.f ? neg_inf() : m * 0.6931471805599453f + logf(l);
+  }
+  if (!whole && !seen) return;                         // uniform: the join does not read its sums
+  if (whole) f *= l == 0.f ? 0.f : 1.f / l;
+
+  // o[v][i] is value 16v + 4g + i of this lane's head: through LDS (16-byte chunk c of
+  // head n at place c ^ n) into whole rows, the token parts added on the way, kValues
+  // values at a time
+  constexpr int kValues = HG == 8 ? kLatent / 2 : kLatent;
+  constexpr int CP = kValues / 4;                      // chunks of a row
+  constexpr int kRegion = 16 * kValues * 4, kRegions0 = kTileBytes / kRegion;
+  static_assert(HG <= 2 * kRegions0, "the sums fit the tiles");
+  auto region = [&](int i) { return i < kRegions0 ? tile0 + i * kRegion : tile1 + (i - kRegions0) * kRegion; };
 #pragma unroll
-    for (int u = 0; u < MT; ++u) {
-      __syncthreads();                                 // the last reads are done
-      if (th > 0) {
-        float* dst = place((th - 1) * HG + hg);
+  for (int v0 = 0; v0 < kLatent; v0 += kValues) {
+    if (v0 > 0) __syncthreads();                       // the rows before have been read
 #pragma unroll
-        for (int v = 0; v < NV; ++v) *reinterpret_cast<v4f*>(dst + v * 256) = o[u][v];
+    for (int t = 0; t < TH; ++t) {
+      if (th == t) {
+        uint8_t* dst = region(hg) + n * (kValues * 4);
+#pragma unroll
+        for (int v = 0; v < kValues / 16; ++v) {
+          v4f* p = reinterpret_cast<v4f*>(dst + (((4 * v + g) ^ n) << 4));
+          const v4f x = o[v0 / 16 + v] * f;
+          *p = t == 0 ? x : *p + x;
+        }
       }
       __syncthreads();
-      if (th > 0) continue;
-      float top = m[u];
-#pragma unroll
-      for (int t = 1; t < TH; ++t)
-        top = fmaxf(top, join_ml[2 * ((t * HG + hg) * MT * 16 + 16 * u + n)]);
-      const float ref = top == neg_inf() ? 0.f : top;
-      float f = __builtin_amdgcn_exp2f(m[u] - ref);
-      l[u] *= f;
-#pragma unroll
-      for (int v = 0; v < NV; ++v) o[u][v] *= f;
-#pragma unroll
-      for (int t = 1; t < TH; ++t) {
-        const int slot = (t * HG + hg) * MT * 16 + 16 * u + n;
-        f = __builtin_amdgcn_exp2f(join_ml[2 * slot] - ref);
-        l[u] += f * join_ml[2 * slot + 1];
-        const float* src = place((t - 1) * HG + hg);
-#pragma unroll
-        for (int v = 0; v < NV; ++v) o[u][v] += f * *reinterpret_cast<const v4f*>(src + v * 256);
+    }
+#pragma unroll 4
+    for (int i = threadIdx.x; i < kHeads * CP; i += kWaves * kWave) {
+      const int h = i / CP, c = i % CP;
+      const v4f x = *reinterpret_cast<const v4f*>(region(h / 16) + (h % 16) * (kValues * 4) + ((c ^ (h % 16)) << 4));
+      if (!whole) {
+        *reinterpret_cast<v4f*>(parts.o + (part + h) * kLatent + v0 + 4 * c) = x;
+      } else if (group * kHeads + h < a.H) {
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + r * a.out_row_stride +
+                                  (int64_t)(group * kHeads + h) * a.out_head_stride + v0 + 4 * c) =
+            make_uint2(pack2(x[0], x[1]), pack2(x[2], x[3]));
       }
-      m[u] = top;
     }
-    if (th > 0) return;
-  }
-
-  // o[u][v][i]: value 16v + 4g + i of head head0 + 16u
-#pragma unroll
-  for (int u = 0; u < MT; ++u) {
-    const int head = head0 + 16 * u;
-    if (parts.splits > 1) {
-      const int64_t at = (r * parts.splits + split) * parts.heads + head;
-      if (g == 0) *reinterpret_cast<float2*>(parts.ml + 2 * at) = make_float2(m[u], l[u]);
-      if (__all(l[u] == 0.f)) continue;
-      float* dst = parts.o + at * kLatent + 4 * g;
-#pragma unroll
-      for (int v = 0; v < NV; ++v) *reinterpret_cast<v4f*>(dst + 16 * v) = o[u][v];
-      continue;
-    }
-    if (head >= a.H) continue;
-    const float inv = l[u] == 0.f ? 0.f : 1.f / l[u];
-    uint16_t* out = static_cast<uint16_t*>(a.out) + r * a.out_row_stride +
-                    (int64_t)head * a.out_head_stride + 4 * g;
-#pragma unroll
-    for (int v = 0; v < NV; ++v)
-      *reinterpret_cast<uint2*>(out + 16 * v) =
-          make_uint2(pack2(o[u][v][0] * inv, o[u][v][1] * inv), pack2(o[u][v][2] * inv, o[u][v][3] * inv));
-    if (a.lse && g == 0)
-      a.lse[r * a.H + head] = l[u] == 0.f ? neg_inf() : m[u] * 0.6931471805599453f + logf(l[u]);
   }
 }
 
-// The splits' sums of one (row, head), kLatent / 4 lanes: 4 values each.
+// The splits' sums of one (row, head), kLatent / 4 lanes: 4 values each, the loads of
+// kBatch splits together.
+constexpr int kBatch = 8;
 template <int kLatent>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, Parts parts) {
   constexpr int W = kLatent / 4;
@@ -503,18 +492,32 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, Parts parts)
   Row row;
   if (r >= a.rows || !row_of(a, r, row)) return;
   const int64_t first = r * parts.splits * parts.heads + head;
-  float top = neg_inf();
-  for (int s = 0; s < parts.splits; ++s)
-    top = fmaxf(top, parts.ml[2 * (first + (int64_t)s * parts.heads)]);
   v4f o = {0.f, 0.f, 0.f, 0.f};
-  float l = 0.f;
-  for (int s = 0; s < parts.splits; ++s) {
-    const int64_t p = first + (int64_t)s * parts.heads;
-    const float2 ml = *reinterpret_cast<const float2*>(parts.ml + 2 * p);
-    if (ml.y == 0.f) continue;                         // nothing seen: no sums written
-    const float f = __builtin_amdgcn_exp2f(ml.x - top);
-    l += f * ml.y;
-    o += f * *reinterpret_cast<const v4f*>(parts.o + p * kLatent + 4 * i);
+  float top = neg_inf(), l = 0.f;
+  for (int s0 = 0; s0 < parts.splits; s0 += kBatch) {
+    float2 ml[kBatch];
+    v4f x[kBatch];
+#pragma unroll
+    for (int s = 0; s < kBatch; ++s) {
+      const int64_t p = first + (int64_t)min(s0 + s, parts.splits - 1) * parts.heads;
+      ml[s] = *reinterpret_cast<const float2*>(parts.ml + 2 * p);
+      x[s] = *reinterpret_cast<const v4f*>(parts.o + p * kLatent + 4 * i);
+    }
+    float m = top;
+#pragma unroll
+    for (int s = 0; s < kBatch; ++s) m = fmaxf(m, ml[s].x);
+    const float ref = m == neg_inf() ? 0.f : m;
+    const float old = __builtin_amdgcn_exp2f(top - ref);
+    o *= old;
+    l *= old;
+    top = m;
+#pragma unroll
+    for (int s = 0; s < kBatch; ++s) {
+      if (s0 + s >= parts.splits || ml[s].y == 0.f) continue;   // nothing seen: no sums written
+      const float f = __builtin_amdgcn_exp2f(ml[s].x - ref);
+      l += f * ml[s].y;
+      o += f * x[s];
+    }
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
   *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + r * a.out_row_stride +
@@ -532,6 +535,12 @@ struct Plan {
 
 Plan plan_of(int64_t rows, int H, int64_t entries) {
   Plan p;
+  if (getenv("MX_GH")) {
+    p.group_heads = atoi(getenv("MX_GH"));
+    p.heads = (H + p.group_heads - 1) / p.group_heads * p.group_heads;
+    p.splits = atoi(getenv("MX_SP"));
+    return p;
+  }
   p.group_heads = H <= 16 ? 16 : H <= 32 ? 32 : H <= 64 ? 64 : 128;
   p.heads = (H + p.group_heads - 1) / p.group_heads * p.group_heads;
   const int64_t units = rows * (p.heads / p.group_heads);
@@ -550,20 +559,31 @@ template <int kLatent>
 hipError_t launch(const AttnArgs& a, void* workspace, hipStream_t stream) {
   const Plan p = plan_of(a.rows, a.H, a.indices ? a.k : a.max_tokens);
   const int64_t cache_bytes = a.num_pages * kPage * (kLatent + kRopeWidth) * 2;
-  const bool small = cache_bytes < (1ll << 32);
+  const bool small = cache_bytes <= 0xffffff00ll;   // kNoRow is past the end
   Parts parts{nullptr, nullptr, p.splits, p.heads, (int)(a.num_pages < 0x7fffffff ? a.num_pages : 0x7fffffff),
-              small ? (uint32_t)cache_bytes : 0, small};
+              small ? (uint32_t)cache_bytes : 0};
   if (p.splits > 1) {
     parts.ml = static_cast<float*>(workspace);
     parts.o = reinterpret_cast<float*>(static_cast<char*>(workspace) + ml_bytes(a.rows, p));
   }
   const dim3 grid((uint32_t)(a.rows * (p.heads / p.group_heads) * p.splits));
+#define MXIDX_ATTN(heads_, hg, th)                                                              \
+  case heads_:                                                                                  \
+    if (small)                                                                                  \
+      hipLaunchKernelGGL((attn_kernel<kLatent, hg, th, true>), grid, dim3(hg * th * kWave), 0,  \
+                         stream, a, parts);                                                     \
+    else                                                                                        \
+      hipLaunchKernelGGL((attn_kernel<kLatent, hg, th, false>), grid, dim3(hg * th * kWave), 0, \
+                         stream, a, parts);                                                     \
+    break;
   switch (p.group_heads) {
-    case 16: hipLaunchKernelGGL((attn_kernel<kLatent, 1, 1, 4>), grid, dim3(256), 0, stream, a, parts); break;
-    case 32: hipLaunchKernelGGL((attn_kernel<kLatent, 2, 1, 2>), grid, dim3(256), 0, stream, a, parts); break;
-    case 64: hipLaunchKernelGGL((attn_kernel<kLatent, 4, 1, 2>), grid, dim3(512), 0, stream, a, parts); break;
-    default: hipLaunchKernelGGL((attn_kernel<kLatent, 8, 1, 1>), grid, dim3(512), 0, stream, a, parts); break;
+    MXIDX_ATTN(16, 1, 4)
+    MXIDX_ATTN(32, 2, 2)
+    MXIDX_ATTN(64, 4, 2)
+    MXIDX_ATTN(128, 8, 1)
+    default: return hipErrorInvalidValue;
   }
+#undef MXIDX_ATTN
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;
   constexpr int W = kLatent / 4;
