@@ -33,7 +33,6 @@
 //
 // Few rows: the tokens are split over workgroups, each leaving its unscaled sums with
 // m and l in the workspace, and a second launch joins them.
-#include <cstdlib>
 #include "common.hpp"
 #include "launch.hpp"
 
@@ -535,12 +534,6 @@ struct Plan {
 
 Plan plan_of(int64_t rows, int H, int64_t entries) {
   Plan p;
-  if (getenv("MX_GH")) {
-    p.group_heads = atoi(getenv("MX_GH"));
-    p.heads = (H + p.group_heads - 1) / p.group_heads * p.group_heads;
-    p.splits = atoi(getenv("MX_SP"));
-    return p;
-  }
   p.group_heads = H <= 16 ? 16 : H <= 32 ? 32 : H <= 64 ? 64 : 128;
   p.heads = (H + p.group_heads - 1) / p.group_heads * p.group_heads;
   const int64_t units = rows * (p.heads / p.group_heads);
