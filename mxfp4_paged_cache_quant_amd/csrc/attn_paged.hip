@@ -70,7 +70,7 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 // halves of the banks, and 8 values over token pairs do.
 template <int kChunks>
 __device__ __forceinline__ int swz(int t) {
-  if constexpr (kChunks >= 16) return ((t & 7) << 1) | ((t >> 3) & 1);
+  if constexpr (kChunks >= 16) return (((t & 7) ^ (((t >> 3) & 1) << 2)) << 1) | ((t >> 3) & 1);
   return (t >> 1) & 7;
 }
 
@@ -121,7 +121,8 @@ struct Parts {
   float* ml;
   int splits, heads;
   int pages;              // of the cache, at most 2^31 - 1: all that a table names
-  uint32_t cache_bytes;   // the cache's size where it is below 4 GiB
+  uint32_t cache_bytes;   // the cache's size where it is below 4 GiB, and of a query row's heads
+  uint32_t q_bytes;
 };
 
 // 16 bytes a lane to LDS, at dst + 16 * lane.
@@ -131,11 +132,13 @@ __device__ __forceinline__ void copy16(__amdgpu_buffer_rsrc_t rs, MXIDX_LDS uint
 
 // The copy of a tile's rows to LDS, kMine of them by each wave, in kPieces parts that
 // the caller issues between its products: latent rows first, then the positional ones,
-// C 16-byte chunks of each.  Lane t of (lo, hi) holds the cache byte of token t's row,
-// or kNoRow as hi: the row is then out of its descriptor's range and reads as zeros.
-// Rows that fill less than an instruction share one where 32-bit offsets reach the
-// whole cache (kSmall), and take one each where they do not.
-constexpr int kNoRow = -1;
+// C 16-byte chunks of each.  Lane t holds the cache byte of token t's row: where 32-bit
+// offsets reach the whole cache (kSmall) as lo, and rows that fill less than an
+// instruction share one; else as (lo, hi), with a descriptor and an instruction for each
+// row.  A place without a row (kNoRow as lo, or as hi) is out of its descriptor's range
+// and reads as zeros.
+constexpr int64_t kReach = 0xfffe0000ll;   // of 32-bit offsets
+constexpr int kNoRow = (int)0xffff0000u;   // past it, no wrap within a row; negative
 
 template <int kLatent, int kMine, bool kSmall>
 struct TileCopy {
@@ -147,15 +150,13 @@ struct TileCopy {
   static_assert(kMine % kLatentPer == 0 && kMine % kPosPer == 0, "whole instructions");
 
   template <int C, int kPer>
-  static __device__ __forceinline__ void rows(const char* base, const Parts& parts, MXIDX_LDS uint8_t* dst,
-                                              int t0, int lo, int hi, int offset) {
-    const int ln = fresh_lane();
-    if constexpr (kPer > 1 && kSmall) {
-      const int t = t0 + ln / C;
-      const int at = (int)((uint32_t)lo | (uint32_t)(hi == kNoRow ? kNoRow : 0));
-      const int row = __shfl(at, t);
-      copy16(buffer_rsrc(base, (int)parts.cache_bytes), dst + t0 * C * 16,
-             row == kNoRow ? row : row + offset + (((ln % C) ^ swz<C>(t)) << 4));
+  static __device__ __forceinline__ void rows(const char* base, uint32_t bytes, MXIDX_LDS uint8_t* dst, int t0,
+                                              int lo, int hi, int offset, int ln) {
+    if constexpr (kSmall) {
+      const __amdgpu_buffer_rsrc_t rs = buffer_rsrc(base, (int)bytes);
+      const int t = t0 + (kPer == 1 ? 0 : ln / C);
+      const int row = kPer == 1 ? __builtin_amdgcn_readlane(lo, t) : __shfl(lo, t);
+      copy16(rs, dst + t0 * C * 16, row + offset + (((ln % C) ^ swz<C>(t)) << 4));
     } else if (kPer == 1 || ln < C) {
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
@@ -164,17 +165,19 @@ struct TileCopy {
         const int h32 = __builtin_amdgcn_readlane(hi, t);
         copy16(buffer_rsrc(base + (((uint64_t)(uint32_t)max(h32, 0) << 32) | l32), h32 < 0 ? 0 : kRowBytes),
                dst + t * C * 16, offset + ((ln ^ swz<C>(t)) << 4));
+        __builtin_amdgcn_sched_barrier(0);             // one row's descriptor at a time
       }
     }
   }
 
-  static __device__ __forceinline__ void latent(int i, const char* base, const Parts& parts,
-                                                MXIDX_LDS uint8_t* tile, int first, int lo, int hi) {
-    rows<LC, kLatentPer>(base, parts, tile, first + i * kLatentPer, lo, hi, 0);
-  }
-  static __device__ __forceinline__ void positional(int i, const char* base, const Parts& parts,
-                                                    MXIDX_LDS uint8_t* tile, int first, int lo, int hi) {
-    rows<PC, kPosPer>(base, parts, tile + kTile * kLatent * 2, first + i * kPosPer, lo, hi, kLatent * 2);
+  // Piece i of the rows from `first` on.
+  static __device__ __forceinline__ void piece(int i, const char* base, uint32_t bytes, MXIDX_LDS uint8_t* tile,
+                                               int first, int lo, int hi, int ln) {
+    if (i < kLatentPieces)
+      rows<LC, kLatentPer>(base, bytes, tile, first + i * kLatentPer, lo, hi, 0, ln);
+    else
+      rows<PC, kPosPer>(base, bytes, tile + kTile * kLatent * 2, first + (i - kLatentPieces) * kPosPer, lo, hi,
+                        kLatent * 2, ln);
   }
 };
 
@@ -226,7 +229,7 @@ __global__ __launch_bounds__(HG * TH * kWave, 1) void attn_kernel(AttnArgs a, Pa
     const bool ok = p >= 0 && page >= 0 && page < parts.pages;
     mask = __ballot(ok);
     const uint64_t mine = ((uint64_t)(uint32_t)page * kPage + (uint32_t)(p % kPage)) * (kRow * 2);
-    lo = (int)(uint32_t)mine;
+    lo = ok || !kSmall ? (int)(uint32_t)mine : kNoRow;
     hi = ok ? (int)(uint32_t)(mine >> 32) : kNoRow;
   };
   const char* cache = static_cast<const char*>(a.cache);
@@ -235,7 +238,10 @@ __global__ __launch_bounds__(HG * TH * kWave, 1) void attn_kernel(AttnArgs a, Pa
   // next tile's copy go between the steps of the first product
   auto compute = [&](MXIDX_LDS const uint8_t* buf, uint64_t mask, MXIDX_LDS uint8_t* nxt, int lo,
                      int hi) __attribute__((always_inline)) {
-    int first = wave * kMine;                          // of the rows left to copy
+    // pieces of the copy in each step: the positional rows are in all of them (they are
+    // few, and the same)
+    constexpr int kL = Copy::kLatentPieces / kSteps, kP = kL + Copy::kPieces - Copy::kLatentPieces;
+    int first = wave * kMine;                          // of the latent rows left to copy
     int stop = (th + 1) * kTokens;
     asm volatile("" : "+s"(stop));                     // stays a loop
 #pragma unroll 1
@@ -269,16 +275,11 @@ __global__ __launch_bounds__(HG * TH * kWave, 1) void attn_kernel(AttnArgs a, Pa
 #pragma unroll
           for (int t = 0; t < NT; ++t) s[t] = mfma_bf16(x[k % kAhead][t], q[k], s[t]);
           if (k + kAhead < KS) keys(k + kAhead, x[k % kAhead]);
-          // (the positional rows are copied in every step: they are few, and the same)
-          constexpr int kL = Copy::kLatentPieces / kSteps, kP = kL + Copy::kPosPieces;
 #pragma unroll
           for (int i = 0; i < kP; ++i)
-            if (i * KS / kP == k) {
-              if (i < kL)
-                Copy::latent(i, cache, parts, nxt, first, lo, hi);
-              else
-                Copy::positional(i - kL, cache, parts, nxt, wave * kMine, lo, hi);
-            }
+            if (i * KS / kP == k)
+              Copy::piece(i < kL ? i : Copy::kLatentPieces + i - kL, cache, parts.cache_bytes, nxt,
+                          i < kL ? first : wave * kMine, lo, hi, ln);
         }
         first += kMine / kSteps;
         __builtin_amdgcn_sched_barrier(0);
@@ -369,22 +370,42 @@ __global__ __launch_bounds__(HG * TH * kWave, 1) void attn_kernel(AttnArgs a, Pa
     int page = token_page(a, row, next);
     uint64_t mask;
     int lo, hi;
-    rows_of(now, now_page, mask, lo, hi);
+    auto copy_all = [&](const char* base, uint32_t bytes, MXIDX_LDS uint8_t* tile) __attribute__((always_inline)) {
+      const int ln = fresh_lane();
 #pragma unroll
-    for (int i = 0; i < Copy::kPosPieces; ++i)
-      Copy::positional(i, cache, parts, (MXIDX_LDS uint8_t*)tile0, wave * kMine, lo, hi);
+      for (int i = 0; i < Copy::kPieces; ++i) Copy::piece(i, base, bytes, tile, wave * kMine, lo, hi, ln);
+    };
+    // the query's rows, as if they were a tile's, to LDS: 64 heads to tile1 behind the
+    // list's and pages' loads, and with 128 heads the others to tile0 before the tile
+    constexpr int kQTiles = (kHeads + kTile - 1) / kTile;
 #pragma unroll
-    for (int i = 0; i < Copy::kLatentPieces; ++i) {
-      Copy::latent(i, cache, parts, (MXIDX_LDS uint8_t*)tile0, wave * kMine, lo, hi);
-      __builtin_amdgcn_sched_barrier(0);               // one row's descriptor at a time
+    for (int i = 0; i < kQTiles; ++i) {
+      const int h = i * kTile + fresh_lane(), head = group * kHeads + h;
+      const uint64_t at = (uint64_t)min(head, a.H - 1) * (uint64_t)a.q_head_stride * 2;
+      const bool ok = h < kHeads && head < a.H;
+      lo = ok || !kSmall ? (int)(uint32_t)at : kNoRow;
+      hi = ok ? (int)(uint32_t)(at >> 32) : kNoRow;
+      copy_all(static_cast<const char*>(a.q) + r * a.q_row_stride * 2, parts.q_bytes,
+               (MXIDX_LDS uint8_t*)(i == 0 ? tile1 : tile0));
     }
+    rows_of(now, now_page, mask, lo, hi);
+    if (kQTiles == 1) copy_all(cache, parts.cache_bytes, (MXIDX_LDS uint8_t*)tile0);
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
     {
-      // the query's loads behind the first tile's, which wait for two lookups
-      const int ln = fresh_lane(), head = min(group * kHeads + hg * 16 + (ln & 15), a.H - 1);
-      const uint16_t* p = static_cast<const uint16_t*>(a.q) + r * a.q_row_stride +
-                          (int64_t)head * a.q_head_stride + 8 * (ln >> 4);
+      const int ln = fresh_lane(), n = ln & 15, g = ln >> 4, h = (hg * 16 + n) % kTile;
+      const int key = h * (kLatent * 2) + ((g ^ swz<LC>(n)) << 4);
+      const int pos = kLatentBytes + h * (kRopeWidth * 2) + ((g ^ swz<8>(n)) << 4);
 #pragma unroll
-      for (int s = 0; s < KS; ++s) q[s] = *reinterpret_cast<const v8s*>(p + 32 * s);
+      for (int k = 0; k < KS; ++k) {
+        const int at = k < KL ? (key ^ ((k & 3) << 6)) + (k >> 2) * 256 : pos ^ ((k - KL) << 6);
+        q[k] = kQTiles > 1 && hg >= kTile / 16 ? *(MXIDX_LDS const v8s*)((MXIDX_LDS uint8_t*)tile0 + at)
+                                               : *(MXIDX_LDS const v8s*)((MXIDX_LDS uint8_t*)tile1 + at);
+      }
+    }
+    if (kQTiles > 1) {
+      __syncthreads();
+      copy_all(cache, parts.cache_bytes, (MXIDX_LDS uint8_t*)tile0);
     }
     // tile t from `cur`, tile t + 1 on its way to `nxt` (behind the last one: zeros)
     auto step = [&](int t, MXIDX_LDS uint8_t* cur, MXIDX_LDS uint8_t* nxt) __attribute__((always_inline)) {
@@ -441,29 +462,35 @@ __global__ __launch_bounds__(HG * TH * kWave, 1) void attn_kernel(AttnArgs a, Pa
 
   // o[v][i] is value 16v + 4g + i of this lane's head: through LDS (16-byte chunk c of
   // head n at place c ^ n) into whole rows, the token parts added on the way, kValues
-  // values at a time
+  // values at a time; each token part begins with a share of its own
   constexpr int kValues = HG == 8 ? kLatent / 2 : kLatent;
   constexpr int CP = kValues / 4;                      // chunks of a row
   constexpr int kRegion = 16 * kValues * 4, kRegions0 = kTileBytes / kRegion;
+  constexpr int NQ = kValues / 16 / TH;                // 16-value parts of a share
   static_assert(HG <= 2 * kRegions0, "the sums fit the tiles");
   auto region = [&](int i) { return i < kRegions0 ? tile0 + i * kRegion : tile1 + (i - kRegions0) * kRegion; };
 #pragma unroll
   for (int v0 = 0; v0 < kLatent; v0 += kValues) {
     if (v0 > 0) __syncthreads();                       // the rows before have been read
+    uint8_t* dst = region(hg) + n * (kValues * 4);
 #pragma unroll
     for (int t = 0; t < TH; ++t) {
-      if (th == t) {
-        uint8_t* dst = region(hg) + n * (kValues * 4);
 #pragma unroll
-        for (int v = 0; v < kValues / 16; ++v) {
-          v4f* p = reinterpret_cast<v4f*>(dst + (((4 * v + g) ^ n) << 4));
-          const v4f x = o[v0 / 16 + v] * f;
-          *p = t == 0 ? x : *p + x;
+      for (int share = 0; share < TH; ++share) {
+        if ((th + t) % TH != share) continue;          // uniform over the wave
+        v4f x[NQ];
+#pragma unroll
+        for (int v = 0; v < NQ; ++v) {
+          x[v] = o[v0 / 16 + share * NQ + v] * f;
+          if (t > 0) x[v] += *reinterpret_cast<const v4f*>(dst + (((4 * (share * NQ + v) + g) ^ n) << 4));
         }
+#pragma unroll
+        for (int v = 0; v < NQ; ++v)
+          *reinterpret_cast<v4f*>(dst + (((4 * (share * NQ + v) + g) ^ n) << 4)) = x[v];
       }
       __syncthreads();
     }
-#pragma unroll 4
+#pragma unroll 8
     for (int i = threadIdx.x; i < kHeads * CP; i += kWaves * kWave) {
       const int h = i / CP, c = i % CP;
       const v4f x = *reinterpret_cast<const v4f*>(region(h / 16) + (h % 16) * (kValues * 4) + ((c ^ (h % 16)) << 4));
@@ -552,9 +579,10 @@ template <int kLatent>
 hipError_t launch(const AttnArgs& a, void* workspace, hipStream_t stream) {
   const Plan p = plan_of(a.rows, a.H, a.indices ? a.k : a.max_tokens);
   const int64_t cache_bytes = a.num_pages * kPage * (kLatent + kRopeWidth) * 2;
-  const bool small = cache_bytes <= 0xffffff00ll;   // kNoRow is past the end
+  const int64_t q_bytes = ((a.H - 1) * a.q_head_stride + kLatent + kRopeWidth) * 2;
+  const bool small = cache_bytes <= kReach && q_bytes <= kReach;
   Parts parts{nullptr, nullptr, p.splits, p.heads, (int)(a.num_pages < 0x7fffffff ? a.num_pages : 0x7fffffff),
-              small ? (uint32_t)cache_bytes : 0};
+              small ? (uint32_t)cache_bytes : 0, small ? (uint32_t)q_bytes : 0};
   if (p.splits > 1) {
     parts.ml = static_cast<float*>(workspace);
     parts.o = reinterpret_cast<float*>(static_cast<char*>(workspace) + ml_bytes(a.rows, p));
