@@ -144,7 +144,8 @@ template <int kLatent, int kMine, bool kSmall>
 struct TileCopy {
   static constexpr int kRowBytes = (kLatent + kRopeWidth) * 2;
   static constexpr int LC = kLatent / 8, PC = kRopeWidth / 8;
-  static constexpr int kLatentPer = LC >= kWave ? 1 : kWave / LC, kPosPer = kWave / PC;
+  static constexpr int kLatentPer = LC >= kWave || !kSmall ? 1 : kWave / LC;
+  static constexpr int kPosPer = kSmall ? kWave / PC : 1;
   static constexpr int kLatentPieces = kMine / kLatentPer, kPosPieces = kMine / kPosPer;
   static constexpr int kPieces = kLatentPieces + kPosPieces;
   static_assert(kMine % kLatentPer == 0 && kMine % kPosPer == 0, "whole instructions");
@@ -157,16 +158,12 @@ struct TileCopy {
       const int t = t0 + (kPer == 1 ? 0 : ln / C);
       const int row = kPer == 1 ? __builtin_amdgcn_readlane(lo, t) : __shfl(lo, t);
       copy16(rs, dst + t0 * C * 16, row + offset + (((ln % C) ^ swz<C>(t)) << 4));
-    } else if (kPer == 1 || ln < C) {
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const int t = t0 + i;
-        const uint32_t l32 = (uint32_t)__builtin_amdgcn_readlane(lo, t);
-        const int h32 = __builtin_amdgcn_readlane(hi, t);
-        copy16(buffer_rsrc(base + (((uint64_t)(uint32_t)max(h32, 0) << 32) | l32), h32 < 0 ? 0 : kRowBytes),
-               dst + t * C * 16, offset + ((ln ^ swz<C>(t)) << 4));
-        __builtin_amdgcn_sched_barrier(0);             // one row's descriptor at a time
-      }
+    } else if (C >= kWave || ln < C) {
+      const uint32_t l32 = (uint32_t)__builtin_amdgcn_readlane(lo, t0);
+      const int h32 = __builtin_amdgcn_readlane(hi, t0);
+      copy16(buffer_rsrc(base + (((uint64_t)(uint32_t)max(h32, 0) << 32) | l32), h32 < 0 ? 0 : kRowBytes),
+             dst + __builtin_amdgcn_readfirstlane(t0 * C * 16),
+             ((ln << 4) ^ __builtin_amdgcn_readfirstlane(swz<C>(t0) << 4)) + offset);
     }
   }
 
