@@ -104,6 +104,7 @@ typedef enum { IDX_BF16 = 0, IDX_F32 = 1 } idx_dtype;
 #define IDX_MAX_DECODE_SEQS 65535
 #define IDX_MERGE_MAX_CANDIDATES 8192
 #define IDX_LATENT_ROPE 64         /* rotated values of a latent row */
+#define IDX_ATTN_MAX_PAGES ((1 << 26) - 1024)   /* row numbers are 32-bit in the kernel */
 
 /* Version of this ABI (major * 100 + minor). */
 int idx_version(void);
@@ -656,7 +657,7 @@ int idx_latent_insert(const void* kv, int dtype, int64_t T, int64_t kv_row_strid
  * over the visible tokens j of row r.  A row that sees none gets out = 0, lse = -inf.
  *   q:   [rows, H, latent + 64] bf16, row (r, h) at q + r*q_row_stride + h*q_head_stride;
  *        strides multiples of 8, 16-byte aligned; 1 <= H <= 128; latent 128, 256 or 512.
- *   cache, num_pages, page_size (64); block_table [B, bt_row_stride] int32 with
+ *   cache, num_pages (up to IDX_ATTN_MAX_PAGES), page_size (64); block_table [B, bt_row_stride] int32 with
  *        bt_row_stride >= ceil(max_tokens / 64).
  *   row_seq: [rows] int32, the row's sequence; NULL: rows is a multiple of B and row r
  *        belongs to sequence r / (rows / B).  Rows whose sequence is outside [0, B) are left

@@ -907,30 +907,35 @@ def _code(table, value, name):
 
 
 def _on(device, t, name, dtype, shape=None):
-    """t: a tensor of that type on that device, contiguous with that shape where one is given."""
-    if not t.is_cuda or t.device != device:
+    """The address of t: a tensor of that type on that device, contiguous with that shape where
+    one is given."""
+    if t.device == device and t.dtype is dtype and \
+            (shape is None or (t.shape == shape and t.is_contiguous())):
+        return t.data_ptr()
+    if t.device != device:
         raise MxidxError(f"{name} must be a device tensor on {device}, got {t.device}")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise MxidxError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and (tuple(t.shape) != shape or not t.is_contiguous()):
-        raise MxidxError(f"{name} must be contiguous of shape {shape}, got {tuple(t.shape)}")
-    return t.data_ptr()
+    raise MxidxError(f"{name} must be contiguous of shape {shape}, got {tuple(t.shape)}")
 
 
 def _call(name, device, stream, *args):
     """One call of the library with `device` current, on `stream` (None: that device's
     current stream)."""
     torch = _torch()
+    index = device.index
     if stream is None:
-        stream = torch.cuda.current_stream(device)
+        raw = torch._C._cuda_getCurrentRawStream(index)
     elif stream.device != device:
         raise MxidxError(f"{name}: the stream belongs to {stream.device}, the tensors to {device}")
+    else:
+        raw = stream.cuda_stream
     fn = getattr(lib(), name)
-    if torch.cuda.current_device() == device.index:
-        status = fn(*args, stream.cuda_stream)
+    if torch._C._cuda_getDevice() == index:
+        status = fn(*args, raw)
     else:
         with torch.cuda.device(device):
-            status = fn(*args, stream.cuda_stream)
+            status = fn(*args, raw)
     if status != 0:
         _check(status, name)
 

@@ -691,7 +691,7 @@ int idx_attn_paged(const void* q, int64_t q_row_stride, int64_t q_head_stride, i
                    float scale, void* out, int64_t out_row_stride, int64_t out_head_stride,
                    float* lse, void* workspace, size_t workspace_bytes, hipStream_t stream) {
   if (!attn_sizes_ok(rows, H, latent, max_tokens) || page_size != IDX_PAGE_SIZE || num_pages < 0 ||
-      num_pages > ((int64_t)1 << 40) || B < 0)
+      num_pages > IDX_ATTN_MAX_PAGES || B < 0)
     return IDX_ERR_ARG;
   if (rows == 0 || B == 0) return IDX_OK;     // no row belongs to a sequence
   const int64_t pages_per_seq = (max_tokens + IDX_PAGE_SIZE - 1) / IDX_PAGE_SIZE;

@@ -8,9 +8,10 @@
 // new maximum scales what was summed so far by 2^(m_old - m_new).
 //
 // Work mapping: one workgroup takes HG * 16 heads of one query row over one share of
-// the row's tokens, 64 tokens (a tile) at a time.  A wave holds 16 heads: their query
-// in registers and their output sums, HG waves the heads and TH waves the tile's
-// token parts.  All products run on the 16x16x32 bf16 MFMA in the transposed form:
+// the row's tokens, 64 tokens (a tile; 32 for many rows) at a time.  A wave holds 16
+// heads: their query in registers and their output sums, HG waves the heads and TH waves
+// the tile's token parts.  All products run on the 16x16x32 bf16 MFMA in the transposed
+// form:
 //   S^T = K Q^T   A = 16 tokens of the tile, B = the wave's 16 heads
 //   O^T = V^T P^T A = 16 of the n values over 32 tokens, B = the weights
 // so a lane holds one head throughout: the weights leave the first product in the
@@ -18,21 +19,31 @@
 // parts), and the running maximum and sum are one register each.
 //
 // A row serves as key and, in its first n values, as value, so each cached row is
-// read once into LDS (two tiles, the next one's loads in flight behind the current
-// one's products).  The copies go straight from the cache rows to LDS in 16-byte
+// read once into LDS (two tiles, the next one's loads between the current one's
+// products).  The copies go straight from the cache rows to LDS in 16-byte
 // chunks; chunk c of token t lands at place c ^ swz(t) of the row, which spreads both
 // the keys' reads (16 tokens, one chunk) and the values' transposing reads (16 tokens,
-// two neighbouring chunks) over all banks.
+// two neighbouring chunks) over all banks.  The query comes the same way, once.
 //
-// Places of a tile that hold no visible token read a visible token's row instead and
-// get weight 0, so nothing that a masked place holds reaches a sum; a tile with no
-// visible token is skipped.
+// What bounds it: with many rows the instruction issue of two waves a SIMD (a step of
+// the second product is an MFMA of 16 cycles, two LDS reads, a wait and an address; 4,700
+// cycles a tile of 64 heads x 64 tokens, of which the MFMAs are 2,176), 854 TFLOP/s at
+// 1024 rows x 2048 tokens x 64 heads where a large library product reaches 1,306; with few
+// rows the way to the first tile (the row's window, its list, its pages, the rows: four
+// round trips) and the partial sums.  32 heads a wave with the tile's weights passed
+// through LDS halves the LDS reads, but not the instructions (8 waves: 482 us; 4 waves
+// of 512 registers: 512 us; where this form took 367).
+//
+// Places of a tile that hold no visible token read as zeros and get weight 0, so
+// nothing that a masked place holds reaches a sum.
 //
 // The weights are rounded to bf16 for the second product (relative error 2^-8 at most,
 // as the cached values' own); l and lse take them unrounded.
 //
 // Few rows: the tokens are split over workgroups, each leaving its unscaled sums with
 // m and l in the workspace, and a second launch joins them.
+#include <algorithm>
+
 #include "common.hpp"
 #include "launch.hpp"
 
@@ -40,9 +51,8 @@ namespace mxidx {
 namespace {
 
 constexpr int kRopeWidth = 64;
-constexpr int kTile = 64;                  // tokens per tile: a lane each
 constexpr int kCus = 256;
-constexpr int kAhead = 3;                  // operand steps in flight from LDS
+constexpr int kMaxSplits = 64;
 constexpr float kSlack = 8.f;               // weights stay below 2^8 of the reference's
 
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
@@ -64,10 +74,13 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 }
 
 // LDS place of a 16-byte chunk: chunk c of token t's row is stored at c ^ swz(t).
-// Latent rows are multiples of 256 bytes, so their banks repeat every 16 chunks and
-// swz runs over 16 values, tokens 0..7 on even ones (a transposing read takes chunk
-// pairs of 8 tokens at a time); the 128-byte positional rows alternate between two
-// halves of the banks, and 8 values over token pairs do.
+// Latent rows are multiples of 256 bytes, so their banks repeat every 16 chunks and swz
+// runs over 16 values; 8-token groups of either kind that one pass of a read takes
+// (0..7 and 8..15 for the transposing reads, which take chunk pairs, {0..3, 12..15} and
+// the like for the 16-byte ones) fall on different places.  Measured: 4.0 cycles a
+// 16-byte and 2.5 a transposing read of a wave, none lost; with the same values in plain
+// order 8.0 and 2.5.  The 128-byte positional rows alternate between two halves of the
+// banks, and 8 values over token pairs do (4.0 cycles).
 template <int kChunks>
 __device__ __forceinline__ int swz(int t) {
   if constexpr (kChunks >= 16) return (((t & 7) ^ (((t >> 3) & 1) << 2)) << 1) | ((t >> 3) & 1);
@@ -120,7 +133,7 @@ struct Parts {
   float* o;
   float* ml;
   int splits, heads;
-  int pages;              // of the cache, at most 2^31 - 1: all that a table names
+  int pages;              // of the cache
   uint32_t cache_bytes;   // the cache's size where it is below 4 GiB, and of a query row's heads
   uint32_t q_bytes;
 };
@@ -132,15 +145,21 @@ __device__ __forceinline__ void copy16(__amdgpu_buffer_rsrc_t rs, MXIDX_LDS uint
 
 // The copy of a tile's rows to LDS, kMine of them by each wave, in kPieces parts that
 // the caller issues between its products: latent rows first, then the positional ones,
-// C 16-byte chunks of each.  Lane t holds the cache byte of token t's row: where 32-bit
-// offsets reach the whole cache (kSmall) as lo, and rows that fill less than an
-// instruction share one; else as (lo, hi), with a descriptor and an instruction for each
-// row.  A place without a row (kNoRow as lo, or as hi) is out of its descriptor's range
-// and reads as zeros.
+// C 16-byte chunks of each.  Lane t of `rows` holds token t's row: where 32-bit offsets
+// reach the whole cache (kSmall) its byte there, and rows that fill less than an
+// instruction share one; else its number (stride bytes each), with a descriptor and an
+// instruction for each row.  A place without a row (kNoRow) is out of its descriptor's
+// range and reads as zeros.
 constexpr int64_t kReach = 0xfffe0000ll;   // of 32-bit offsets
-constexpr int kNoRow = (int)0xffff0000u;   // past it, no wrap within a row; negative
+constexpr int kNoRow = (int)0xffff0000u;   // past it, no wrap within a row
 
-template <int kLatent, int kMine, bool kSmall>
+struct Source {
+  const char* base;
+  uint32_t bytes;         // kSmall: of the whole
+  int64_t stride;         // else: from one row to the next
+};
+
+template <int kLatent, int kTile, int kMine, bool kSmall>
 struct TileCopy {
   static constexpr int kRowBytes = (kLatent + kRopeWidth) * 2;
   static constexpr int LC = kLatent / 8, PC = kRopeWidth / 8;
@@ -151,51 +170,52 @@ struct TileCopy {
   static_assert(kMine % kLatentPer == 0 && kMine % kPosPer == 0, "whole instructions");
 
   template <int C, int kPer>
-  static __device__ __forceinline__ void rows(const char* base, uint32_t bytes, MXIDX_LDS uint8_t* dst, int t0,
-                                              int lo, int hi, int offset, int ln) {
+  static __device__ __forceinline__ void part(const Source& src, MXIDX_LDS uint8_t* dst, int t0, int rows,
+                                              int offset, int ln) {
     if constexpr (kSmall) {
-      const __amdgpu_buffer_rsrc_t rs = buffer_rsrc(base, (int)bytes);
       const int t = t0 + (kPer == 1 ? 0 : ln / C);
-      const int row = kPer == 1 ? __builtin_amdgcn_readlane(lo, t) : __shfl(lo, t);
-      copy16(rs, dst + t0 * C * 16, row + offset + (((ln % C) ^ swz<C>(t)) << 4));
+      const int row = kPer == 1 ? __builtin_amdgcn_readlane(rows, t) : __shfl(rows, t);
+      copy16(buffer_rsrc(src.base, (int)src.bytes), dst + t0 * C * 16,
+             row + offset + (((ln % C) ^ swz<C>(t)) << 4));
     } else if (C >= kWave || ln < C) {
-      const uint32_t l32 = (uint32_t)__builtin_amdgcn_readlane(lo, t0);
-      const int h32 = __builtin_amdgcn_readlane(hi, t0);
-      copy16(buffer_rsrc(base + (((uint64_t)(uint32_t)max(h32, 0) << 32) | l32), h32 < 0 ? 0 : kRowBytes),
-             dst + __builtin_amdgcn_readfirstlane(t0 * C * 16),
-             ((ln << 4) ^ __builtin_amdgcn_readfirstlane(swz<C>(t0) << 4)) + offset);
+      int t = t0;
+      asm volatile("" : "+s"(t));                      // what follows from it is not kept over the loop
+      const int row = __builtin_amdgcn_readlane(rows, t);
+      copy16(buffer_rsrc(src.base + (uint32_t)row * src.stride, row == kNoRow ? 0 : kRowBytes), dst + t * C * 16,
+             ((ln << 4) ^ (swz<C>(t) << 4)) + offset);
     }
   }
 
   // Piece i of the rows from `first` on.
-  static __device__ __forceinline__ void piece(int i, const char* base, uint32_t bytes, MXIDX_LDS uint8_t* tile,
-                                               int first, int lo, int hi, int ln) {
+  static __device__ __forceinline__ void piece(int i, const Source& src, MXIDX_LDS uint8_t* tile, int first,
+                                               int rows, int ln) {
     if (i < kLatentPieces)
-      rows<LC, kLatentPer>(base, bytes, tile, first + i * kLatentPer, lo, hi, 0, ln);
+      part<LC, kLatentPer>(src, tile, first + i * kLatentPer, rows, 0, ln);
     else
-      rows<PC, kPosPer>(base, bytes, tile + kTile * kLatent * 2, first + (i - kLatentPieces) * kPosPer, lo, hi,
-                        kLatent * 2, ln);
+      part<PC, kPosPer>(src, tile + kTile * kLatent * 2, first + (i - kLatentPieces) * kPosPer, rows, kLatent * 2,
+                        ln);
   }
 };
 
-template <int kLatent, int HG, int TH, bool kSmall>
-__global__ __launch_bounds__(HG * TH * kWave, 1) void attn_kernel(AttnArgs a, Parts parts) {
+template <int kLatent, int kTile, int HG, int TH, bool kSmall>
+__global__ __launch_bounds__(HG * TH * kWave, kTile == 32 ? 2 : 1) void attn_kernel(AttnArgs a, Parts parts) {
   constexpr int kRow = kLatent + kRopeWidth;
   constexpr int kWaves = HG * TH, kHeads = HG * 16;
   constexpr int kTokens = kTile / TH;                  // of a tile, per wave
-  constexpr int NT = kTokens < 32 ? 1 : 2;             // 16-token parts of a step
+  constexpr int NT = kTokens / 16;                     // 16-token parts of those
+  static_assert(NT == 1 || NT == 2, "one step of the second product");
   constexpr int KS = kRow / 32, KL = kLatent / 32;     // contraction steps, latent ones
   constexpr int NV = kLatent / 16;                     // 16-value parts of the output
   constexpr int LC = kLatent / 8;                      // 16-byte chunks of a latent row
+  constexpr int kAhead = kSmall ? 3 : 2;               // operand steps in flight from LDS, as registers allow
   constexpr int kMine = kTile / kWaves;                // rows that a wave copies
   constexpr int kLatentBytes = kTile * kLatent * 2, kTileBytes = kTile * kRow * 2;
-  using Copy = TileCopy<kLatent, kMine, kSmall>;
-  constexpr int kSteps = kTokens / (16 * NT);          // of a wave's part of a tile
+  using Copy = TileCopy<kLatent, kTile, kMine, kSmall>;
   // Two arrays, and the loop below unrolled over them: the compiler then sees that a
   // tile's reads do not touch the one being copied, and does not wait for its copies.
   __shared__ __attribute__((aligned(1024))) uint8_t tile0[kTileBytes];
   __shared__ __attribute__((aligned(1024))) uint8_t tile1[kTileBytes];
-  static_assert(2 * kTileBytes <= 156 * 1024, "two tiles fit the LDS");
+  static_assert(kTile <= kWave && 2 * kTileBytes <= 156 * 1024, "a lane for each token; two tiles fit the LDS");
   __shared__ float2 stats[TH][kHeads];                 // the waves' (m, l), then the output's scale
 
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -221,143 +241,136 @@ __global__ __launch_bounds__(HG * TH * kWave, 1) void attn_kernel(AttnArgs a, Pa
   const float scale2 = a.scale * 1.4426950408889634f;  // scores in powers of two
   bool seen = false;                                   // a visible token
 
-  // The lanes' cache rows of a tile as byte offsets, and which places hold a token.
-  auto rows_of = [&](int p, int page, uint64_t& mask, int& lo, int& hi) __attribute__((always_inline)) {
+  // The lanes' cache rows of a tile, and which places hold a token.
+  auto rows_of = [&](int p, int page, uint64_t& mask) __attribute__((always_inline)) {
     const bool ok = p >= 0 && page >= 0 && page < parts.pages;
     mask = __ballot(ok);
-    const uint64_t mine = ((uint64_t)(uint32_t)page * kPage + (uint32_t)(p % kPage)) * (kRow * 2);
-    lo = ok || !kSmall ? (int)(uint32_t)mine : kNoRow;
-    hi = ok ? (int)(uint32_t)(mine >> 32) : kNoRow;
+    const uint32_t row = (uint32_t)page * kPage + (uint32_t)(p % kPage);
+    return ok ? (int)(kSmall ? row * (kRow * 2) : row) : kNoRow;
   };
-  const char* cache = static_cast<const char*>(a.cache);
+  const Source cache{static_cast<const char*>(a.cache), parts.cache_bytes, kRow * 2};
 
-  // kTokens tokens of a tile against the wave's heads, 16 * NT at a time; the pieces of the
-  // next tile's copy go between the steps of the first product
-  auto compute = [&](MXIDX_LDS const uint8_t* buf, uint64_t mask, MXIDX_LDS uint8_t* nxt, int lo,
-                     int hi) __attribute__((always_inline)) {
-    // pieces of the copy in each step: the positional rows are in all of them (they are
-    // few, and the same)
-    constexpr int kL = Copy::kLatentPieces / kSteps, kP = kL + Copy::kPieces - Copy::kLatentPieces;
-    int first = wave * kMine;                          // of the latent rows left to copy
-    int stop = (th + 1) * kTokens;
-    asm volatile("" : "+s"(stop));                     // stays a loop
-#pragma unroll 1
-    for (int base = th * kTokens; base < stop; base += 16 * NT) {
-      v4f s[NT];
-      {
-        // LDS offsets of the operands in the tile: the places of the chunks differ
-        // between steps by constants xored into few bits (swz), so one register for each
-        // kind of row does
-        const int ln = fresh_lane(), n = ln & 15, g = ln >> 4;
-        const int key = (base + n) * (kLatent * 2) + ((g ^ swz<LC>(n)) << 4);
-        const int pos = kLatentBytes + (base + n) * (kRopeWidth * 2) + ((g ^ swz<8>(n)) << 4);
-        // kAhead steps are on their way while one is used
-        auto keys = [&](int k, v8s (&x)[NT]) __attribute__((always_inline)) {
-#pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            // chunk 4k + g: bits 0..3 xored with swz, the rest added
-            const int at = k < KL ? (key ^ ((k & 3) << 6)) + (k >> 2) * 256 + t * 16 * (kLatent * 2)
-                                  : (pos ^ ((k - KL) << 6)) + t * 16 * (kRopeWidth * 2);
-            x[t] = *(MXIDX_LDS const v8s*)(buf + at);
-          }
-        };
-        v8s x[kAhead][NT];
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k) keys(k, x[k]);
-#pragma unroll
-        for (int t = 0; t < NT; ++t) s[t] = v4f{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-          for (int t = 0; t < NT; ++t) s[t] = mfma_bf16(x[k % kAhead][t], q[k], s[t]);
-          if (k + kAhead < KS) keys(k + kAhead, x[k % kAhead]);
-#pragma unroll
-          for (int i = 0; i < kP; ++i)
-            if (i * KS / kP == k)
-              Copy::piece(i < kL ? i : Copy::kLatentPieces + i - kL, cache, parts.cache_bytes, nxt,
-                          i < kL ? first : wave * kMine, lo, hi, ln);
-        }
-        first += kMine / kSteps;
-        __builtin_amdgcn_sched_barrier(0);
-      }
-      // s[t][i]: token base + 16t + 4g + i of this lane's head
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s[t][i] *= scale2;
-      if (mask != ~0ull) {
+  // The wave's kTokens tokens of a tile against its heads; the pieces of the next tile's
+  // copy go between the steps of the first product.
+  auto compute = [&](MXIDX_LDS const uint8_t* buf, uint64_t mask, MXIDX_LDS uint8_t* nxt,
+                     int rows) __attribute__((always_inline)) {
+    const int base = th * kTokens;
+    v4f s[NT];
+    {
+      // LDS offsets of the operands in the tile: the places of the chunks differ
+      // between steps by constants xored into few bits (swz), so one register for each
+      // kind of row does
+      const int ln = fresh_lane(), n = ln & 15, g = ln >> 4;
+      const int key = (base + n) * (kLatent * 2) + ((g ^ swz<LC>(n)) << 4);
+      const int pos = kLatentBytes + (base + n) * (kRopeWidth * 2) + ((g ^ swz<8>(n)) << 4);
+      // kAhead steps are on their way while one is used
+      auto keys = [&](int k, v8s (&x)[NT]) __attribute__((always_inline)) {
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-          const uint32_t bits = (uint32_t)(mask >> (base + 16 * t + 4 * (fresh_lane() >> 4)));
-#pragma unroll
-          for (int i = 0; i < 4; ++i) s[t][i] = (bits >> i) & 1 ? s[t][i] : neg_inf();
+          // chunk 4k + g: bits 0..3 xored with swz, the rest added
+          const int at = k < KL ? (key ^ ((k & 3) << 6)) + (k >> 2) * 256 + t * 16 * (kLatent * 2)
+                                : (pos ^ ((k - KL) << 6)) + t * 16 * (kRopeWidth * 2);
+          x[t] = *(MXIDX_LDS const v8s*)(buf + at);
         }
-      }
-      float top = neg_inf();
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) top = fmaxf(top, s[t][i]);
-      top = fmaxf(top, __shfl_xor(top, 16));
-      top = fmaxf(top, __shfl_xor(top, 32));
-      // the reference is raised only where weights would pass 2^kSlack: what was summed so
-      // far is seldom rescaled
-      const bool grow = m != neg_inf() && top > m + kSlack;
-      const float m2 = grow || m == neg_inf() ? top : m;
-      if (__any(grow)) {
-        const float f = grow ? __builtin_amdgcn_exp2f(m - m2) : 1.f;
-        l *= f;
-#pragma unroll
-        for (int v = 0; v < NV; ++v) o[v] *= f;
-      }
-      m = m2;
-      const float ref = m == neg_inf() ? 0.f : m;      // no token yet: every weight 0
-      uint32_t w[NT][2];
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        float p[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          p[i] = __builtin_amdgcn_exp2f(s[t][i] - ref);
-          l += p[i];
-        }
-        w[t][0] = pack2(p[0], p[1]);
-        w[t][1] = pack2(p[2], p[3]);
-      }
-      // values: lane 4j + c of a 16-lane group reads tokens 4g + j, values 4c..4c+3, and
-      // gets tokens 4g..4g+3 of value n
-      const int vl = fresh_lane(), vn = vl & 15, vt = 4 * (vl >> 4) + (vn >> 2);
-      const int val = (base + vt) * (kLatent * 2) + ((((vn >> 1) & 1) ^ swz<LC>(vt)) << 4) + 8 * (vn & 1);
-      v4s y[kAhead][NT];
-      auto values = [&](int v, v4s (&x)[NT]) __attribute__((always_inline)) {
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-          x[t] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((MXIDX_LDS v4s*)(
-              buf + (val ^ ((v & 7) << 5)) + (v >> 3) * 256 + t * 16 * (kLatent * 2)));
       };
+      v8s x[kAhead][NT];
 #pragma unroll
-      for (int v = 0; v < kAhead; ++v) values(v, y[v]);
+      for (int k = 0; k < kAhead; ++k) keys(k, x[k]);
 #pragma unroll
-      for (int v = 0; v < NV; ++v) {
+      for (int t = 0; t < NT; ++t) s[t] = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
         __builtin_amdgcn_sched_barrier(0);
-        const v4s(&z)[NT] = y[v % kAhead];
-        if constexpr (NT == 1)
-          o[v] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(z[0], __builtin_bit_cast(v4s, uint2{w[0][0], w[0][1]}),
-                                                            o[v], 0, 0, 0);
-        else
-          o[v] = mfma_bf16(__builtin_shufflevector(z[0], z[NT - 1], 0, 1, 2, 3, 4, 5, 6, 7),
-                           __builtin_bit_cast(v8s, uint4{w[0][0], w[0][1], w[NT - 1][0], w[NT - 1][1]}), o[v]);
-        if (v + kAhead < NV) values(v + kAhead, y[v % kAhead]);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) s[t] = mfma_bf16(x[k % kAhead][t], q[k], s[t]);
+        if (k + kAhead < KS) keys(k + kAhead, x[k % kAhead]);
+#pragma unroll
+        for (int i = 0; i < Copy::kPieces; ++i)
+          if (i * KS / Copy::kPieces == k)
+            Copy::piece(i, cache, nxt, wave * kMine, rows, ln);
       }
       __builtin_amdgcn_sched_barrier(0);
     }
+    // s[t][i]: token base + 16t + 4g + i of this lane's head
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[t][i] *= scale2;
+    if (mask != (kTile == 64 ? ~0ull : (1ull << (kTile % 64)) - 1)) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const uint32_t bits = (uint32_t)(mask >> (base + 16 * t + 4 * (fresh_lane() >> 4)));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[t][i] = (bits >> i) & 1 ? s[t][i] : neg_inf();
+      }
+    }
+    float top = neg_inf();
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) top = fmaxf(top, s[t][i]);
+    top = fmaxf(top, __shfl_xor(top, 16));
+    top = fmaxf(top, __shfl_xor(top, 32));
+    // the reference is raised only where weights would pass 2^kSlack: what was summed so
+    // far is seldom rescaled
+    const bool grow = m != neg_inf() && top > m + kSlack;
+    const float m2 = grow || m == neg_inf() ? top : m;
+    if (__any(grow)) {
+      const float f = grow ? __builtin_amdgcn_exp2f(m - m2) : 1.f;
+      l *= f;
+#pragma unroll
+      for (int v = 0; v < NV; ++v) o[v] *= f;
+    }
+    m = m2;
+    const float ref = m == neg_inf() ? 0.f : m;      // no token yet: every weight 0
+    uint32_t w[NT][2];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      float p[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        p[i] = __builtin_amdgcn_exp2f(s[t][i] - ref);
+        l += p[i];
+      }
+      w[t][0] = pack2(p[0], p[1]);
+      w[t][1] = pack2(p[2], p[3]);
+    }
+    // values: lane 4j + c of a 16-lane group reads tokens 4g + j, values 4c..4c+3, and
+    // gets tokens 4g..4g+3 of value n
+    const int vl = fresh_lane(), vn = vl & 15, vt = 4 * (vl >> 4) + (vn >> 2);
+    const int val = (base + vt) * (kLatent * 2) + ((((vn >> 1) & 1) ^ swz<LC>(vt)) << 4) + 8 * (vn & 1);
+    v4s y[kAhead][NT];
+    auto values = [&](int v, v4s (&x)[NT]) __attribute__((always_inline)) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+        x[t] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((MXIDX_LDS v4s*)(
+            buf + (val ^ ((v & 7) << 5)) + (v >> 3) * 256 + t * 16 * (kLatent * 2)));
+    };
+#pragma unroll
+    for (int v = 0; v < kAhead; ++v) values(v, y[v]);
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      __builtin_amdgcn_sched_barrier(0);
+      const v4s(&z)[NT] = y[v % kAhead];
+      if constexpr (NT == 1)
+        o[v] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(z[0], __builtin_bit_cast(v4s, uint2{w[0][0], w[0][1]}),
+                                                          o[v], 0, 0, 0);
+      else
+        o[v] = mfma_bf16(__builtin_shufflevector(z[0], z[NT - 1], 0, 1, 2, 3, 4, 5, 6, 7),
+                         __builtin_bit_cast(v8s, uint4{w[0][0], w[0][1], w[NT - 1][0], w[NT - 1][1]}), o[v]);
+      if (v + kAhead < NV) values(v + kAhead, y[v % kAhead]);
+    }
+    __builtin_amdgcn_sched_barrier(0);
   };
 
   // the pipeline: the tile computed, the next one's rows on their way to LDS, the one
   // behind it looking up its pages and the one behind that its list entries
   if (t0 < t1) {
-    auto place = [&](int t) { return t * kTile + fresh_lane(); };
+    // a place past the list for lanes without a token
+    auto place = [&](int t) {
+      const int ln = fresh_lane();
+      return kTile == kWave || ln < kTile ? t * kTile + ln : 0x7fffffff;
+    };
     auto entry = [&](int t) { return list_entry(a, r, place(min(t, t1 - 1))); };
     const int e0 = entry(t0), e1 = entry(t0 + 1);
     int far = entry(t0 + 2);
@@ -366,11 +379,10 @@ __global__ __launch_bounds__(HG * TH * kWave, 1) void attn_kernel(AttnArgs a, Pa
     int next = token_of(a, row, e1, place(t0 + 1));
     int page = token_page(a, row, next);
     uint64_t mask;
-    int lo, hi;
-    auto copy_all = [&](const char* base, uint32_t bytes, MXIDX_LDS uint8_t* tile) __attribute__((always_inline)) {
+    auto copy_all = [&](const Source& src, MXIDX_LDS uint8_t* tile, int rows) __attribute__((always_inline)) {
       const int ln = fresh_lane();
 #pragma unroll
-      for (int i = 0; i < Copy::kPieces; ++i) Copy::piece(i, base, bytes, tile, wave * kMine, lo, hi, ln);
+      for (int i = 0; i < Copy::kPieces; ++i) Copy::piece(i, src, tile, wave * kMine, rows, ln);
     };
     // the query's rows, as if they were a tile's, to LDS: 64 heads to tile1 behind the
     // list's and pages' loads, and with 128 heads the others to tile0 before the tile
@@ -378,15 +390,12 @@ __global__ __launch_bounds__(HG * TH * kWave, 1) void attn_kernel(AttnArgs a, Pa
 #pragma unroll
     for (int i = 0; i < kQTiles; ++i) {
       const int h = i * kTile + fresh_lane(), head = group * kHeads + h;
-      const uint64_t at = (uint64_t)min(head, a.H - 1) * (uint64_t)a.q_head_stride * 2;
-      const bool ok = h < kHeads && head < a.H;
-      lo = ok || !kSmall ? (int)(uint32_t)at : kNoRow;
-      hi = ok ? (int)(uint32_t)(at >> 32) : kNoRow;
-      copy_all(static_cast<const char*>(a.q) + r * a.q_row_stride * 2, parts.q_bytes,
-               (MXIDX_LDS uint8_t*)(i == 0 ? tile1 : tile0));
+      const uint32_t at = kSmall ? (uint32_t)head * (uint32_t)(a.q_head_stride * 2) : (uint32_t)head;
+      copy_all(Source{static_cast<const char*>(a.q) + r * a.q_row_stride * 2, parts.q_bytes, a.q_head_stride * 2},
+               (MXIDX_LDS uint8_t*)(i == 0 ? tile1 : tile0), h < kHeads && head < a.H ? (int)at : kNoRow);
     }
-    rows_of(now, now_page, mask, lo, hi);
-    if (kQTiles == 1) copy_all(cache, parts.cache_bytes, (MXIDX_LDS uint8_t*)tile0);
+    const int first_rows = rows_of(now, now_page, mask);
+    if (kQTiles == 1) copy_all(cache, (MXIDX_LDS uint8_t*)tile0, first_rows);
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
     {
@@ -402,19 +411,19 @@ __global__ __launch_bounds__(HG * TH * kWave, 1) void attn_kernel(AttnArgs a, Pa
     }
     if (kQTiles > 1) {
       __syncthreads();
-      copy_all(cache, parts.cache_bytes, (MXIDX_LDS uint8_t*)tile0);
+      copy_all(cache, (MXIDX_LDS uint8_t*)tile0, first_rows);
     }
     // tile t from `cur`, tile t + 1 on its way to `nxt` (behind the last one: zeros)
     auto step = [&](int t, MXIDX_LDS uint8_t* cur, MXIDX_LDS uint8_t* nxt) __attribute__((always_inline)) {
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
       __syncthreads();
       uint64_t next_mask;
-      rows_of(t + 1 < t1 ? next : -1, page, next_mask, lo, hi);
+      const int rows = rows_of(t + 1 < t1 ? next : -1, page, next_mask);
       next = token_of(a, row, far, place(t + 2));
       page = token_page(a, row, next);
       far = entry(t + 3);
       seen |= mask != 0;
-      compute(cur, mask, nxt, lo, hi);
+      compute(cur, mask, nxt, rows);
       mask = next_mask;
     };
     for (int t = t0; t < t1; t += 2) {
@@ -460,7 +469,7 @@ __global__ __launch_bounds__(HG * TH * kWave, 1) void attn_kernel(AttnArgs a, Pa
   // o[v][i] is value 16v + 4g + i of this lane's head: through LDS (16-byte chunk c of
   // head n at place c ^ n) into whole rows, the token parts added on the way, kValues
   // values at a time; each token part begins with a share of its own
-  constexpr int kValues = HG == 8 ? kLatent / 2 : kLatent;
+  constexpr int kValues = HG <= 2 * (kTileBytes / (kLatent * 64)) ? kLatent : kLatent / 2;
   constexpr int CP = kValues / 4;                      // chunks of a row
   constexpr int kRegion = 16 * kValues * 4, kRegions0 = kTileBytes / kRegion;
   constexpr int NQ = kValues / 16 / TH;                // 16-value parts of a share
@@ -552,19 +561,32 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, Parts parts)
 
 struct Plan {
   int group_heads;        // heads of a workgroup
+  int tile;               // tokens at a time
   int heads;              // H rounded up to whole groups
   int splits;
 };
 
+// Few rows are split over the tokens, up to one workgroup for each CU.  A split costs its
+// share of the workspace's traffic (2 KB a head, written and read), so it takes 4 tiles
+// or more (16 rows of 2048 tokens, 64 heads: 27.4 us with 8 splits, 29.6 with 16), or 2
+// where even 64 workgroups do not come together (one such row: 15.5 us with 16 splits of
+// 32 heads); and the join of a row reads them one after the other (one row of 32768
+// tokens: 36 us with 64 splits, 43 with 128).
+// 64 heads a workgroup read the rows fewest times (32 rows of 2 x 6600 tokens, 128
+// heads: 99 us with 64, 168 with 32); 32 heads spread a call over twice the CUs that
+// would not fill them otherwise (one row: 15.5 us, 19.1 with 64; 16 rows: 27.3 and 27.4).
+// Many rows: two workgroups of four waves a CU, 32 tokens at a time, whose phases do not
+// fall together (1024 rows of 2048 tokens, 64 heads: 330-346 us, 355-363 with one of
+// eight waves); with 200 rows, which do not fill both places, 136 us and 119.
 Plan plan_of(int64_t rows, int H, int64_t entries) {
   Plan p;
-  p.group_heads = H <= 16 ? 16 : H <= 32 ? 32 : H <= 64 ? 64 : 128;
+  const int64_t tiles = (entries + 63) / 64, quarter = std::min<int64_t>((tiles + 3) / 4, kMaxSplits);
+  p.group_heads = H <= 16 ? 16 : H <= 32 || rows * ((H + 31) / 32) * quarter <= kCus ? 32 : 64;
   p.heads = (H + p.group_heads - 1) / p.group_heads * p.group_heads;
   const int64_t units = rows * (p.heads / p.group_heads);
-  const int64_t tiles = (entries + kTile - 1) / kTile;
-  int64_t s = units > 0 ? kCus / units : 1;
-  s = s < tiles ? s : tiles;
-  p.splits = (int)(s > 1 ? s : 1);
+  p.tile = p.group_heads == 64 && units >= 2 * kCus ? 32 : 64;
+  const int64_t shares = units * quarter <= 64 ? std::min<int64_t>((tiles + 1) / 2, kMaxSplits) : quarter;
+  p.splits = (int)std::max<int64_t>(1, std::min(kCus / std::max<int64_t>(units, 1), shares));
   return p;
 }
 
@@ -578,27 +600,27 @@ hipError_t launch(const AttnArgs& a, void* workspace, hipStream_t stream) {
   const int64_t cache_bytes = a.num_pages * kPage * (kLatent + kRopeWidth) * 2;
   const int64_t q_bytes = ((a.H - 1) * a.q_head_stride + kLatent + kRopeWidth) * 2;
   const bool small = cache_bytes <= kReach && q_bytes <= kReach;
-  Parts parts{nullptr, nullptr, p.splits, p.heads, (int)(a.num_pages < 0x7fffffff ? a.num_pages : 0x7fffffff),
+  Parts parts{nullptr, nullptr, p.splits, p.heads, (int)a.num_pages,
               small ? (uint32_t)cache_bytes : 0, small ? (uint32_t)q_bytes : 0};
   if (p.splits > 1) {
     parts.ml = static_cast<float*>(workspace);
     parts.o = reinterpret_cast<float*>(static_cast<char*>(workspace) + ml_bytes(a.rows, p));
   }
   const dim3 grid((uint32_t)(a.rows * (p.heads / p.group_heads) * p.splits));
-#define MXIDX_ATTN(heads_, hg, th)                                                              \
-  case heads_:                                                                                  \
-    if (small)                                                                                  \
-      hipLaunchKernelGGL((attn_kernel<kLatent, hg, th, true>), grid, dim3(hg * th * kWave), 0,  \
-                         stream, a, parts);                                                     \
-    else                                                                                        \
-      hipLaunchKernelGGL((attn_kernel<kLatent, hg, th, false>), grid, dim3(hg * th * kWave), 0, \
-                         stream, a, parts);                                                     \
+#define MXIDX_ATTN(heads_, tile_, hg, th)                                                     \
+  case heads_ * 64 + tile_:                                                                   \
+    if (small)                                                                               \
+      hipLaunchKernelGGL((attn_kernel<kLatent, tile_, hg, th, true>), grid,                  \
+                         dim3(hg * th * kWave), 0, stream, a, parts);                        \
+    else                                                                                     \
+      hipLaunchKernelGGL((attn_kernel<kLatent, tile_, hg, th, false>), grid,                 \
+                         dim3(hg * th * kWave), 0, stream, a, parts);                        \
     break;
-  switch (p.group_heads) {
-    MXIDX_ATTN(16, 1, 4)
-    MXIDX_ATTN(32, 2, 2)
-    MXIDX_ATTN(64, 4, 2)
-    MXIDX_ATTN(128, 8, 1)
+  switch (p.group_heads * 64 + p.tile) {
+    MXIDX_ATTN(16, 64, 1, 4)
+    MXIDX_ATTN(32, 64, 2, 2)
+    MXIDX_ATTN(64, 64, 4, 2)
+    MXIDX_ATTN(64, 32, 4, 1)
     default: return hipErrorInvalidValue;
   }
 #undef MXIDX_ATTN
