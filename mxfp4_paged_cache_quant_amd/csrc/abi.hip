@@ -625,6 +625,7 @@ int idx_norm_rope(const idx_heads* q, const idx_heads* k, int dtype, int64_t T,
   const int64_t heads = (int64_t)(q ? q->heads : 0) + (k ? k->heads : 0);
   if (heads > (1 << 20)) return IDX_ERR_ARG;
   if (T == 0 || heads == 0) return IDX_OK;
+  if (T > ((int64_t)1 << 27) / heads) return IDX_ERR_ARG;   // the grid: 16 lanes a row
   if (rope->rope_dim > 0 && !rope->positions && rope->table_rows < T) return IDX_ERR_ARG;
   if ((st = gate_current()) != IDX_OK) return st;
   return launched(mxidx::launch_norm_rope(heads_spec(q), heads_spec(k), dtype == IDX_F32, T,
@@ -647,7 +648,7 @@ int idx_latent_insert(const void* kv, int dtype, int64_t T, int64_t kv_row_strid
       num_pages > ((int64_t)1 << 40) || T < 0 || H < 0)
     return IDX_ERR_ARG;
   // the grid is one workgroup for 4 tokens and one for 32 query rows
-  if (T > (1 << 28) || (q_pe && T * H > ((int64_t)1 << 30))) return IDX_ERR_ARG;
+  if (T > (1 << 28) || (q_pe && T * H > ((int64_t)1 << 28))) return IDX_ERR_ARG;
   if (norm != IDX_NORM_NONE && norm != IDX_NORM_RMS) return IDX_ERR_ARG;
   if (T == 0) return IDX_OK;
   const int al = dtype == IDX_BF16 ? 8 : 4;
