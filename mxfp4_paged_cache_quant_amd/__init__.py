@@ -179,9 +179,15 @@ def init(device=0):
 # torch-facing wrappers (torch supplies device memory and the stream only)
 # ---------------------------------------------------------------------------
 
+_TORCH = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _TORCH
+    if _TORCH is None:
+        import torch
+        _TORCH = torch
+    return _TORCH
 
 
 def _stream(stream):
@@ -1028,29 +1034,27 @@ def step_map(seq_lens, query_lens, block_table, num_rows, free_pages=None, free_
 
 def _heads_block(device, stream, x, out, norm, weight, bias, eps, name, tokens, dtype):
     """(idx_heads block, out) of x [T, H, 128] or [T, 128]."""
-    torch = _torch()
-    _on(device, x, name, dtype)
-    if x.dim() not in (2, 3) or x.shape[-1] != HEAD_DIM or x.shape[0] != tokens:
+    shape, strides = x.shape, x.stride()
+    xp = _on(device, x, name, dtype)
+    if len(shape) not in (2, 3) or shape[-1] != HEAD_DIM or shape[0] != tokens:
         raise MxidxError(f"{name} must be [{tokens}, H, {HEAD_DIM}] or [{tokens}, {HEAD_DIM}]")
     if out is None:
-        out = _empty(stream, x.shape, dtype, device)
-    _on(device, out, f"{name}_out", dtype)
-    if out.shape != x.shape:
+        out = _empty(stream, shape, dtype, device)
+    op = _on(device, out, f"{name}_out", dtype)
+    if out.shape != shape:
         raise MxidxError(f"{name}_out must have {name}'s shape")
-    heads = x.shape[1] if x.dim() == 3 else 1
+    out_strides = out.stride()
+    heads = shape[1] if len(shape) == 3 else 1
     if tokens and heads:
-        if x.stride(-1) != 1 or out.stride(-1) != 1:
+        if strides[-1] != 1 or out_strides[-1] != 1:
             raise MxidxError(f"{name} and {name}_out must have a contiguous last dim")
-        if out.data_ptr() == x.data_ptr() and out.stride() != x.stride():
+        if op == xp and out_strides != strides:
             raise MxidxError(f"{name}_out may be {name} itself only with the same strides")
-    params = []
-    for what, p in (("weight", weight), ("bias", bias)):
-        params.append(None if p is None else
-                      _on(device, p, f"{name}_{what}", torch.float32, (HEAD_DIM,)))
-    xh = x.stride(1) if x.dim() == 3 else HEAD_DIM
-    oh = out.stride(1) if x.dim() == 3 else HEAD_DIM
-    return _Heads(x.data_ptr(), out.data_ptr(), x.stride(0), xh, out.stride(0), oh, heads,
-                  _code(_NORMS, norm, f"{name}_norm"), params[0], params[1], eps), out
+    wp = None if weight is None else _on(device, weight, f"{name}_weight", _torch().float32, (HEAD_DIM,))
+    bp = None if bias is None else _on(device, bias, f"{name}_bias", _torch().float32, (HEAD_DIM,))
+    return _Heads(xp, op, strides[0], strides[1] if len(shape) == 3 else HEAD_DIM, out_strides[0],
+                  out_strides[1] if len(shape) == 3 else HEAD_DIM, heads,
+                  _code(_NORMS, norm, f"{name}_norm"), wp, bp, eps), out
 
 
 def norm_rope(q, k, cos, sin, rope_dim, mode="neox", positions=None, q_norm="none", q_weight=None,
