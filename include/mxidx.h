@@ -105,6 +105,7 @@ typedef enum { IDX_BF16 = 0, IDX_F32 = 1 } idx_dtype;
 #define IDX_MERGE_MAX_CANDIDATES 8192
 #define IDX_LATENT_ROPE 64         /* rotated values of a latent row */
 #define IDX_ATTN_MAX_PAGES ((1 << 26) - 1024)   /* row numbers are 32-bit in the kernel */
+#define IDX_ATTN_MAX_ROWS (1 << 22)              /* and a launch has fewer than 2^32 lanes */
 
 /* Version of this ABI (major * 100 + minor). */
 int idx_version(void);
@@ -620,7 +621,7 @@ typedef struct {
  *     strides multiples of 8 (bf16) or 4 (fp32), head strides >= 128 where heads
  *     > 1.  out may be x itself with the same strides; any other overlap, also of
  *     q's and k's rows with each other's output, is not allowed.
- *   rope: required (rope_dim 0 rotates nothing). */
+ *   rope: required (rope_dim 0 rotates nothing).  T * (q's and k's heads) <= 2^27. */
 int idx_norm_rope(const idx_heads* q, const idx_heads* k, int dtype, int64_t T,
                   const idx_rope* rope, hipStream_t stream);
 
@@ -642,7 +643,8 @@ int idx_norm_rope(const idx_heads* q, const idx_heads* k, int dtype, int64_t T,
  *     t*out_row_stride + h*out_head_stride (values 64): with q_out = q + latent the tail
  *     of idx_attn_paged's query rows.  Rows of tokens without a slot are written too.
  *   kv, q_pe and q_out 16-byte aligned, strides multiples of 8 (bf16) or 4 (fp32 inputs);
- *   cache 16-byte aligned; page_size must be 64.  No output may overlap an input. */
+ *   cache 16-byte aligned; page_size must be 64.  No output may overlap an input.
+ *   T <= 2^24 and T * H <= 2^28. */
 int idx_latent_insert(const void* kv, int dtype, int64_t T, int64_t kv_row_stride, int latent,
                       int norm, const float* weight, float eps, const idx_rope* rope,
                       const int64_t* slot_mapping, void* cache, int64_t num_pages, int page_size,
@@ -671,7 +673,7 @@ int idx_latent_insert(const void* kv, int dtype, int64_t T, int64_t kv_row_strid
  *   max_tokens: host-side upper bound of ke - ks: later tokens are not read.  Tokens whose
  *        page lies outside the cache are skipped.
  *   out: [rows, H, latent] bf16, strides multiples of 4, 8-byte aligned; lse: [rows, H]
- *        fp32 or NULL.
+ *        fp32 or NULL.  rows <= IDX_ATTN_MAX_ROWS.
  *   workspace: device memory of at least idx_attn_workspace_bytes(rows, H, latent, k with
  *        indices, else max_tokens) bytes, 256-byte aligned, as for idx_topk_ws: no
  *        initialization, scratch after the call, not shared by calls that may run at the

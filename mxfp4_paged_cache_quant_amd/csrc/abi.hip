@@ -647,8 +647,8 @@ int idx_latent_insert(const void* kv, int dtype, int64_t T, int64_t kv_row_strid
   if (!latent_ok(latent) || page_size != IDX_PAGE_SIZE || num_pages < 0 ||
       num_pages > ((int64_t)1 << 40) || T < 0 || H < 0)
     return IDX_ERR_ARG;
-  // the grid is one workgroup for 4 tokens and one for 32 query rows
-  if (T > (1 << 28) || (q_pe && T * H > ((int64_t)1 << 28))) return IDX_ERR_ARG;
+  // the grid is a wave a token and 8 lanes a query row, and a launch has fewer than 2^32 lanes
+  if (T > (1 << 24) || (q_pe && T * H > ((int64_t)1 << 28))) return IDX_ERR_ARG;
   if (norm != IDX_NORM_NONE && norm != IDX_NORM_RMS) return IDX_ERR_ARG;
   if (T == 0) return IDX_OK;
   const int al = dtype == IDX_BF16 ? 8 : 4;
@@ -673,9 +673,10 @@ int idx_latent_insert(const void* kv, int dtype, int64_t T, int64_t kv_row_strid
   return launched(mxidx::launch_latent_insert(a, dtype == IDX_F32, latent, rope_spec(rope), stream));
 }
 
-// What the two calls below share: sizes that the kernels' grid and indexes take.
+// What the two calls below share: sizes that the kernels' grid and indexes take.  A row takes
+// two workgroups of 256 lanes at most where rows are many, and a launch has fewer than 2^32.
 static bool attn_sizes_ok(int64_t rows, int H, int latent, int64_t max_tokens) {
-  return rows >= 0 && H >= 1 && H <= IDX_MAX_HEADS && rows <= 0x7fffffffLL / IDX_MAX_HEADS &&
+  return rows >= 0 && H >= 1 && H <= IDX_MAX_HEADS && rows <= IDX_ATTN_MAX_ROWS &&
          latent_ok(latent) && max_tokens >= 0 && max_tokens <= 0x7fffffffLL - IDX_PAGE_SIZE;
 }
 

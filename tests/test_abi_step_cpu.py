@@ -129,6 +129,22 @@ def test_latent_insert_refuses(L, change):
     assert _latent(L, **change) == ERR_ARG
 
 
+@pytest.mark.parametrize("rows,heads", [(1 << 26, 2), ((1 << 20) + 1, 127), (1 << 7, 1 << 20)])
+def test_norm_rope_refuses_more_lanes_than_a_launch_has(L, rows, heads):
+    # rows * (heads + 1) rows of 16 lanes each: past 2^31 lanes
+    assert _norm(L, q=_heads(heads=heads), k=_heads(heads=1), T=rows) == ERR_ARG
+
+
+def test_latent_insert_and_attn_refuse_more_lanes_than_a_launch_has(L):
+    assert _latent(L, T=(1 << 24) + 1, q_pe=None, H=0) == ERR_ARG
+    assert _latent(L, T=1 << 24, H=17) == ERR_ARG
+    assert L.idx_attn_paged(*_args(ATTN, rows=(1 << 22) + 1)) == ERR_ARG
+    if _no_gpu():
+        assert _latent(L, T=1 << 24, H=16, qs=1024, qh=64) == ERR_NO_DEVICE
+        assert L.idx_attn_paged(*_args(ATTN, rows=1 << 22)) == ERR_NO_DEVICE
+        assert _norm(L, q=_heads(), k=_heads(heads=1), T=(1 << 27) // 3) == ERR_NO_DEVICE
+
+
 def test_latent_insert_rope_and_empty(L):
     for change in (dict(dim=0), dict(dim=128), dict(mode=5), dict(cos=None), dict(positions=MIS),
                    dict(positions=None, rows=3)):
