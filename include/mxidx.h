@@ -105,6 +105,7 @@ typedef enum { IDX_BF16 = 0, IDX_F32 = 1 } idx_dtype;
 #define IDX_MERGE_MAX_CANDIDATES 8192
 #define IDX_LATENT_ROPE 64         /* rotated values of a latent row */
 #define IDX_ATTN_MAX_PAGES ((1 << 26) - 1024)   /* row numbers are 32-bit in the kernel */
+#define IDX_ATTN_MAX_TOKENS 0x7ffffe00           /* places of a row: tiles beyond it still count in 32 bits */
 #define IDX_ATTN_MAX_ROWS (1 << 22)              /* and a launch has fewer than 2^32 lanes */
 
 /* Version of this ABI (major * 100 + minor). */
@@ -556,7 +557,8 @@ int idx_topk_merge(const float* values, const int32_t* indices, int world, int64
  *     has no row in this step).  Negative lengths count as 0.
  *   The step's rows are the requests' new tokens in order: request b's rows begin
  *   at row sum(query_lens[:b]).  num_rows is how many rows the outputs hold; rows
- *   behind the last new token are padding, new tokens behind num_rows are dropped.
+ *   behind the last new token are padding, new tokens behind num_rows are dropped (a page
+ *   is written into the table by the row of its first token: one that is dropped is not).
  *   block_table: [B, bt_row_stride] int32, bt_pages columns in use; NULL only when
  *     slot_mapping is NULL too.  With free_pages NULL it is read only.  With free_pages
  *     it is read up to the pages a request held before the step,
@@ -643,7 +645,8 @@ int idx_norm_rope(const idx_heads* q, const idx_heads* k, int dtype, int64_t T,
  *     t*out_row_stride + h*out_head_stride (values 64): with q_out = q + latent the tail
  *     of idx_attn_paged's query rows.  Rows of tokens without a slot are written too.
  *   kv, q_pe and q_out 16-byte aligned, strides multiples of 8 (bf16) or 4 (fp32 inputs);
- *   cache 16-byte aligned; page_size must be 64.  No output may overlap an input.
+ *   cache 16-byte aligned; page_size must be 64.  q_out may be q_pe itself (bf16, the same
+ *     strides); no other output may overlap an input.
  *   T <= 2^24 and T * H <= 2^28. */
 int idx_latent_insert(const void* kv, int dtype, int64_t T, int64_t kv_row_stride, int latent,
                       int norm, const float* weight, float eps, const idx_rope* rope,
@@ -673,7 +676,8 @@ int idx_latent_insert(const void* kv, int dtype, int64_t T, int64_t kv_row_strid
  *   max_tokens: host-side upper bound of ke - ks: later tokens are not read.  Tokens whose
  *        page lies outside the cache are skipped.
  *   out: [rows, H, latent] bf16, strides multiples of 4, 8-byte aligned; lse: [rows, H]
- *        fp32 or NULL.  rows <= IDX_ATTN_MAX_ROWS.
+ *        fp32 or NULL.  They overlap no input.  rows <= IDX_ATTN_MAX_ROWS; max_tokens and k
+ *        <= IDX_ATTN_MAX_TOKENS.
  *   workspace: device memory of at least idx_attn_workspace_bytes(rows, H, latent, k with
  *        indices, else max_tokens) bytes, 256-byte aligned, as for idx_topk_ws: no
  *        initialization, scratch after the call, not shared by calls that may run at the

@@ -1103,8 +1103,8 @@ def latent_insert(kv, slot_mapping, cache, cos, sin, mode="neox", positions=None
     latent + 64] bf16: the latent part RMS-normed (``norm`` "rms", fp32 ``weight`` [latent] or
     None; or "none"), the last 64 values rotated (cos / sin fp32 [table_rows, 32]), slots < 0
     skipped.  ``q_pe`` [T, H, 64]: the query's positional part, rotated into ``q_out``
-    [T, H, 64] bf16 (``q[..., latent:]`` of attn_paged's query, say) in the same launch.
-    Returns cache, or (cache, q_out) with q_pe."""
+    [T, H, 64] bf16 (``q[..., latent:]`` of attn_paged's query, say; q_pe itself if that is
+    bf16) in the same launch.  Returns cache, or (cache, q_out) with q_pe."""
     torch = _torch()
     device = _device_of(kv, "kv")
     dtype = kv.dtype
@@ -1190,6 +1190,8 @@ def attn_paged(q, cache, block_table, ke, scale, indices=None, ks=None, row_seq=
                 (indices.numel() and indices.shape[1] > 1 and indices.stride(1) != 1):
             raise MxidxError("indices must be [rows, k] with unit inner stride")
         k, istride = indices.shape[1], indices.stride(0)
+        if k > 0x7fffffff:
+            raise MxidxError("indices has too many columns")
         ip = ip or ep      # a list of no columns has no address of its own, and is still a list
     if out is None:
         out = _empty(stream, (rows, H, latent), torch.bfloat16, device)

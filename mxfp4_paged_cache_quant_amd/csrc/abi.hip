@@ -600,6 +600,10 @@ static int check_heads(const idx_heads* s, int dtype, int64_t T) {
       !stride_ok(s->out_row_stride, T, IDX_HEAD_DIM, al) ||
       !stride_ok(s->out_head_stride, s->heads, IDX_HEAD_DIM, al))
     return IDX_ERR_ARG;
+  // in place: row by row
+  if (s->out == s->x && ((T > 1 && s->out_row_stride != s->row_stride) ||
+                         (s->heads > 1 && s->out_head_stride != s->head_stride)))
+    return IDX_ERR_ARG;
   if (s->norm != IDX_NORM_NONE &&
       (!aligned(s->weight, 16) || !aligned(s->bias, 16) || !(s->eps >= 0.f)))
     return IDX_ERR_ARG;
@@ -665,6 +669,10 @@ int idx_latent_insert(const void* kv, int dtype, int64_t T, int64_t kv_row_strid
                 !stride_ok(out_row_stride, T, IDX_LATENT_ROPE, 8) ||
                 !stride_ok(out_head_stride, H, IDX_LATENT_ROPE, 8)))
     return IDX_ERR_ARG;
+  if (has_q && q_out == q_pe &&                // in place: row by row
+      (dtype != IDX_BF16 || (T > 1 && out_row_stride != q_row_stride) ||
+       (H > 1 && out_head_stride != q_head_stride)))
+    return IDX_ERR_ARG;
   if ((st = gate_current()) != IDX_OK) return st;
   const mxidx::LatentSpec a{kv, T, kv_row_stride, norm, norm == IDX_NORM_RMS ? weight : nullptr,
                             eps, slot_mapping, cache, num_pages * IDX_PAGE_SIZE,
@@ -677,7 +685,7 @@ int idx_latent_insert(const void* kv, int dtype, int64_t T, int64_t kv_row_strid
 // two workgroups of 256 lanes at most where rows are many, and a launch has fewer than 2^32.
 static bool attn_sizes_ok(int64_t rows, int H, int latent, int64_t max_tokens) {
   return rows >= 0 && H >= 1 && H <= IDX_MAX_HEADS && rows <= IDX_ATTN_MAX_ROWS &&
-         latent_ok(latent) && max_tokens >= 0 && max_tokens <= 0x7fffffffLL - IDX_PAGE_SIZE;
+         latent_ok(latent) && max_tokens >= 0 && max_tokens <= IDX_ATTN_MAX_TOKENS;
 }
 
 size_t idx_attn_workspace_bytes(int64_t rows, int H, int latent, int64_t entries) {
@@ -707,7 +715,7 @@ int idx_attn_paged(const void* q, int64_t q_row_stride, int64_t q_head_stride, i
     return IDX_ERR_ARG;
   if (!ke || !aligned(ke, 4) || !aligned(ks, 4) || !aligned(row_seq, 4) || !aligned(lse, 4))
     return IDX_ERR_ARG;
-  if (indices && (k < 0 || !aligned(indices, 4) || !stride_ok(idx_row_stride, rows, k, 1)))
+  if (indices && (k < 0 || k > IDX_ATTN_MAX_TOKENS || !aligned(indices, 4) || !stride_ok(idx_row_stride, rows, k, 1)))
     return IDX_ERR_ARG;
   if (max_tokens > 0 && (!block_table || !aligned(block_table, 4))) return IDX_ERR_ARG;
   if (num_pages > 0 && (!cache || !aligned(cache, 16))) return IDX_ERR_ARG;

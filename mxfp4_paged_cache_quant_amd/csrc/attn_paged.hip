@@ -216,7 +216,7 @@ __global__ __launch_bounds__(HG * TH * kWave, kTile == 32 ? 2 : 1) void attn_ker
   __shared__ __attribute__((aligned(1024))) uint8_t tile0[kTileBytes];
   __shared__ __attribute__((aligned(1024))) uint8_t tile1[kTileBytes];
   static_assert(kTile <= kWave && 2 * kTileBytes <= 156 * 1024, "a lane for each token; two tiles fit the LDS");
-  __shared__ float2 stats[TH][kHeads];                 // the waves' (m, l), then the output's scale
+  __shared__ float2 stats[TH][kHeads];                 // the waves' (m, l)
 
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int hg = wave % HG, th = wave / HG;

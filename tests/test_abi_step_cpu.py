@@ -109,7 +109,7 @@ def test_norm_rope_refuses(L):
 
 
 LATENT = dict(kv=A, dtype=0, T=4, stride=640, latent=512, norm=1, weight=A, eps=1e-6, rope=None,
-              slots=A, cache=A, pages=8, page=64, q_pe=A, H=2, qs=256, qh=128, q_out=A, os=1152,
+              slots=A, cache=A, pages=8, page=64, q_pe=A, H=2, qs=256, qh=128, q_out=2 * A, os=1152,
               oh=576, stream=None)
 
 
@@ -143,6 +143,27 @@ def test_latent_insert_and_attn_refuse_more_lanes_than_a_launch_has(L):
         assert _latent(L, T=1 << 24, H=16, qs=1024, qh=64) == ERR_NO_DEVICE
         assert L.idx_attn_paged(*_args(ATTN, rows=1 << 22)) == ERR_NO_DEVICE
         assert _norm(L, q=_heads(), k=_heads(heads=1), T=(1 << 27) // 3) == ERR_NO_DEVICE
+
+
+def test_in_place_needs_the_same_strides(L):
+    for change in (dict(out_row_stride=512), dict(out_head_stride=256)):
+        assert _norm(L, q=_heads(**change)) == ERR_ARG
+        assert _norm(L, k=_heads(**change)) == ERR_ARG
+    same = dict(q_out=A, os=256, oh=128)
+    for change in (dict(os=512), dict(oh=64), dict(dtype=1)):
+        assert _latent(L, **{**same, **change}) == ERR_ARG
+    if _no_gpu():
+        assert _norm(L, q=_heads(out_row_stride=512, out=2 * A)) == ERR_NO_DEVICE
+        assert _norm(L, q=_heads(out_row_stride=512), T=1) == ERR_NO_DEVICE
+        assert _latent(L, **same) == ERR_NO_DEVICE
+
+
+@pytest.mark.parametrize("k", [(1 << 31) - 1, (1 << 31) - 64, 0x7ffffe01])
+def test_attn_refuses_places_past_32_bits(L, k):
+    # tiles behind the last place are counted in 32 bits too
+    assert L.idx_attn_paged(*_args(ATTN, k=k, idx_stride=k, ws=None, wb=0)) == ERR_ARG
+    assert L.idx_attn_paged(*_args(ATTN, most=k, idx=None, bt=1 << 26, ws=None, wb=0)) == ERR_ARG
+    assert L.idx_attn_workspace_bytes(4, 2, 512, k) == 0
 
 
 def test_latent_insert_rope_and_empty(L):

@@ -91,6 +91,21 @@ def test_strided_views():
     assert (q[..., :latent] == 2.0).all() and qo.data_ptr() == q[..., latent:].data_ptr()
 
 
+@pytest.mark.parametrize("T,H", [(1, 1), (50, 6), (8200, 33)])
+def test_query_in_place(T, H):
+    # the query's tail rotated where it lies, one row a run and several
+    gen = torch.Generator("cuda").manual_seed(T)
+    q = torch.randn((T, H, 192), device="cuda", generator=gen, dtype=torch.float32).bfloat16()
+    kv = torch.randn((T, 192), device="cuda", generator=gen, dtype=torch.float32).bfloat16()
+    cos, sin = rope_tables(T, 64)
+    cache = torch.zeros((-(-T // 64), 64, 192), dtype=torch.bfloat16, device="cuda")
+    args = dict(slot_mapping=torch.arange(T, device="cuda"), cache=cache, cos=dev(cos), sin=dev(sin))
+    before = q.clone()
+    _, want = mx.latent_insert(kv, q_pe=before[..., 128:], **args)
+    mx.latent_insert(kv, q_pe=q[..., 128:], q_out=q[..., 128:], **args)
+    assert torch.equal(q[..., 128:], want) and torch.equal(q[..., :128], before[..., :128])
+
+
 def test_cache_beyond_4_gib():
     latent, pages = 512, 60000                                # 4.4 GB
     cache = torch.zeros((pages, 64, latent + 64), dtype=torch.bfloat16, device="cuda")
