@@ -915,7 +915,7 @@ def _code(table, value, name):
 def _on(device, t, name, dtype, shape=None):
     """The address of t: a tensor of that type on that device, contiguous with that shape where
     one is given."""
-    if t.device == device and t.dtype is dtype and \
+    if t.get_device() == device.index and t.dtype is dtype and \
             (shape is None or (t.shape == shape and t.is_contiguous())):
         return t.data_ptr()
     if t.device != device:
@@ -964,12 +964,12 @@ def _device_of(t, name):
 def _rope_args(device, cos, sin, rope_dim, mode, positions, tokens):
     """The checked idx_rope block of a call on `device` (host memory; the tensors must outlive it)."""
     torch = _torch()
-    rows = cos.shape[0]
-    half = int(rope_dim) // 2
-    cp = _on(device, cos, "cos", torch.float32, (rows, half))
-    sp = _on(device, sin, "sin", torch.float32, (rows, half))
+    rope_dim = int(rope_dim)
+    table = (cos.shape[0], rope_dim // 2)
+    cp = _on(device, cos, "cos", torch.float32, table)
+    sp = _on(device, sin, "sin", torch.float32, table)
     pp = None if positions is None else _on(device, positions, "positions", torch.int64, (tokens,))
-    return _Rope(cp, sp, rows, pp, int(rope_dim), _code(_MODES, mode, "mode"))
+    return _Rope(cp, sp, table[0], pp, rope_dim, _code(_MODES, mode, "mode"))
 
 
 StepMap = collections.namedtuple("StepMap", ["slot_mapping", "positions", "row_seq", "ks", "ke",
@@ -996,11 +996,11 @@ def step_map(seq_lens, query_lens, block_table, num_rows, free_pages=None, free_
     sp = _on(device, seq_lens, "seq_lens", i32, (B,))
     qp = _on(device, query_lens, "query_lens", i32, (B,))
     bp = _on(device, block_table, "block_table", i32)
-    if block_table.dim() != 2 or block_table.shape[0] != B or \
-            (block_table.numel() and block_table.shape[1] > 1 and block_table.stride(1) != 1):
+    shape, strides = block_table.shape, block_table.stride()
+    if len(shape) != 2 or shape[0] != B or (shape[1] > 1 and strides[1] != 1 and B):
         raise MxidxError("block_table must be [B, pages] with unit inner stride")
-    pages = block_table.shape[1]
-    stride = block_table.stride(0) if B > 1 else max(pages, 1)
+    pages = shape[1]
+    stride = strides[0] if B > 1 else max(pages, 1)
     fp = ip = None
     free = 0
     if free_pages is not None:
@@ -1013,22 +1013,27 @@ def step_map(seq_lens, query_lens, block_table, num_rows, free_pages=None, free_
     elif free_start is not None:
         raise MxidxError("free_start needs free_pages")
 
-    def out(t, name, dtype, n):
-        if t is None:
-            return _empty(stream, n, dtype, device)
-        _on(device, t, name, dtype, (n,))
-        return t
-
-    slot_mapping = out(slot_mapping, "slot_mapping", i64, rows)
-    positions = out(positions, "positions", i64, rows)
-    row_seq = out(row_seq, "row_seq", i32, rows)
-    ks, ke = out(ks, "ks", i32, rows), out(ke, "ke", i32, rows)
-    cu_seq_offsets = out(cu_seq_offsets, "cu_seq_offsets", i64, B + 1)
-    free_next = out(free_next, "free_next", i64, 1)
+    if slot_mapping is None:
+        slot_mapping = _empty(stream, rows, i64, device)
+    if positions is None:
+        positions = _empty(stream, rows, i64, device)
+    if row_seq is None:
+        row_seq = _empty(stream, rows, i32, device)
+    if ks is None:
+        ks = _empty(stream, rows, i32, device)
+    if ke is None:
+        ke = _empty(stream, rows, i32, device)
+    if cu_seq_offsets is None:
+        cu_seq_offsets = _empty(stream, B + 1, i64, device)
+    if free_next is None:
+        free_next = _empty(stream, 1, i64, device)
+    n = (rows,)
     _call("idx_step_map", device, stream, sp, qp, B, bp, stride, pages, fp, free, ip,
-          free_next.data_ptr(), PAGE_SIZE, _code(_COLUMNS, columns, "columns"), rows,
-          slot_mapping.data_ptr(), positions.data_ptr(), row_seq.data_ptr(), ks.data_ptr(),
-          ke.data_ptr(), cu_seq_offsets.data_ptr())
+          _on(device, free_next, "free_next", i64, (1,)), PAGE_SIZE,
+          _code(_COLUMNS, columns, "columns"), rows, _on(device, slot_mapping, "slot_mapping", i64, n),
+          _on(device, positions, "positions", i64, n), _on(device, row_seq, "row_seq", i32, n),
+          _on(device, ks, "ks", i32, n), _on(device, ke, "ke", i32, n),
+          _on(device, cu_seq_offsets, "cu_seq_offsets", i64, (B + 1,)))
     return StepMap(slot_mapping, positions, row_seq, ks, ke, cu_seq_offsets, free_next)
 
 
@@ -1090,11 +1095,12 @@ def _latent_cache(device, cache):
     """(address, num_pages, latent) of a latent cache."""
     torch = _torch()
     cp = _on(device, cache, "cache", torch.bfloat16)
-    if cache.dim() != 3 or cache.shape[1] != PAGE_SIZE or not cache.is_contiguous() or \
-            cache.shape[2] - LATENT_ROPE not in LATENT_DIMS:
+    shape = cache.shape
+    if len(shape) != 3 or shape[1] != PAGE_SIZE or not cache.is_contiguous() or \
+            shape[2] - LATENT_ROPE not in LATENT_DIMS:
         raise MxidxError("cache must be a contiguous bfloat16 [num_pages, 64, latent + 64], latent "
                          f"one of {LATENT_DIMS}")
-    return cp, cache.shape[0], cache.shape[2] - LATENT_ROPE
+    return cp, shape[0], shape[2] - LATENT_ROPE
 
 
 def latent_insert(kv, slot_mapping, cache, cos, sin, mode="neox", positions=None, norm="rms",
@@ -1111,9 +1117,10 @@ def latent_insert(kv, slot_mapping, cache, cos, sin, mode="neox", positions=None
     if dtype not in (torch.bfloat16, torch.float32):
         raise MxidxError("kv must be bfloat16 or float32")
     cp, num_pages, latent = _latent_cache(device, cache)
-    if kv.dim() != 2 or kv.shape[1] != latent + LATENT_ROPE or (kv.shape[0] and kv.stride(1) != 1):
+    shape, kv_strides = kv.shape, kv.stride()
+    if len(shape) != 2 or shape[1] != latent + LATENT_ROPE or (shape[0] and kv_strides[1] != 1):
         raise MxidxError(f"kv must be [T, {latent + LATENT_ROPE}] with a contiguous last dim")
-    T = kv.shape[0]
+    T = shape[0]
     mp = _on(device, slot_mapping, "slot_mapping", torch.int64, (T,))
     wp = None if weight is None else _on(device, weight, "weight", torch.float32, (latent,))
     rope = _rope_args(device, cos, sin, LATENT_ROPE, mode, positions, T)
@@ -1121,21 +1128,22 @@ def latent_insert(kv, slot_mapping, cache, cos, sin, mode="neox", positions=None
     H = qs = qh = os_ = oh = 0
     if q_pe is not None:
         qp = _on(device, q_pe, "q_pe", dtype)
-        if q_pe.dim() != 3 or q_pe.shape[0] != T or q_pe.shape[2] != LATENT_ROPE:
+        shape = q_pe.shape
+        if len(shape) != 3 or shape[0] != T or shape[2] != LATENT_ROPE:
             raise MxidxError(f"q_pe must be [{T}, H, {LATENT_ROPE}]")
+        H = shape[1]
         if q_out is None:
-            q_out = _empty(stream, q_pe.shape, torch.bfloat16, device)
+            q_out = _empty(stream, shape, torch.bfloat16, device)
         op = _on(device, q_out, "q_out", torch.bfloat16)
-        if q_out.shape != q_pe.shape:
+        if q_out.shape != shape:
             raise MxidxError("q_out must have q_pe's shape")
-        if q_pe.numel() and (q_pe.stride(2) != 1 or q_out.stride(2) != 1):
+        (qs, qh, qi), (os_, oh, oi) = q_pe.stride(), q_out.stride()
+        if T and H and (qi != 1 or oi != 1):
             raise MxidxError("q_pe and q_out must have a contiguous last dim")
-        H, qs, qh = q_pe.shape[1], q_pe.stride(0), q_pe.stride(1)
-        os_, oh = q_out.stride(0), q_out.stride(1)
     elif q_out is not None:
         raise MxidxError("q_out needs q_pe")
     _call("idx_latent_insert", device, stream, kv.data_ptr(),
-          IDX_BF16 if dtype == torch.bfloat16 else IDX_F32, T, kv.stride(0), latent,
+          IDX_BF16 if dtype == torch.bfloat16 else IDX_F32, T, kv_strides[0], latent,
           _code({"none": 0, "rms": 1}, norm, "norm"), wp, eps, ctypes.addressof(rope), mp, cp,
           num_pages, PAGE_SIZE, qp, H, qs, qh, op, os_, oh)
     return cache if q_pe is None else (cache, q_out)
@@ -1166,16 +1174,18 @@ def attn_paged(q, cache, block_table, ke, scale, indices=None, ks=None, row_seq=
     torch = _torch()
     device = _device_of(q, "q")
     cp, num_pages, latent = _latent_cache(device, cache)
-    qp = _on(device, q, "q", torch.bfloat16)
-    if q.dim() != 3 or q.shape[2] != latent + LATENT_ROPE or (q.numel() and q.stride(2) != 1):
+    bf16, i32 = torch.bfloat16, torch.int32
+    qp = _on(device, q, "q", bf16)
+    shape, q_strides = q.shape, q.stride()
+    if len(shape) != 3 or shape[2] != latent + LATENT_ROPE or (q_strides[2] != 1 and q.numel()):
         raise MxidxError(f"q must be [rows, H, {latent + LATENT_ROPE}] with a contiguous last dim")
-    rows, H = q.shape[0], q.shape[1]
-    i32 = torch.int32
+    rows, H = shape[0], shape[1]
     bp = _on(device, block_table, "block_table", i32)
-    if block_table.dim() != 2 or (block_table.numel() and block_table.shape[1] > 1 and block_table.stride(1) != 1):
+    shape, strides = block_table.shape, block_table.stride()
+    if len(shape) != 2 or (shape[1] > 1 and strides[1] != 1 and shape[0]):
         raise MxidxError("block_table must be [B, pages] with unit inner stride")
-    B, pages = block_table.shape
-    stride = block_table.stride(0) if B > 1 else max(pages, 1)
+    B, pages = shape
+    stride = strides[0] if B > 1 else max(pages, 1)
     if max_tokens is None:
         max_tokens = pages * PAGE_SIZE
     elif max_tokens > pages * PAGE_SIZE:
@@ -1186,28 +1196,30 @@ def attn_paged(q, cache, block_table, ke, scale, indices=None, ks=None, row_seq=
     ip, istride, k = None, 0, 0
     if indices is not None:
         ip = _on(device, indices, "indices", i32)
-        if indices.dim() != 2 or indices.shape[0] != rows or \
-                (indices.numel() and indices.shape[1] > 1 and indices.stride(1) != 1):
+        shape, strides = indices.shape, indices.stride()
+        if len(shape) != 2 or shape[0] != rows or (shape[1] > 1 and strides[1] != 1 and rows):
             raise MxidxError("indices must be [rows, k] with unit inner stride")
-        k, istride = indices.shape[1], indices.stride(0)
+        k, istride = shape[1], strides[0]
         if k > 0x7fffffff:
             raise MxidxError("indices has too many columns")
         ip = ip or ep      # a list of no columns has no address of its own, and is still a list
     if out is None:
-        out = _empty(stream, (rows, H, latent), torch.bfloat16, device)
-    op = _on(device, out, "out", torch.bfloat16)
-    if tuple(out.shape) != (rows, H, latent) or (out.numel() and out.stride(2) != 1):
+        out = _empty(stream, (rows, H, latent), bf16, device)
+    op = _on(device, out, "out", bf16)
+    strides = out.stride()
+    if out.shape != (rows, H, latent) or (strides[2] != 1 and rows and H):
         raise MxidxError(f"out must be [{rows}, {H}, {latent}] with a contiguous last dim")
     if lse is None:
         lse = _empty(stream, (rows, H), torch.float32, device)
     lp = _on(device, lse, "lse", torch.float32, (rows, H))
+    wp, wb = None, 0
     if workspace is None:
         need = attn_workspace_bytes(rows, H, latent, k if indices is not None else max_tokens)
         if need:
             workspace = _empty(stream, need, torch.uint8, device)
-    wp = None if workspace is None else _on(device, workspace, "workspace", torch.uint8)
-    wb = 0 if workspace is None else workspace.numel()
-    _call("idx_attn_paged", device, stream, qp, q.stride(0), q.stride(1), rows, H, latent, cp,
+    if workspace is not None:
+        wp, wb = _on(device, workspace, "workspace", torch.uint8), workspace.numel()
+    _call("idx_attn_paged", device, stream, qp, q_strides[0], q_strides[1], rows, H, latent, cp,
           num_pages, PAGE_SIZE, bp, stride, B, rp, kp, ep, ip, istride, k, max_tokens, scale, op,
-          out.stride(0), out.stride(1), lp, wp, wb)
+          strides[0], strides[1], lp, wp, wb)
     return out, lse

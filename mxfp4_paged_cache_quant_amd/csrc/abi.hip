@@ -37,10 +37,12 @@ int gate_device(int dev) {
 }
 
 int gate_current() {
-  int count = 0;
-  if (hipGetDeviceCount(&count) != hipSuccess || count <= 0) return IDX_ERR_NO_DEVICE;
   int dev = 0;
   if (hipGetDevice(&dev) != hipSuccess) return IDX_ERR_NO_DEVICE;
+  if (dev >= 0 && dev < kMaxDevices && g_gate[dev].load(std::memory_order_acquire) == 1)
+    return IDX_OK;                             // the common call: nothing more is asked
+  int count = 0;
+  if (hipGetDeviceCount(&count) != hipSuccess || count <= 0) return IDX_ERR_NO_DEVICE;
   return gate_device(dev);
 }
 
