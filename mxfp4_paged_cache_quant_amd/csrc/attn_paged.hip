@@ -87,6 +87,14 @@ __device__ __forceinline__ int swz(int t) {
   return (t >> 1) & 7;
 }
 
+// The maximum over the four lanes of one head (lane groups of 16).
+__device__ __forceinline__ float max_groups(float v) {
+  const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+  const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
+
 // The lane number, computed anew where it is called: nothing derived from it can be
 // kept in registers from one call to the next.
 __device__ __forceinline__ int fresh_lane() {
@@ -97,7 +105,7 @@ __device__ __forceinline__ int fresh_lane() {
 
 struct Row {                               // a query row's window
   int seq;
-  int64_t ks;
+  int ks;
   int window;
 };
 
@@ -106,7 +114,7 @@ __device__ __forceinline__ bool row_of(const AttnArgs& a, int64_t r, Row& o) {
   o.seq = a.row_seq ? a.row_seq[r] : (int)((uint32_t)r / (uint32_t)a.rows_per_seq);
   if (o.seq < 0 || o.seq >= a.B) return false;
   o.ks = a.ks ? a.ks[r] : 0;
-  o.window = (int)min(max((int64_t)a.ke[r] - o.ks, (int64_t)0), a.max_tokens);
+  o.window = (int)min(max((int64_t)a.ke[r] - (int64_t)o.ks, (int64_t)0), a.max_tokens);
   return true;
 }
 
@@ -119,8 +127,9 @@ __device__ __forceinline__ int list_entry(const AttnArgs& a, int64_t r, int e) {
 }
 
 __device__ __forceinline__ int token_of(const AttnArgs& a, const Row& row, int entry, int e) {
-  const int64_t p = a.indices ? (int64_t)entry - row.ks : entry;
-  return p >= 0 && p < row.window && (!a.indices || e < a.k) ? (int)p : -1;
+  if (!a.indices) return entry < row.window ? entry : -1;
+  const uint32_t p = (uint32_t)entry - (uint32_t)row.ks;   // exact from ks on
+  return entry >= row.ks && p < (uint32_t)row.window && e < a.k ? (int)p : -1;
 }
 
 __device__ __forceinline__ int token_page(const AttnArgs& a, const Row& row, int p) {
@@ -174,7 +183,7 @@ struct TileCopy {
                                               int offset, int ln) {
     if constexpr (kSmall) {
       const int t = t0 + (kPer == 1 ? 0 : ln / C);
-      const int row = kPer == 1 ? __builtin_amdgcn_readlane(rows, t) : __shfl(rows, t);
+      const int row = kPer == 1 ? __builtin_amdgcn_readlane(rows, t) : __builtin_amdgcn_ds_bpermute(4 * t, rows);
       copy16(buffer_rsrc(src.base, (int)src.bytes), dst + t0 * C * 16,
              row + offset + (((ln % C) ^ swz<C>(t)) << 4));
     } else if (C >= kWave || ln < C) {
@@ -245,7 +254,7 @@ __global__ __launch_bounds__(HG * TH * kWave, kTile == 32 ? 2 : 1) void attn_ker
   auto rows_of = [&](int p, int page, uint64_t& mask) __attribute__((always_inline)) {
     const bool ok = p >= 0 && page >= 0 && page < parts.pages;
     mask = __ballot(ok);
-    const uint32_t row = (uint32_t)page * kPage + (uint32_t)(p % kPage);
+    const uint32_t row = (uint32_t)page * kPage + ((uint32_t)p & (kPage - 1));
     return ok ? (int)(kSmall ? row * (kRow * 2) : row) : kNoRow;
   };
   const Source cache{static_cast<const char*>(a.cache), parts.cache_bytes, kRow * 2};
@@ -309,8 +318,7 @@ __global__ __launch_bounds__(HG * TH * kWave, kTile == 32 ? 2 : 1) void attn_ker
     for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int i = 0; i < 4; ++i) top = fmaxf(top, s[t][i]);
-    top = fmaxf(top, __shfl_xor(top, 16));
-    top = fmaxf(top, __shfl_xor(top, 32));
+    top = max_groups(top);
     // the reference is raised only where weights would pass 2^kSlack: what was summed so
     // far is seldom rescaled
     const bool grow = m != neg_inf() && top > m + kSlack;
