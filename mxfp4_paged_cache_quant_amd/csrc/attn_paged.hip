@@ -229,8 +229,12 @@ __global__ __launch_bounds__(HG * TH * kWave, kTile == 32 ? 2 : 1) void attn_ker
 
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int hg = wave % HG, th = wave / HG;
-  const uint32_t groups = (uint32_t)parts.heads / kHeads, unit = blockIdx.x / groups;
-  const int group = (int)(blockIdx.x - unit * groups);
+  // Workgroups go to the eight XCDs in turn: each takes a run of neighbouring numbers, so that
+  // the head groups of a row, and rows of one sequence, read the same rows through one L2 (16
+  // rows of 2048 tokens, 2 groups: 27.3 -> 23.6 us; 64 rows of two: 86.6 -> 83.7)
+  const uint32_t xcd = blockIdx.x % 8, number = xcd * (gridDim.x / 8) + min(xcd, gridDim.x % 8) + blockIdx.x / 8;
+  const uint32_t groups = (uint32_t)parts.heads / kHeads, unit = number / groups;
+  const int group = (int)(number - unit * groups);
   const uint32_t r32 = unit / (uint32_t)parts.splits;
   const int split = (int)(unit - r32 * (uint32_t)parts.splits);
   const int64_t r = r32;
