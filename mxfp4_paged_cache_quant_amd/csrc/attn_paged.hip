@@ -580,20 +580,22 @@ struct Plan {
 
 // Few rows are split over the tokens, up to one workgroup for each CU.  A split costs its
 // share of the workspace's traffic (2 KB a head, written and read), so it takes 4 tiles
-// or more (16 rows of 2048 tokens, 64 heads: 27.4 us with 8 splits, 29.6 with 16), or 2
+// or more (16 rows of 2048 tokens, 32 heads: 21.0 us with 8 splits, 22.9 with 16), or 2
 // where even 64 workgroups do not come together (one such row: 15.5 us with 16 splits of
 // 32 heads); and the join of a row reads them one after the other (one row of 32768
 // tokens: 36 us with 64 splits, 43 with 128).
 // 64 heads a workgroup read the rows fewest times (32 rows of 2 x 6600 tokens, 128
-// heads: 99 us with 64, 168 with 32); 32 heads spread a call over twice the CUs that
-// would not fill them otherwise (one row: 15.5 us, 19.1 with 64; 16 rows: 27.3 and 27.4).
+// heads: 91 us with 64, 132 with 32; 64 rows of 2048 tokens, 64 heads: 55 and 58); 32
+// heads spread a call over twice the CUs that would not fill them otherwise (one row:
+// 15.5 us, 19.1 with 64) or fill them with half the partial sums (32 rows of 2048 tokens,
+// 64 heads: 31 us with 4 splits, 34 with 64 heads and 8; 4 rows of 16384: 32 and 38).
 // Many rows: two workgroups of four waves a CU, 32 tokens at a time, whose phases do not
 // fall together (1024 rows of 2048 tokens, 64 heads: 330-346 us, 355-363 with one of
 // eight waves); with 200 rows, which do not fill both places, 136 us and 119.
 Plan plan_of(int64_t rows, int H, int64_t entries) {
   Plan p;
   const int64_t tiles = (entries + 63) / 64, quarter = std::min<int64_t>((tiles + 3) / 4, kMaxSplits);
-  p.group_heads = H <= 16 ? 16 : H <= 32 || rows * ((H + 31) / 32) * quarter <= kCus ? 32 : 64;
+  p.group_heads = H <= 16 ? 16 : H <= 32 || rows * ((H + 31) / 32) * quarter <= 2 * kCus ? 32 : 64;
   p.heads = (H + p.group_heads - 1) / p.group_heads * p.group_heads;
   const int64_t units = rows * (p.heads / p.group_heads);
   p.tile = p.group_heads == 64 && units >= 2 * kCus ? 32 : 64;
