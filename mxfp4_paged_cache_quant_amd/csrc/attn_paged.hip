@@ -226,6 +226,10 @@ __global__ __launch_bounds__(HG * TH * kWave, kTile == 32 ? 2 : 1) void attn_ker
   __shared__ __attribute__((aligned(1024))) uint8_t tile1[kTileBytes];
   static_assert(kTile <= kWave && 2 * kTileBytes <= 156 * 1024, "a lane for each token; two tiles fit the LDS");
   __shared__ float2 stats[TH][kHeads];                 // the waves' (m, l)
+  // Query steps that stay in LDS where the registers do not hold all (a row a copy takes
+  // more of them): a spilled one is read back behind the copies on their way.
+  constexpr int kRest = kLatent == 512 && !kSmall ? 1 : 0, kKept = KS - kRest;
+  __shared__ v8s q_rest[kRest ? kRest * HG * kWave : 1];
 
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int hg = wave % HG, th = wave / HG;
@@ -246,7 +250,7 @@ __global__ __launch_bounds__(HG * TH * kWave, kTile == 32 ? 2 : 1) void attn_ker
   const int t0 = split * share + min(split, more);     // the first `more` splits take one more
   const int t1 = t0 + share + (split < more ? 1 : 0);
 
-  v8s q[KS];                                           // step s: values 32s + 8g .. +7
+  v8s q[kKept];                                        // step s: values 32s + 8g .. +7
   v4f o[NV];
 #pragma unroll
   for (int v = 0; v < NV; ++v) o[v] = v4f{0.f, 0.f, 0.f, 0.f};
@@ -286,7 +290,7 @@ __global__ __launch_bounds__(HG * TH * kWave, kTile == 32 ? 2 : 1) void attn_ker
           x[t] = *(MXIDX_LDS const v8s*)(buf + at);
         }
       };
-      v8s x[kAhead][NT];
+      v8s x[kAhead][NT], rest[kRest ? kRest : 1];
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) keys(k, x[k]);
 #pragma unroll
@@ -295,8 +299,10 @@ __global__ __launch_bounds__(HG * TH * kWave, kTile == 32 ? 2 : 1) void attn_ker
       for (int k = 0; k < KS; ++k) {
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int t = 0; t < NT; ++t) s[t] = mfma_bf16(x[k % kAhead][t], q[k], s[t]);
+        for (int t = 0; t < NT; ++t) s[t] = mfma_bf16(x[k % kAhead][t], k < kKept ? q[k] : rest[k - kKept], s[t]);
         if (k + kAhead < KS) keys(k + kAhead, x[k % kAhead]);
+        if (kRest > 0 && k + kAhead >= kKept && k + kAhead < KS)
+          rest[k + kAhead - kKept] = *(MXIDX_LDS const v8s*)(q_rest + ((k + kAhead - kKept) * HG + hg) * kWave + ln);
 #pragma unroll
         for (int i = 0; i < Copy::kPieces; ++i)
           if (i * KS / Copy::kPieces == k)
@@ -417,8 +423,12 @@ __global__ __launch_bounds__(HG * TH * kWave, kTile == 32 ? 2 : 1) void attn_ker
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
         const int at = k < KL ? (key ^ ((k & 3) << 6)) + (k >> 2) * 256 : pos ^ ((k - KL) << 6);
-        q[k] = kQTiles > 1 && hg >= kTile / 16 ? *(MXIDX_LDS const v8s*)((MXIDX_LDS uint8_t*)tile0 + at)
-                                               : *(MXIDX_LDS const v8s*)((MXIDX_LDS uint8_t*)tile1 + at);
+        const v8s x = kQTiles > 1 && hg >= kTile / 16 ? *(MXIDX_LDS const v8s*)((MXIDX_LDS uint8_t*)tile0 + at)
+                                                      : *(MXIDX_LDS const v8s*)((MXIDX_LDS uint8_t*)tile1 + at);
+        if (k < kKept)
+          q[k] = x;
+        else
+          q_rest[((k - kKept) * HG + hg) * kWave + ln] = x;   // both halves' waves the same
       }
     }
     if (kQTiles > 1) {
