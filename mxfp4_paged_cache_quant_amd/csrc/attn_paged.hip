@@ -156,8 +156,9 @@ __device__ __forceinline__ void copy16(__amdgpu_buffer_rsrc_t rs, MXIDX_LDS uint
 // the caller issues between its products: latent rows first, then the positional ones,
 // C 16-byte chunks of each.  Lane t of `rows` holds token t's row: where 32-bit offsets
 // reach the whole cache (kSmall) its byte there, and rows that fill less than an
-// instruction share one; else its number (stride bytes each), with a descriptor and an
-// instruction for each row.  A place without a row (kNoRow) is out of its descriptor's
+// instruction share one; else its number (stride bytes each), with a descriptor for each
+// row and both its parts behind one another (the parts in two passes, with a descriptor
+// each: 84 us for 64 rows of 2048 tokens, 128 heads; 75 so).  A place without a row (kNoRow) is out of its descriptor's
 // range and reads as zeros.
 constexpr int64_t kReach = 0xfffe0000ll;   // of 32-bit offsets
 constexpr int kNoRow = (int)0xffff0000u;   // past it, no wrap within a row
@@ -173,32 +174,38 @@ struct TileCopy {
   static constexpr int kRowBytes = (kLatent + kRopeWidth) * 2;
   static constexpr int LC = kLatent / 8, PC = kRopeWidth / 8;
   static constexpr int kLatentPer = LC >= kWave || !kSmall ? 1 : kWave / LC;
-  static constexpr int kPosPer = kSmall ? kWave / PC : 1;
-  static constexpr int kLatentPieces = kMine / kLatentPer, kPosPieces = kMine / kPosPer;
-  static constexpr int kPieces = kLatentPieces + kPosPieces;
+  static constexpr int kPosPer = kWave / PC;
+  static constexpr int kLatentPieces = kMine / kLatentPer;
+  static constexpr int kPieces = kLatentPieces + (kSmall ? kMine / kPosPer : 0);
   static_assert(kMine % kLatentPer == 0 && kMine % kPosPer == 0, "whole instructions");
 
   template <int C, int kPer>
   static __device__ __forceinline__ void part(const Source& src, MXIDX_LDS uint8_t* dst, int t0, int rows,
                                               int offset, int ln) {
-    if constexpr (kSmall) {
-      const int t = t0 + (kPer == 1 ? 0 : ln / C);
-      const int row = kPer == 1 ? __builtin_amdgcn_readlane(rows, t) : __builtin_amdgcn_ds_bpermute(4 * t, rows);
-      copy16(buffer_rsrc(src.base, (int)src.bytes), dst + t0 * C * 16,
-             row + offset + (((ln % C) ^ swz<C>(t)) << 4));
-    } else if (C >= kWave || ln < C) {
-      int t = t0;
-      asm volatile("" : "+s"(t));                      // what follows from it is not kept over the loop
-      const int row = __builtin_amdgcn_readlane(rows, t);
-      copy16(buffer_rsrc(src.base + (uint32_t)row * src.stride, row == kNoRow ? 0 : kRowBytes), dst + t * C * 16,
-             ((ln << 4) ^ (swz<C>(t) << 4)) + offset);
-    }
+    const int t = t0 + (kPer == 1 ? 0 : ln / C);
+    const int row = kPer == 1 ? __builtin_amdgcn_readlane(rows, t) : __builtin_amdgcn_ds_bpermute(4 * t, rows);
+    copy16(buffer_rsrc(src.base, (int)src.bytes), dst + t0 * C * 16,
+           row + offset + (((ln % C) ^ swz<C>(t)) << 4));
+  }
+
+  // One row, its latent part and its positional one, from a descriptor of its own.
+  static __device__ __forceinline__ void whole(const Source& src, MXIDX_LDS uint8_t* tile, int t, int rows,
+                                               int ln) {
+    asm volatile("" : "+s"(t));                        // what follows from it is not kept over the loop
+    const int row = __builtin_amdgcn_readlane(rows, t);
+    const __amdgpu_buffer_rsrc_t rs =
+        buffer_rsrc(src.base + (uint32_t)row * src.stride, row == kNoRow ? 0 : kRowBytes);
+    if (LC >= kWave || ln < LC) copy16(rs, tile + t * LC * 16, (ln << 4) ^ (swz<LC>(t) << 4));
+    if (ln < PC)
+      copy16(rs, tile + kTile * kLatent * 2 + t * PC * 16, ((ln << 4) ^ (swz<PC>(t) << 4)) + kLatent * 2);
   }
 
   // Piece i of the rows from `first` on.
   static __device__ __forceinline__ void piece(int i, const Source& src, MXIDX_LDS uint8_t* tile, int first,
                                                int rows, int ln) {
-    if (i < kLatentPieces)
+    if constexpr (!kSmall)
+      whole(src, tile, first + i, rows, ln);
+    else if (i < kLatentPieces)
       part<LC, kLatentPer>(src, tile, first + i * kLatentPer, rows, 0, ln);
     else
       part<PC, kPosPer>(src, tile + kTile * kLatent * 2, first + (i - kLatentPieces) * kPosPer, rows, kLatent * 2,
@@ -226,10 +233,6 @@ __global__ __launch_bounds__(HG * TH * kWave, kTile == 32 ? 2 : 1) void attn_ker
   __shared__ __attribute__((aligned(1024))) uint8_t tile1[kTileBytes];
   static_assert(kTile <= kWave && 2 * kTileBytes <= 156 * 1024, "a lane for each token; two tiles fit the LDS");
   __shared__ float2 stats[TH][kHeads];                 // the waves' (m, l)
-  // Query steps that stay in LDS where the registers do not hold all (a row a copy takes
-  // more of them): a spilled one is read back behind the copies on their way.
-  constexpr int kRest = kLatent == 512 && !kSmall ? 1 : 0, kKept = KS - kRest;
-  __shared__ v8s q_rest[kRest ? kRest * HG * kWave : 1];
 
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int hg = wave % HG, th = wave / HG;
@@ -250,7 +253,7 @@ __global__ __launch_bounds__(HG * TH * kWave, kTile == 32 ? 2 : 1) void attn_ker
   const int t0 = split * share + min(split, more);     // the first `more` splits take one more
   const int t1 = t0 + share + (split < more ? 1 : 0);
 
-  v8s q[kKept];                                        // step s: values 32s + 8g .. +7
+  v8s q[KS];                                           // step s: values 32s + 8g .. +7
   v4f o[NV];
 #pragma unroll
   for (int v = 0; v < NV; ++v) o[v] = v4f{0.f, 0.f, 0.f, 0.f};
@@ -290,7 +293,7 @@ __global__ __launch_bounds__(HG * TH * kWave, kTile == 32 ? 2 : 1) void attn_ker
           x[t] = *(MXIDX_LDS const v8s*)(buf + at);
         }
       };
-      v8s x[kAhead][NT], rest[kRest ? kRest : 1];
+      v8s x[kAhead][NT];
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) keys(k, x[k]);
 #pragma unroll
@@ -299,10 +302,8 @@ __global__ __launch_bounds__(HG * TH * kWave, kTile == 32 ? 2 : 1) void attn_ker
       for (int k = 0; k < KS; ++k) {
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int t = 0; t < NT; ++t) s[t] = mfma_bf16(x[k % kAhead][t], k < kKept ? q[k] : rest[k - kKept], s[t]);
+        for (int t = 0; t < NT; ++t) s[t] = mfma_bf16(x[k % kAhead][t], q[k], s[t]);
         if (k + kAhead < KS) keys(k + kAhead, x[k % kAhead]);
-        if (kRest > 0 && k + kAhead >= kKept && k + kAhead < KS)
-          rest[k + kAhead - kKept] = *(MXIDX_LDS const v8s*)(q_rest + ((k + kAhead - kKept) * HG + hg) * kWave + ln);
 #pragma unroll
         for (int i = 0; i < Copy::kPieces; ++i)
           if (i * KS / Copy::kPieces == k)
@@ -423,12 +424,8 @@ __global__ __launch_bounds__(HG * TH * kWave, kTile == 32 ? 2 : 1) void attn_ker
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
         const int at = k < KL ? (key ^ ((k & 3) << 6)) + (k >> 2) * 256 : pos ^ ((k - KL) << 6);
-        const v8s x = kQTiles > 1 && hg >= kTile / 16 ? *(MXIDX_LDS const v8s*)((MXIDX_LDS uint8_t*)tile0 + at)
-                                                      : *(MXIDX_LDS const v8s*)((MXIDX_LDS uint8_t*)tile1 + at);
-        if (k < kKept)
-          q[k] = x;
-        else
-          q_rest[((k - kKept) * HG + hg) * kWave + ln] = x;   // both halves' waves the same
+        q[k] = kQTiles > 1 && hg >= kTile / 16 ? *(MXIDX_LDS const v8s*)((MXIDX_LDS uint8_t*)tile0 + at)
+                                               : *(MXIDX_LDS const v8s*)((MXIDX_LDS uint8_t*)tile1 + at);
       }
     }
     if (kQTiles > 1) {
