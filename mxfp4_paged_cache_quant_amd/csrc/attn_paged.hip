@@ -25,14 +25,15 @@
 // the keys' reads (16 tokens, one chunk) and the values' transposing reads (16 tokens,
 // two neighbouring chunks) over all banks.  The query comes the same way, once.
 //
-// What bounds it: with many rows the instruction issue of two waves a SIMD (a step of
-// the second product is an MFMA of 16 cycles, two LDS reads, a wait and an address; 4,700
-// cycles a tile of 64 heads x 64 tokens, of which the MFMAs are 2,176), 854 TFLOP/s at
-// 1024 rows x 2048 tokens x 64 heads where a large library product reaches 1,306; with few
-// rows the way to the first tile (the row's window, its list, its pages, the rows: four
-// round trips) and the partial sums.  32 heads a wave with the tile's weights passed
-// through LDS halves the LDS reads, but not the instructions (8 waves: 482 us; 4 waves
-// of 512 registers: 512 us; where this form took 367).
+// What bounds it: with many rows the instruction issue of two waves a SIMD and LDS
+// together (1024 rows x 2048 tokens x 64 heads: of the SIMDs' cycles 42% MFMAs and 30%
+// other vector instructions, LDS 59% busy without a bank conflict), 315-330 us = 890-930
+// TFLOP/s where a large library product reaches 1,306; with few rows the way to the first
+// tile (the row's window, its list, its pages, the rows: four round trips) and the partial
+// sums.  32 heads a wave with the tile's weights passed through LDS halves the LDS reads,
+// but not the instructions (8 waves: 482 us; 4 waves of 512 registers: 512 us; where this
+// form took 367).  A register spilled in the loop is read back behind the copies on their
+// way, so none may be (5 of them: 331 us).
 //
 // Places of a tile that hold no visible token read as zeros and get weight 0, so
 // nothing that a masked place holds reaches a sum.
@@ -75,9 +76,9 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 
 // LDS place of a 16-byte chunk: chunk c of token t's row is stored at c ^ swz(t).
 // Latent rows are multiples of 256 bytes, so their banks repeat every 16 chunks and swz
-// runs over 16 values; 8-token groups of either kind that one pass of a read takes
-// (0..7 and 8..15 for the transposing reads, which take chunk pairs, {0..3, 12..15} and
-// the like for the 16-byte ones) fall on different places.  Measured: 4.0 cycles a
+// runs over 16 values; the 8-token groups that one pass of a read takes (0..7 and 8..15
+// for the transposing reads, which take chunk pairs, {0..3, 12..15} and the like for the
+// 16-byte ones) fall on different places.  Measured: 4.0 cycles a
 // 16-byte and 2.5 a transposing read of a wave, none lost; with the same values in plain
 // order 8.0 and 2.5.  The 128-byte positional rows alternate between two halves of the
 // banks, and 8 values over token pairs do (4.0 cycles).
@@ -596,8 +597,8 @@ struct Plan {
 // 15.5 us, 19.1 with 64) or fill them with half the partial sums (32 rows of 2048 tokens,
 // 64 heads: 31 us with 4 splits, 34 with 64 heads and 8; 4 rows of 16384: 32 and 38).
 // Many rows: two workgroups of four waves a CU, 32 tokens at a time, whose phases do not
-// fall together (1024 rows of 2048 tokens, 64 heads: 330-346 us, 355-363 with one of
-// eight waves); with 200 rows, which do not fill both places, 136 us and 119.
+// fall together (1024 rows of 2048 tokens, 64 heads: 312-328 us, 325-342 with one of
+// eight waves); with 200 rows, which do not fill both places, 128 us and 112.
 Plan plan_of(int64_t rows, int H, int64_t entries) {
   Plan p;
   const int64_t tiles = (entries + 63) / 64, quarter = std::min<int64_t>((tiles + 3) / 4, kMaxSplits);

@@ -66,6 +66,11 @@ independently of its code.  Function -> pin (test file):
 * kpool.write_mask / pool_indices / pooled_rows / insert -- P3's printed
   bookkeeping worked by hand, plain-loop brute force, closed forms (mean,
   selection, shift invariance), masked writes only (test_oracle_kpool)
+* step_map.step_map -- hand-worked requests (page borders, padding, a list of pages that runs
+  out) (test_oracle_step)
+* norm_rope.norm / rope / bound -- hand-worked rows; the rotation against rope.apply_rope
+  (test_oracle_step)
+* latent_attn.attn -- hand-worked weights, columns, pages and empty rows (test_oracle_step)
 
 The pins of the comparison rules and of A are also run against copies of the
 functions with one planted mistake each, and must reject every copy.  The
@@ -74,4 +79,5 @@ of zero, scale byte order) are pinned by the hand-worked bytes derived from the
 adopted reading.
 """
 
-from . import mxfp4, paged_cache, logits, topk, tolerance, fp8, rope, kpool  # noqa: F401
+from . import (mxfp4, paged_cache, logits, topk, tolerance, fp8, rope, kpool, step_map, norm_rope,  # noqa: F401
+               latent_attn)
