@@ -224,6 +224,40 @@ def test_cache_beyond_4_gib(k):
     _close(got, _oracle(small))
 
 
+@pytest.mark.parametrize("rows,H", [(3, 8), (3, 20), (200, 64), (600, 40)])
+@pytest.mark.parametrize("k", [0, 130])
+def test_many_and_few_rows_of_a_cache_beyond_4_gib(rows, H, k):
+    # every grouping of heads and tile, with rows' numbers instead of their places
+    latent, pages = 512, 60000
+    used = np.array([59999, 0, 58255, 29128, 59000, 3, 40000, 59998, 5, 30000, 44444], np.int32)
+    c = _case(rows, [650], next_n=rows, H=H, latent=latent, k=k)
+    vals = c["cache"][c["bt"][0]]
+    d = _to_dev(c)
+    d["cache"] = torch.zeros((pages, 64, latent + 64), dtype=torch.bfloat16, device="cuda")
+    d["cache"][torch.from_numpy(used.astype(np.int64)).cuda()] = torch.from_numpy(vals).to(torch.bfloat16).cuda()
+    d["block_table"] = dev(used[None])
+    got = mx.attn_paged(**d)
+    torch.cuda.synchronize()
+    pick = np.unique(np.array([0, 1, rows // 2, rows - 2, rows - 1]))
+    part = dict(c, q=c["q"][pick], ke=c["ke"][pick], indices=None if k == 0 else c["indices"][pick],
+                row_seq=np.zeros(len(pick), np.int32))
+    _close((got[0][dev(pick)], got[1][dev(pick)]), _oracle(part))
+
+
+@pytest.mark.parametrize("latent", [128, 256, 512])
+@pytest.mark.parametrize("rows,H,n", [(520, 64, 97), (300, 100, 33), (150, 64, 700), (70, 128, 1400)])
+@pytest.mark.parametrize("k", [0, 70])
+def test_many_rows(latent, rows, H, n, k):
+    # two workgroups a CU, one, and one whose tokens are split; NaN in all places that no row sees
+    c = _case(rows, [n, 64, 1, n - 1, n], next_n=rows // 5, H=H, latent=latent, k=k)
+    got = mx.attn_paged(**_to_dev(c, float("nan")))
+    torch.cuda.synchronize()
+    pick = np.arange(0, rows, 9)
+    part = dict(c, q=c["q"][pick], ke=c["ke"][pick], indices=None if k == 0 else c["indices"][pick],
+                row_seq=(pick // (rows // 5)).astype(np.int32))
+    _close((got[0][dev(pick)], got[1][dev(pick)]), _oracle(part))
+
+
 @pytest.mark.parametrize("k", [0, 2048])
 def test_decode_batch(k):
     # the decode workload's batch of 16 x 8192, on two of its rows

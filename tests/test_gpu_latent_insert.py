@@ -106,6 +106,35 @@ def test_query_in_place(T, H):
     assert torch.equal(q[..., 128:], want) and torch.equal(q[..., :128], before[..., :128])
 
 
+@pytest.mark.parametrize("latent,dtype,T,H", [(512, "bf16", 16401, 0), (128, "f32", 16385, 17), (256, "bf16", 8200, 33)])
+def test_many_tokens(latent, dtype, T, H):
+    # two tokens a wave and several heads a run, on every 97th token
+    rng = np.random.default_rng(T)
+    kv, q_pe = _draw(rng, (T, latent + 64), dtype), _draw(rng, (T, H, 64), dtype)
+    w = rng.standard_normal(latent).astype(np.float32)
+    cos, sin = rope_tables(500, 64)
+    pos = rng.integers(0, 501, T).astype(np.int64)            # 500: outside the table
+    pages = -(-T // 64) + 1
+    slots = rng.permutation(pages * 64)[:T].astype(np.int64)
+    slots[7::61] = -1
+    cache = torch.full((pages, 64, latent + 64), 5.0, dtype=torch.bfloat16, device="cuda")
+    got = mx.latent_insert(dev(kv), dev(slots), cache, dev(cos), dev(sin), "interleaved", positions=dev(pos),
+                           weight=dev(w), q_pe=dev(q_pe) if H else None)
+    torch.cuda.synchronize()
+    rows = host(cache.float()).astype(np.float64).reshape(-1, latent + 64)
+    pick = np.union1d(np.arange(0, T, 97), [T - 2, T - 1])
+    ref, scale = _want(_exact(kv[pick], dtype), latent, "rms", w, cos, sin, "interleaved", pos[pick])
+    live = slots[pick] >= 0
+    _close(rows[slots[pick][live]], ref[live], scale[live], "cache")
+    rest = np.ones(len(rows), bool)
+    rest[slots[slots >= 0]] = False
+    assert (rows[rest] == 5.0).all() and not (rows[~rest] == 5.0).all(1).any()
+    if H:
+        q = _exact(q_pe[pick], dtype)
+        y, sc = onr.rope(q, np.abs(q), cos, sin, 64, "interleaved", pos[pick])
+        _close(host(got[1][dev(pick)].float()), y, sc, "q")
+
+
 def test_cache_beyond_4_gib():
     latent, pages = 512, 60000                                # 4.4 GB
     cache = torch.zeros((pages, 64, latent + 64), dtype=torch.bfloat16, device="cuda")

@@ -86,6 +86,28 @@ def test_sizes_and_strides(T, Hq, Hk):
     assert torch.equal(d[:, :(Hq + Hk) * 128], out[:, :(Hq + Hk) * 128])
 
 
+@pytest.mark.parametrize("T,Hq,Hk,dtype", [(2100, 64, 1, "bf16"), (8200, 63, 2, "bf16"), (8200, 41, 0, "f32")])
+def test_runs_of_heads(T, Hq, Hk, dtype):
+    # enough rows for runs of four and more heads, some of them cut short, on every 101st token
+    gen = torch.Generator("cuda").manual_seed(T + Hq)
+    draw = lambda h: torch.randn((T, h, 128), device="cuda", generator=gen).to(  # noqa: E731
+        torch.bfloat16 if dtype == "bf16" else torch.float32)
+    q, k = draw(Hq), draw(Hk) if Hk else None
+    rng = np.random.default_rng(T)
+    w = [rng.standard_normal(128).astype(np.float32) for _ in range(2)]
+    cos, sin = rope_tables(300, 96)
+    pos = rng.integers(-1, 301, T).astype(np.int64)
+    qo, ko = mx.norm_rope(q, k, dev(cos), dev(sin), 96, "neox", positions=dev(pos), q_norm="rms", q_weight=dev(w[0]),
+                          k_norm="layer", k_weight=dev(w[1]))
+    torch.cuda.synchronize()
+    pick = np.union1d(np.arange(0, T, 101), [T - 1])
+    for name, x, y, kind, weight in (("q", q, qo, "rms", w[0]), ("k", k, ko, "layer", w[1])):
+        if x is not None:
+            part = host(x[dev(pick)].view(torch.int16)).view(np.uint16) if dtype == "bf16" else host(x[dev(pick)])
+            _check(y[dev(pick)], part, dtype, kind, weight, None, 1e-6, cos, sin, 96,
+                   "neox", pos[pick], name)
+
+
 def test_heads_in_front_of_tokens():
     # [H, T, 128] seen as [T, H, 128]: a head stride larger than the row stride
     rng = np.random.default_rng(4)
