@@ -102,6 +102,19 @@ def test_many_requests():
     _check(lens, new, table, int(new.sum()) + 50, rng.integers(0, 1 << 20, B).astype(np.int32), 0, "gathered")
 
 
+@pytest.mark.parametrize("B,longest,most_new", [(3, 300000, 250000), (900, 1500, 1400), (2500, 700, 500)])
+def test_many_rows(B, longest, most_new):
+    # more rows than the workgroups take at once
+    lens, new, table, free, _ = _case(B, B, longest, most_new)
+    new[0], lens[0] = most_new, longest
+    held, need = -(-(lens[0] - new[0]) // 64), -(-lens[0] // 64)
+    table = np.pad(table, ((0, 0), (0, max(0, int(need) - table.shape[1]))))
+    free = np.concatenate([free, np.arange(need - held, dtype=np.int32)])
+    rows = int(new.sum()) + 300
+    assert rows > 1024 * 256
+    _check(lens, new, table, rows, free, 1, "gathered")
+
+
 def test_negative_lengths_count_as_zero():
     lens = np.array([100, -5, 70, 30], np.int32)
     new = np.array([2, 3, -1, 30], np.int32)
