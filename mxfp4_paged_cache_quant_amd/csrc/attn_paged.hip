@@ -531,44 +531,67 @@ __global__ __launch_bounds__(HG * TH * kWave, kTile == 32 ? 2 : 1) void attn_ker
   }
 }
 
-// The splits' sums of one (row, head), kLatent / 4 lanes: 4 values each, the loads of
-// kBatch splits together (past the last one, its sums again).
-template <int kLatent, int kBatch>
-__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, Parts parts) {
-  constexpr int W = kLatent / 4;
-  const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) / W;
-  const int i = threadIdx.x % W;
+// The splits' sums of one (row, head) by kGroups * kLatent / 4 lanes: 4 values each, a group of
+// lanes takes every kGroups-th split, the loads of kBatch splits together (past the last
+// one, its sums again), and with more groups than one LDS joins those, one (row, head) a workgroup.
+template <int kLatent, int kBatch, int kGroups>
+__global__ __launch_bounds__(kGroups == 1 ? 256 : kGroups * kLatent / 4) void attn_join_kernel(AttnArgs a,
+                                                                                            Parts parts) {
+  constexpr int W = kLatent / 4, kThreads = kGroups == 1 ? 256 : kGroups * W;
+  __shared__ v4f sums[kGroups > 1 ? kGroups - 1 : 1][W];
+  __shared__ float2 tops[kGroups > 1 ? kGroups - 1 : 1][W];
+  const int64_t at = kGroups == 1 ? ((int64_t)blockIdx.x * kThreads + threadIdx.x) / W : (int64_t)blockIdx.x;
+  const int i = threadIdx.x % W, group = kGroups == 1 ? 0 : threadIdx.x / W;
   const int64_t r = (uint32_t)at / (uint32_t)a.H;      // rows * H < 2^31
   const int head = (int)(at - r * a.H);
   Row row;
-  if (r >= a.rows || !row_of(a, r, row)) return;
+  if (r >= a.rows || !row_of(a, r, row)) return;       // with groups uniform over the workgroup
   const int64_t first = r * parts.splits * parts.heads + head;
   v4f o = {0.f, 0.f, 0.f, 0.f};
   float top = neg_inf(), l = 0.f;
-  for (int s0 = 0; s0 < parts.splits; s0 += kBatch) {
+  // what another has summed: o * 2^-top, l * 2^-top
+  auto add = [&](float m, float ml, const v4f& x) __attribute__((always_inline)) {
+    if (ml == 0.f) return;                             // nothing seen: no sums written
+    const float f = __builtin_amdgcn_exp2f(m - (top == neg_inf() ? 0.f : top));
+    l += f * ml;
+    o += f * x;
+  };
+  auto raise = [&](float m) __attribute__((always_inline)) {
+    const float old = __builtin_amdgcn_exp2f(top - (m == neg_inf() ? 0.f : m));
+    o *= old;
+    l *= old;
+    top = m;
+  };
+  for (int s0 = group; s0 < parts.splits; s0 += kBatch * kGroups) {
     float2 ml[kBatch];
     v4f x[kBatch];
 #pragma unroll
     for (int s = 0; s < kBatch; ++s) {
-      const int64_t p = first + (int64_t)min(s0 + s, parts.splits - 1) * parts.heads;
+      const int64_t p = first + (int64_t)min(s0 + s * kGroups, parts.splits - 1) * parts.heads;
       ml[s] = *reinterpret_cast<const float2*>(parts.ml + 2 * p);
       x[s] = *reinterpret_cast<const v4f*>(parts.o + p * kLatent + 4 * i);
     }
     float m = top;
 #pragma unroll
     for (int s = 0; s < kBatch; ++s) m = fmaxf(m, ml[s].x);
-    const float ref = m == neg_inf() ? 0.f : m;
-    const float old = __builtin_amdgcn_exp2f(top - ref);
-    o *= old;
-    l *= old;
-    top = m;
+    raise(m);
 #pragma unroll
-    for (int s = 0; s < kBatch; ++s) {
-      if (s0 + s >= parts.splits || ml[s].y == 0.f) continue;   // nothing seen: no sums written
-      const float f = __builtin_amdgcn_exp2f(ml[s].x - ref);
-      l += f * ml[s].y;
-      o += f * x[s];
+    for (int s = 0; s < kBatch; ++s)
+      if (s0 + s * kGroups < parts.splits) add(ml[s].x, ml[s].y, x[s]);
+  }
+  if constexpr (kGroups > 1) {
+    if (group > 0) {
+      sums[group - 1][i] = o;
+      tops[group - 1][i] = make_float2(top, l);
     }
+    __syncthreads();
+    if (group > 0) return;
+    float m = top;
+#pragma unroll
+    for (int g = 0; g < kGroups - 1; ++g) m = fmaxf(m, tops[g][i].x);
+    raise(m);
+#pragma unroll
+    for (int g = 0; g < kGroups - 1; ++g) add(tops[g][i].x, tops[g][i].y, sums[g][i]);
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
   *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + r * a.out_row_stride +
@@ -653,11 +676,14 @@ hipError_t launch(const AttnArgs& a, void* workspace, hipStream_t stream) {
   // no loads beyond the splits that there are, as far as a power of two goes (2 splits of 64
   // rows, 128 heads: 10.2 us, 13.4 with eight loads; 4 of 32 rows: 8.8 and 9.9)
   if (p.splits <= 2)
-    hipLaunchKernelGGL((attn_join_kernel<kLatent, 2>), join, dim3(256), 0, stream, a, parts);
+    hipLaunchKernelGGL((attn_join_kernel<kLatent, 2, 1>), join, dim3(256), 0, stream, a, parts);
   else if (p.splits <= 4)
-    hipLaunchKernelGGL((attn_join_kernel<kLatent, 4>), join, dim3(256), 0, stream, a, parts);
+    hipLaunchKernelGGL((attn_join_kernel<kLatent, 4, 1>), join, dim3(256), 0, stream, a, parts);
+  else if (p.splits <= 8)
+    hipLaunchKernelGGL((attn_join_kernel<kLatent, 8, 1>), join, dim3(256), 0, stream, a, parts);
   else
-    hipLaunchKernelGGL((attn_join_kernel<kLatent, 8>), join, dim3(256), 0, stream, a, parts);
+    hipLaunchKernelGGL((attn_join_kernel<kLatent, 8, 4>), dim3((uint32_t)(a.rows * a.H)), dim3(4 * W), 0, stream,
+                       a, parts);
   return hipGetLastError();
 }
 
