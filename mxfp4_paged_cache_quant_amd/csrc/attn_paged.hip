@@ -53,7 +53,7 @@ namespace {
 
 constexpr int kRopeWidth = 64;
 constexpr int kCus = 256;
-constexpr int kMaxSplits = 64;
+constexpr int kMaxSplits = 128;
 constexpr float kSlack = 8.f;               // weights stay below 2^8 of the reference's
 
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
@@ -608,29 +608,31 @@ struct Plan {
   int splits;
 };
 
-// Few rows are split over the tokens, up to one workgroup for each CU.  A split costs its
-// share of the workspace's traffic (2 KB a head, written and read), so it takes 4 tiles
-// or more (16 rows of 2048 tokens, 32 heads: 21.0 us with 8 splits, 22.9 with 16), or 2
-// where even 64 workgroups do not come together (one such row: 15.5 us with 16 splits of
-// 32 heads); and the join of a row reads them one after the other (one row of 32768
-// tokens: 36 us with 64 splits, 43 with 128).
+// Few rows are split over the tokens, up to one workgroup for each CU (two of latent 128, whose
+// tiles leave the LDS room: 32 windows of 8192, 128 heads: 41.7 us, 45.5 with one).  A split
+// costs its share of the workspace's traffic (2 KB a head, written and read), so it takes 4
+// tiles or more (16 rows of 2048 tokens, 32 heads: 21.0 us with 8 splits, 22.9 with 16), or
+// 2 where even 64 workgroups do not come together (one such row: 15.3 us with 16 splits of
+// 32 heads, 16.5 with 8); one row of 131072 tokens, 64 heads, latent 128: 28 us with 128
+// splits, 41 with 64.
 // 64 heads a workgroup read the rows fewest times (32 rows of 2 x 6600 tokens, 128
 // heads: 91 us with 64, 132 with 32; 64 rows of 2048 tokens, 64 heads: 55 and 58); 32
 // heads spread a call over twice the CUs that would not fill them otherwise (one row:
-// 15.5 us, 19.1 with 64) or fill them with half the partial sums (32 rows of 2048 tokens,
+// 15.3 us, 17.5 with 64) or fill them with half the partial sums (32 rows of 2048 tokens,
 // 64 heads: 31 us with 4 splits, 34 with 64 heads and 8; 4 rows of 16384: 32 and 38).
 // Many rows: two workgroups of four waves a CU, 32 tokens at a time, whose phases do not
 // fall together (1024 rows of 2048 tokens, 64 heads: 312-328 us, 325-342 with one of
 // eight waves); with 200 rows, which do not fill both places, 128 us and 112.
-Plan plan_of(int64_t rows, int H, int64_t entries) {
+Plan plan_of(int64_t rows, int H, int latent, int64_t entries) {
   Plan p;
   const int64_t tiles = (entries + 63) / 64, quarter = std::min<int64_t>((tiles + 3) / 4, kMaxSplits);
+  const int64_t places = latent <= 128 ? 2 * kCus : kCus;
   p.group_heads = H <= 16 ? 16 : H <= 32 || rows * ((H + 31) / 32) * quarter <= 2 * kCus ? 32 : 64;
   p.heads = (H + p.group_heads - 1) / p.group_heads * p.group_heads;
   const int64_t units = rows * (p.heads / p.group_heads);
   p.tile = p.group_heads == 64 && units >= 2 * kCus ? 32 : 64;
   const int64_t shares = units * quarter <= 64 ? std::min<int64_t>((tiles + 1) / 2, kMaxSplits) : quarter;
-  p.splits = (int)std::max<int64_t>(1, std::min(kCus / std::max<int64_t>(units, 1), shares));
+  p.splits = (int)std::max<int64_t>(1, std::min(places / std::max<int64_t>(units, 1), shares));
   return p;
 }
 
@@ -640,7 +642,7 @@ int64_t ml_bytes(int64_t rows, const Plan& p) { return align256(rows * p.splits 
 
 template <int kLatent>
 hipError_t launch(const AttnArgs& a, void* workspace, hipStream_t stream) {
-  const Plan p = plan_of(a.rows, a.H, a.indices ? a.k : a.max_tokens);
+  const Plan p = plan_of(a.rows, a.H, kLatent, a.indices ? a.k : a.max_tokens);
   const int64_t cache_bytes = a.num_pages * kPage * (kLatent + kRopeWidth) * 2;
   const int64_t q_bytes = ((a.H - 1) * a.q_head_stride + kLatent + kRopeWidth) * 2;
   const bool small = cache_bytes <= kReach && q_bytes <= kReach;
@@ -690,7 +692,7 @@ hipError_t launch(const AttnArgs& a, void* workspace, hipStream_t stream) {
 }  // namespace
 
 int64_t attn_workspace_bytes(int64_t rows, int H, int latent, int64_t entries) {
-  const Plan p = plan_of(rows, H, entries);
+  const Plan p = plan_of(rows, H, latent, entries);
   if (p.splits == 1) return 0;
   return ml_bytes(rows, p) + rows * p.splits * p.heads * latent * 4;
 }

@@ -277,6 +277,13 @@ def test_long_windows_of_mixed_lengths():
     _check(c)
 
 
+@pytest.mark.parametrize("lens,H,latent,k", [([33000], 40, 128, 0), ([17000, 0, 100], 8, 512, 0), ([20000, 19000], 64, 256, 0),
+                                             ([5000], 3, 128, 4999), ([3000, 40], 20, 512, 1500)])
+def test_many_splits(lens, H, latent, k):
+    # up to 128 splits of a row, joined by several groups of lanes; splits that see nothing among them
+    _check(_case(H, lens, H=H, latent=latent, k=k))
+
+
 def test_same_call_gives_the_same_bits():
     c = _case(24, [3000, 900, 5000, 64], H=40, latent=512)
     d = _to_dev(c)
