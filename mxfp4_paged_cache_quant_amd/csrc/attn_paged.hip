@@ -676,7 +676,9 @@ hipError_t launch(const AttnArgs& a, void* workspace, hipStream_t stream) {
   const int64_t threads = a.rows * a.H * W;
   const dim3 join((uint32_t)((threads + 255) / 256));
   // no loads beyond the splits that there are, as far as a power of two goes (2 splits of 64
-  // rows, 128 heads: 10.2 us, 13.4 with eight loads; 4 of 32 rows: 8.8 and 9.9)
+  // rows, 128 heads: 10.2 us, 13.4 with eight loads; 4 of 32 rows: 8.8 and 9.9), and more lanes
+  // where few rows have many splits (one row of 32768 tokens, 64 heads, 64 splits: 27.6 us
+  // with four groups, 33.5 with one; 16 splits: 15.1 and 15.4)
   if (p.splits <= 2)
     hipLaunchKernelGGL((attn_join_kernel<kLatent, 2, 1>), join, dim3(256), 0, stream, a, parts);
   else if (p.splits <= 4)
