@@ -38,8 +38,12 @@
 // Places of a tile that hold no visible token read as zeros and get weight 0, so
 // nothing that a masked place holds reaches a sum.
 //
-// The weights are rounded to bf16 for the second product (relative error 2^-8 at most,
-// as the cached values' own); l and lse take them unrounded.
+// The weights go to the second product in bf16; l and lse take them unrounded.  Groups of 16
+// and 32 heads, which are bound by latency, take them in two parts, the rounded weight and
+// what rounding left (relative error 2^-16; the output's error is its own rounding's:
+// 3-8% of the time, 16 rows of 2048 tokens 23.9 -> 24.9 us).  Groups of 64, whose calls fill
+// the card, take one part (2^-8 at most, as the cached values' own: with 2048 tokens the
+// output's error is 1.24 times its rounding's; two parts are half as many products again).
 //
 // Few rows: the tokens are split over workgroups, each leaving its unscaled sums with
 // m and l in the workspace, and a second launch joins them.
@@ -73,6 +77,9 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   const v2bf r = {(__bf16)a, (__bf16)b};
   return __builtin_bit_cast(uint32_t, r);
 }
+
+__device__ __forceinline__ float low_half(uint32_t x) { return __uint_as_float(x << 16); }
+__device__ __forceinline__ float high_half(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
 
 // LDS place of a 16-byte chunk: chunk c of token t's row is stored at c ^ swz(t).
 // Latent rows are multiples of 256 bytes, so their banks repeat every 16 chunks and swz
@@ -225,6 +232,8 @@ __global__ __launch_bounds__(HG * TH * kWave, kTile == 32 ? 2 : 1) void attn_ker
   constexpr int NV = kLatent / 16;                     // 16-value parts of the output
   constexpr int LC = kLatent / 8;                      // 16-byte chunks of a latent row
   constexpr int kAhead = kSmall ? 3 : 2;               // operand steps in flight from LDS, as registers allow
+  constexpr bool kFine = HG <= 2;                      // the weights in two bf16 parts
+  constexpr int kValuesAhead = kFine ? 4 : kAhead;
   constexpr int kMine = kTile / kWaves;                // rows that a wave copies
   constexpr int kLatentBytes = kTile * kLatent * 2, kTileBytes = kTile * kRow * 2;
   using Copy = TileCopy<kLatent, kTile, kMine, kSmall>;
@@ -343,7 +352,7 @@ __global__ __launch_bounds__(HG * TH * kWave, kTile == 32 ? 2 : 1) void attn_ker
     }
     m = m2;
     const float ref = m == neg_inf() ? 0.f : m;      // no token yet: every weight 0
-    uint32_t w[NT][2];
+    uint32_t w[NT][2], rest[NT][2];                  // rest: what rounding left of the weights
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       float p[4];
@@ -354,31 +363,45 @@ __global__ __launch_bounds__(HG * TH * kWave, kTile == 32 ? 2 : 1) void attn_ker
       }
       w[t][0] = pack2(p[0], p[1]);
       w[t][1] = pack2(p[2], p[3]);
+      if constexpr (kFine) {
+        rest[t][0] = pack2(p[0] - low_half(w[t][0]), p[1] - high_half(w[t][0]));
+        rest[t][1] = pack2(p[2] - low_half(w[t][1]), p[3] - high_half(w[t][1]));
+      }
     }
     // values: lane 4j + c of a 16-lane group reads tokens 4g + j, values 4c..4c+3, and
     // gets tokens 4g..4g+3 of value n
     const int vl = fresh_lane(), vn = vl & 15, vt = 4 * (vl >> 4) + (vn >> 2);
     const int val = (base + vt) * (kLatent * 2) + ((((vn >> 1) & 1) ^ swz<LC>(vt)) << 4) + 8 * (vn & 1);
-    v4s y[kAhead][NT];
+    v4s y[kValuesAhead][NT];
     auto values = [&](int v, v4s (&x)[NT]) __attribute__((always_inline)) {
 #pragma unroll
       for (int t = 0; t < NT; ++t)
         x[t] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((MXIDX_LDS v4s*)(
             buf + (val ^ ((v & 7) << 5)) + (v >> 3) * 256 + t * 16 * (kLatent * 2)));
     };
-#pragma unroll
-    for (int v = 0; v < kAhead; ++v) values(v, y[v]);
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      __builtin_amdgcn_sched_barrier(0);
-      const v4s(&z)[NT] = y[v % kAhead];
+    auto product = [&](const v4s (&z)[NT], const uint32_t (&by)[NT][2], v4f c) __attribute__((always_inline)) {
       if constexpr (NT == 1)
-        o[v] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(z[0], __builtin_bit_cast(v4s, uint2{w[0][0], w[0][1]}),
-                                                          o[v], 0, 0, 0);
+        return __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(
+            z[0], __builtin_bit_cast(v4s, uint2{by[0][0], by[0][1]}), c, 0, 0, 0);
       else
-        o[v] = mfma_bf16(__builtin_shufflevector(z[0], z[NT - 1], 0, 1, 2, 3, 4, 5, 6, 7),
-                         __builtin_bit_cast(v8s, uint4{w[0][0], w[0][1], w[NT - 1][0], w[NT - 1][1]}), o[v]);
-      if (v + kAhead < NV) values(v + kAhead, y[v % kAhead]);
+        return mfma_bf16(__builtin_shufflevector(z[0], z[NT - 1], 0, 1, 2, 3, 4, 5, 6, 7),
+                         __builtin_bit_cast(v8s, uint4{by[0][0], by[0][1], by[NT - 1][0], by[NT - 1][1]}), c);
+    };
+#pragma unroll
+    for (int v = 0; v < kValuesAhead; ++v) values(v, y[v]);
+    constexpr int kStep = kFine ? 2 : 1;             // parts of the output at a time, so that no sum waits
+#pragma unroll
+    for (int v = 0; v < NV; v += kStep) {
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int i = 0; i < kStep; ++i) o[v + i] = product(y[(v + i) % kValuesAhead], w, o[v + i]);
+      if constexpr (kFine) {
+#pragma unroll
+        for (int i = 0; i < kStep; ++i) o[v + i] = product(y[(v + i) % kValuesAhead], rest, o[v + i]);
+      }
+#pragma unroll
+      for (int i = 0; i < kStep; ++i)
+        if (v + i + kValuesAhead < NV) values(v + i + kValuesAhead, y[(v + i) % kValuesAhead]);
     }
     __builtin_amdgcn_sched_barrier(0);
   };
