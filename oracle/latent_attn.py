@@ -24,7 +24,8 @@ def visible_rows(r, block_table, num_pages, seq, ks, ke, indices, max_tokens):
     return page[ok] * PAGE + tok[ok] % PAGE
 
 
-def attn(q, cache, block_table, ke, scale, indices=None, ks=None, row_seq=None, max_tokens=None):
+def attn(q, cache, block_table, ke, scale, indices=None, ks=None, row_seq=None, max_tokens=None,
+         weight_rounding=2.0 ** -8):
     """(out, lse, out_bound, lse_bound) as float64; rows of no sequence are NaN.
 
     The bounds follow the definition's error in the arithmetic it is computed in.
@@ -32,8 +33,8 @@ def attn(q, cache, block_table, ke, scale, indices=None, ks=None, row_seq=None, 
       |ds_j|  <= d u scale sum|q c_j| + 4 u |s_j|           (fp32 sum; scaling, base change, exp)
       |dlse|  <= max|ds| + (2n + 32) u + 4 u |lse|          (n positive terms, each added with
                                                              a rescaling: two roundings)
-      |dout|  <= (h + 2 max|ds| + (4n + 64) u) sum_j p_j |c_j| + h |out|
-    (the weights' rounding to bf16; score and sum errors in weight and total; the output's
+      |dout|  <= (w + 2 max|ds| + (4n + 64) u) sum_j p_j |c_j| + h |out|
+    (the weights' rounding w = weight_rounding: h for one bf16 part, h^2 for two; score and sum errors in weight and total; the output's
     rounding)."""
     q, rows = np.asarray(q, np.float64), np.asarray(cache, np.float64).reshape(-1, cache.shape[-1])
     R, H, d = q.shape
@@ -62,5 +63,5 @@ def attn(q, cache, block_table, ke, scale, indices=None, ks=None, row_seq=None, 
         out[r], lse[r] = p @ c[:, :L], (top + np.log(total))[:, 0]
         ds = (d * u * abs(scale) * (np.abs(q[r]) @ np.abs(c).T) + 4 * u * np.abs(s)).max(-1)
         lse_b[r] = ds + (2 * n + 32) * u + 4 * u * np.abs(lse[r])
-        out_b[r] = (h + 2 * ds + (4 * n + 64) * u)[:, None] * (p @ np.abs(c[:, :L])) + h * np.abs(out[r])
+        out_b[r] = (weight_rounding + 2 * ds + (4 * n + 64) * u)[:, None] * (p @ np.abs(c[:, :L])) + h * np.abs(out[r])
     return out, lse, out_b, lse_b

@@ -180,6 +180,17 @@ def test_peaked_flat_and_far_scores(q_scale, lift):
     _check(c)
 
 
+@pytest.mark.parametrize("H,latent", [(1, 512), (16, 128), (20, 512), (32, 256), (64, 512)])
+@pytest.mark.parametrize("k", [0, 120])
+def test_weights_of_few_rows_in_two_parts(H, latent, k):
+    # a weight's rounding leaves 2^-8 of it at most, and rounding that 2^-8 of what is left
+    c = _case(H, [300, 65, 1000], H=H, latent=latent, k=k)
+    got = mx.attn_paged(**_to_dev(c, float("nan")))
+    torch.cuda.synchronize()
+    _close(got, oattn.attn(c["q"], c["cache"], c["bt"], c["ke"], c["scale"], c["indices"], c["ks"], c["row_seq"],
+                           weight_rounding=2.0 ** -16))
+
+
 def test_growing_maximum():
     # each token scores above all before it: every step rescales what was summed
     c = _case(18, [500], H=32, latent=128, q_scale=0.5)
