@@ -683,8 +683,9 @@ int idx_latent_insert(const void* kv, int dtype, int64_t T, int64_t kv_row_strid
  *        initialization, scratch after the call, not shared by calls that may run at the
  *        same time.  May be NULL where that size is 0.
  * Products are exact, sums and softmax statistics fp32; the softmax weights take the second
- * product in bf16 (calls of many rows with more than 32 heads) or in two bf16 parts, 16 bits
- * (the others); the statistics, and so lse, take them unrounded; the output is rounded once. */
+ * product in two bf16 parts (16 bits); the statistics, and so lse, take them unrounded; the output
+ * is rounded once.  Equal calls give equal bits.  The order of a row's sums depends on rows, H and
+ * k (with indices) or max_tokens, so its last bits may differ between calls that differ in these. */
 size_t idx_attn_workspace_bytes(int64_t rows, int H, int latent, int64_t entries);
 int idx_attn_paged(const void* q, int64_t q_row_stride, int64_t q_head_stride, int64_t rows, int H,
                    int latent, const void* cache, int64_t num_pages, int page_size,

@@ -38,12 +38,12 @@
 // Places of a tile that hold no visible token read as zeros and get weight 0, so
 // nothing that a masked place holds reaches a sum.
 //
-// The weights go to the second product in bf16; l and lse take them unrounded.  Groups of 16
-// and 32 heads, which are bound by latency, take them in two parts, the rounded weight and
-// what rounding left (relative error 2^-16; the output's error is its own rounding's:
-// 3-8% of the time, 16 rows of 2048 tokens 23.9 -> 24.9 us).  Groups of 64, whose calls fill
-// the card, take one part (2^-8 at most, as the cached values' own: with 2048 tokens the
-// output's error is 1.24 times its rounding's; two parts are half as many products again).
+// The weights go to the second product in two bf16 parts, the rounded weight and what rounding
+// left (2^-16 of it at most); l and lse take them unrounded.  The output's error is then its own
+// rounding's whatever the call's sizes.  With one part (2^-8) it is 1.24 times that over 2048
+// tokens, and a row that one token dominates is off by that token's rounding, since the
+// reference is no power of two from it.  Two parts are half as many products again: 1024 rows of 2048
+// tokens, 64 heads, 310 -> 363 us; 32 windows of 6600, 128 heads, 90 -> 101; 16 rows of 2048 24 -> 25.
 //
 // Few rows: the tokens are split over workgroups, each leaving its unscaled sums with
 // m and l in the workspace, and a second launch joins them.
@@ -232,8 +232,7 @@ __global__ __launch_bounds__(HG * TH * kWave, kTile == 32 ? 2 : 1) void attn_ker
   constexpr int NV = kLatent / 16;                     // 16-value parts of the output
   constexpr int LC = kLatent / 8;                      // 16-byte chunks of a latent row
   constexpr int kAhead = kSmall ? 3 : 2;               // operand steps in flight from LDS, as registers allow
-  constexpr bool kFine = HG <= 2;                      // the weights in two bf16 parts
-  constexpr int kValuesAhead = kFine ? 4 : kAhead;
+  constexpr int kValuesAhead = HG <= 2 ? 4 : kAhead;
   constexpr int kMine = kTile / kWaves;                // rows that a wave copies
   constexpr int kLatentBytes = kTile * kLatent * 2, kTileBytes = kTile * kRow * 2;
   using Copy = TileCopy<kLatent, kTile, kMine, kSmall>;
@@ -363,10 +362,8 @@ __global__ __launch_bounds__(HG * TH * kWave, kTile == 32 ? 2 : 1) void attn_ker
       }
       w[t][0] = pack2(p[0], p[1]);
       w[t][1] = pack2(p[2], p[3]);
-      if constexpr (kFine) {
-        rest[t][0] = pack2(p[0] - low_half(w[t][0]), p[1] - high_half(w[t][0]));
-        rest[t][1] = pack2(p[2] - low_half(w[t][1]), p[3] - high_half(w[t][1]));
-      }
+      rest[t][0] = pack2(p[0] - low_half(w[t][0]), p[1] - high_half(w[t][0]));
+      rest[t][1] = pack2(p[2] - low_half(w[t][1]), p[3] - high_half(w[t][1]));
     }
     // values: lane 4j + c of a 16-lane group reads tokens 4g + j, values 4c..4c+3, and
     // gets tokens 4g..4g+3 of value n
@@ -389,16 +386,16 @@ __global__ __launch_bounds__(HG * TH * kWave, kTile == 32 ? 2 : 1) void attn_ker
     };
 #pragma unroll
     for (int v = 0; v < kValuesAhead; ++v) values(v, y[v]);
-    constexpr int kStep = kFine ? 2 : 1;             // parts of the output at a time, so that no sum waits
+    // parts of the output at a time: two where a wave is alone on its SIMD, so that no sum waits
+    // (1024 rows of 2048 tokens, 64 heads: 363 us with one, 367 with two)
+    constexpr int kStep = HG <= 2 ? 2 : 1;
 #pragma unroll
     for (int v = 0; v < NV; v += kStep) {
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int i = 0; i < kStep; ++i) o[v + i] = product(y[(v + i) % kValuesAhead], w, o[v + i]);
-      if constexpr (kFine) {
 #pragma unroll
-        for (int i = 0; i < kStep; ++i) o[v + i] = product(y[(v + i) % kValuesAhead], rest, o[v + i]);
-      }
+      for (int i = 0; i < kStep; ++i) o[v + i] = product(y[(v + i) % kValuesAhead], rest, o[v + i]);
 #pragma unroll
       for (int i = 0; i < kStep; ++i)
         if (v + i + kValuesAhead < NV) values(v + i + kValuesAhead, y[(v + i) % kValuesAhead]);

@@ -25,7 +25,7 @@ def visible_rows(r, block_table, num_pages, seq, ks, ke, indices, max_tokens):
 
 
 def attn(q, cache, block_table, ke, scale, indices=None, ks=None, row_seq=None, max_tokens=None,
-         weight_rounding=2.0 ** -8):
+         weight_rounding=2.0 ** -16):
     """(out, lse, out_bound, lse_bound) as float64; rows of no sequence are NaN.
 
     The bounds follow the definition's error in the arithmetic it is computed in.
@@ -34,8 +34,8 @@ def attn(q, cache, block_table, ke, scale, indices=None, ks=None, row_seq=None, 
       |dlse|  <= max|ds| + (2n + 32) u + 4 u |lse|          (n positive terms, each added with
                                                              a rescaling: two roundings)
       |dout|  <= (w + 2 max|ds| + (4n + 64) u) sum_j p_j |c_j| + h |out|
-    (the weights' rounding w = weight_rounding: h for one bf16 part, h^2 for two; score and sum errors in weight and total; the output's
-    rounding)."""
+    (the weights' rounding w = weight_rounding: two bf16 parts, h^2; score and sum errors in weight
+    and total; the output's rounding)."""
     q, rows = np.asarray(q, np.float64), np.asarray(cache, np.float64).reshape(-1, cache.shape[-1])
     R, H, d = q.shape
     L = d - 64
