@@ -1219,6 +1219,8 @@ def attn_paged(q, cache, block_table, ke, scale, indices=None, ks=None, row_seq=
             workspace = _empty(stream, need, torch.uint8, device)
     if workspace is not None:
         wp, wb = _on(device, workspace, "workspace", torch.uint8), workspace.numel()
+        if not workspace.is_contiguous():      # an expanded view has less memory than numel
+            raise MxidxError("workspace must be contiguous")
     _call("idx_attn_paged", device, stream, qp, q_strides[0], q_strides[1], rows, H, latent, cp,
           num_pages, PAGE_SIZE, bp, stride, B, rp, kp, ep, ip, istride, k, max_tokens, scale, op,
           strides[0], strides[1], lp, wp, wb)
