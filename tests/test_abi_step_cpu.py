@@ -210,6 +210,22 @@ def test_attn_workspace(L):
         assert L.idx_attn_paged(*_args(ATTN, most=0, table=None, pages=0, cache=None)) == ERR_NO_DEVICE
 
 
+# sizes whose rows are split over the tokens: the partial sums need the workspace
+SPLIT = [dict(k=2048, idx_stride=2048), dict(idx=None, most=1000), dict(k=2048, idx_stride=2048, H=64, qs=64 * 576, os=64 * 512)]
+
+
+@pytest.mark.parametrize("sizes", SPLIT)
+def test_attn_refuses_a_workspace_that_does_not_hold_the_partial_sums(L, sizes):
+    call = {**ATTN, **sizes}
+    need = L.idx_attn_workspace_bytes(call["rows"], call["H"], call["latent"],
+                                      call["k"] if call["idx"] else call["most"])
+    assert need > 0
+    for change in (dict(ws=None), dict(ws=0x20010), dict(ws=0x20080), dict(wb=need - 1), dict(wb=0)):
+        assert L.idx_attn_paged(*_args(call, **change)) == ERR_ARG, change
+    if _no_gpu():
+        assert L.idx_attn_paged(*_args(call, wb=need)) == ERR_NO_DEVICE
+
+
 def test_wrappers_refuse_host_tensors():
     import torch
     z = torch.zeros
