@@ -681,12 +681,16 @@ int idx_latent_insert(const void* kv, int dtype, int64_t T, int64_t kv_row_strid
  *   workspace: device memory of at least idx_attn_workspace_bytes(rows, H, latent, k with
  *        indices, else max_tokens) bytes, 256-byte aligned, as for idx_topk_ws: no
  *        initialization, scratch after the call, not shared by calls that may run at the
- *        same time.  May be NULL where that size is 0.
+ *        same time.  May be NULL where that size is 0.  That size does not grow with its
+ *        arguments (256 rows of 64 heads and 2048 tokens need none, 16 such rows 16.8 MB):
+ *        idx_attn_workspace_max_bytes is enough for every call of the same latent with up
+ *        to so many rows, heads and entries (at most 34 MB), and grows with each.
  * Products are exact, sums and softmax statistics fp32; the softmax weights take the second
  * product in two bf16 parts (16 bits); the statistics, and so lse, take them unrounded; the output
  * is rounded once.  Equal calls give equal bits.  The order of a row's sums depends on rows, H and
  * k (with indices) or max_tokens, so its last bits may differ between calls that differ in these. */
 size_t idx_attn_workspace_bytes(int64_t rows, int H, int latent, int64_t entries);
+size_t idx_attn_workspace_max_bytes(int64_t rows, int H, int latent, int64_t entries);
 int idx_attn_paged(const void* q, int64_t q_row_stride, int64_t q_head_stride, int64_t rows, int H,
                    int latent, const void* cache, int64_t num_pages, int page_size,
                    const int32_t* block_table, int64_t bt_row_stride, int B,

@@ -23,7 +23,7 @@ __all__ = [
     "quantize_fp8", "insert_fp8", "gather_fp8", "logits_prefill_fp8", "logits_paged_fp8",
     "logits_paged_insert_fp8",
     "StepMap", "step_map", "norm_rope", "latent_insert", "attn_paged", "attn_workspace_bytes",
-    "attn_workspace", "LATENT_ROPE", "LATENT_DIMS",
+    "attn_workspace_max_bytes", "attn_workspace", "LATENT_ROPE", "LATENT_DIMS",
     "FP8_ROW_BYTES", "FP8_SCALE_F32", "FP8_SCALE_POW2",
     "HEAD_DIM", "ROW_BYTES", "PAGE_SIZE", "TOPK_MAX", "EXPORTS",
 ]
@@ -130,6 +130,7 @@ EXPORTS = {
                                  _c_void_p, _c_void_p, _c_void_p, _i64, _int, _c_void_p, _int, _i64,
                                  _i64, _c_void_p, _i64, _i64, _c_void_p]),
     "idx_attn_workspace_bytes": (ctypes.c_size_t, [_i64, _int, _int, _i64]),
+    "idx_attn_workspace_max_bytes": (ctypes.c_size_t, [_i64, _int, _int, _i64]),
     "idx_attn_paged": (_int, [_c_void_p, _i64, _i64, _i64, _int, _int, _c_void_p, _i64, _int,
                               _c_void_p, _i64, _int, _c_void_p, _c_void_p, _c_void_p, _c_void_p,
                               _i64, _int, _i64, _float, _c_void_p, _i64, _i64, _c_void_p, _c_void_p,
@@ -1150,14 +1151,21 @@ def latent_insert(kv, slot_mapping, cache, cos, sin, mode="neox", positions=None
 
 
 def attn_workspace_bytes(rows, heads, latent, entries):
-    """Workspace bytes of attn_paged; entries: k with indices, else max_tokens (0: no workspace)."""
+    """Workspace bytes of attn_paged; entries: k with indices, else max_tokens (0: no workspace).
+    Fewer rows, heads or entries may need more."""
     return int(lib().idx_attn_workspace_bytes(rows, heads, latent, entries))
 
 
+def attn_workspace_max_bytes(rows, heads, latent, entries):
+    """Workspace bytes that are enough for attn_paged calls with up to so many rows, heads and entries."""
+    return int(lib().idx_attn_workspace_max_bytes(rows, heads, latent, entries))
+
+
 def attn_workspace(rows, heads, latent, entries, device="cuda"):
-    """A workspace for attn_paged: reusable, not by calls that may run at the same time."""
+    """A workspace for attn_paged calls with up to so many rows, heads and entries: reusable, not by
+    calls that may run at the same time."""
     torch = _torch()
-    return torch.empty(max(attn_workspace_bytes(rows, heads, latent, entries), 1),
+    return torch.empty(max(attn_workspace_max_bytes(rows, heads, latent, entries), 1),
                        dtype=torch.uint8, device=device)
 
 

@@ -695,6 +695,11 @@ size_t idx_attn_workspace_bytes(int64_t rows, int H, int latent, int64_t entries
   return (size_t)mxidx::attn_workspace_bytes(rows, H, latent, entries);
 }
 
+size_t idx_attn_workspace_max_bytes(int64_t rows, int H, int latent, int64_t entries) {
+  if (!attn_sizes_ok(rows, H, latent, entries)) return 0;
+  return (size_t)mxidx::attn_workspace_max_bytes(rows, H, latent, entries);
+}
+
 int idx_attn_paged(const void* q, int64_t q_row_stride, int64_t q_head_stride, int64_t rows, int H,
                    int latent, const void* cache, int64_t num_pages, int page_size,
                    const int32_t* block_table, int64_t bt_row_stride, int B,

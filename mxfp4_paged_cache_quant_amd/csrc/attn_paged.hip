@@ -643,10 +643,12 @@ struct Plan {
 // Many rows: two workgroups of four waves a CU, 32 tokens at a time, whose phases do not
 // fall together (1024 rows of 2048 tokens, 64 heads: 312-328 us, 325-342 with one of
 // eight waves); with 200 rows, which do not fill both places, 128 us and 112.
+int64_t split_places(int latent) { return latent <= 128 ? 2 * kCus : kCus; }
+
 Plan plan_of(int64_t rows, int H, int latent, int64_t entries) {
   Plan p;
   const int64_t tiles = (entries + 63) / 64, quarter = std::min<int64_t>((tiles + 3) / 4, kMaxSplits);
-  const int64_t places = latent <= 128 ? 2 * kCus : kCus;
+  const int64_t places = split_places(latent);
   p.group_heads = H <= 16 ? 16 : H <= 32 || rows * ((H + 31) / 32) * quarter <= 2 * kCus ? 32 : 64;
   p.heads = (H + p.group_heads - 1) / p.group_heads * p.group_heads;
   const int64_t units = rows * (p.heads / p.group_heads);
@@ -658,7 +660,9 @@ Plan plan_of(int64_t rows, int H, int latent, int64_t entries) {
 
 int64_t align256(int64_t x) { return (x + 255) / 256 * 256; }
 
-int64_t ml_bytes(int64_t rows, const Plan& p) { return align256(rows * p.splits * p.heads * 8); }
+// Of the partial sums of so many (row, split, head).
+int64_t ml_bytes(int64_t parts) { return align256(parts * 8); }
+int64_t part_bytes(int64_t parts, int latent) { return ml_bytes(parts) + parts * latent * 4; }
 
 template <int kLatent>
 hipError_t launch(const AttnArgs& a, void* workspace, hipStream_t stream) {
@@ -670,7 +674,7 @@ hipError_t launch(const AttnArgs& a, void* workspace, hipStream_t stream) {
               small ? (uint32_t)cache_bytes : 0, small ? (uint32_t)q_bytes : 0};
   if (p.splits > 1) {
     parts.ml = static_cast<float*>(workspace);
-    parts.o = reinterpret_cast<float*>(static_cast<char*>(workspace) + ml_bytes(a.rows, p));
+    parts.o = reinterpret_cast<float*>(static_cast<char*>(workspace) + ml_bytes(a.rows * p.splits * p.heads));
   }
   const dim3 grid((uint32_t)(a.rows * (p.heads / p.group_heads) * p.splits));
 #define MXIDX_ATTN(heads_, tile_, hg, th)                                                     \
@@ -715,8 +719,15 @@ hipError_t launch(const AttnArgs& a, void* workspace, hipStream_t stream) {
 
 int64_t attn_workspace_bytes(int64_t rows, int H, int latent, int64_t entries) {
   const Plan p = plan_of(rows, H, latent, entries);
-  if (p.splits == 1) return 0;
-  return ml_bytes(rows, p) + rows * p.splits * p.heads * latent * 4;
+  return p.splits == 1 ? 0 : part_bytes(rows * p.splits * p.heads, latent);
+}
+
+// Split rows come to at most `places` workgroups of the largest group that so few heads take, and
+// to so many splits of the heads rounded up to it.
+int64_t attn_workspace_max_bytes(int64_t rows, int H, int latent, int64_t entries) {
+  const int64_t group = H <= 16 ? 16 : H <= 32 ? 32 : 64, heads = (H + group - 1) / group * group;
+  const int64_t tiles = (entries + 63) / 64, splits = std::min<int64_t>((tiles + 1) / 2, kMaxSplits);
+  return splits <= 1 ? 0 : part_bytes(std::min(split_places(latent) * group, rows * heads * splits), latent);
 }
 
 hipError_t launch_attn_paged(const AttnArgs& a, int latent, void* workspace, hipStream_t stream) {

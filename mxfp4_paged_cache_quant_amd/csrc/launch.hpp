@@ -222,6 +222,8 @@ struct AttnArgs {
 };
 // Workspace bytes for rows whose windows (or lists) hold up to `entries` tokens.
 int64_t attn_workspace_bytes(int64_t rows, int H, int latent, int64_t entries);
+// The same, of any call with up to so many rows, heads and entries.
+int64_t attn_workspace_max_bytes(int64_t rows, int H, int latent, int64_t entries);
 hipError_t launch_attn_paged(const AttnArgs& a, int latent, void* workspace, hipStream_t stream);
 
 }  // namespace mxidx

@@ -226,6 +226,33 @@ def test_attn_refuses_a_workspace_that_does_not_hold_the_partial_sums(L, sizes):
         assert L.idx_attn_paged(*_args(call, wb=need)) == ERR_NO_DEVICE
 
 
+@pytest.mark.parametrize("latent", [128, 256, 512])
+def test_attn_workspace_of_the_largest_call_holds_the_smaller_ones(L, latent):
+    rows = [1, 2, 3, 7, 16, 33, 64, 128, 129, 200, 256, 257, 512, 1024, 5000]
+    heads = [1, 8, 16, 17, 32, 33, 64, 65, 96, 128]
+    entries = [0, 1, 64, 65, 128, 129, 192, 256, 257, 1000, 2048, 8192, 40000, 131072, 1 << 30]
+    most, size = L.idx_attn_workspace_max_bytes, {}
+    for r in rows:
+        for h in heads:
+            for e in entries:
+                size[r, h, e] = L.idx_attn_workspace_bytes(r, h, latent, e)
+                assert size[r, h, e] <= most(r, h, latent, e), (r, h, e)
+    for r in rows:                       # and it grows with each of them
+        for h in heads:
+            for e0, e1 in zip(entries, entries[1:]):
+                assert most(r, h, latent, e0) <= most(r, h, latent, e1)
+    for r0, r1 in zip(rows, rows[1:]):
+        assert all(most(r0, h, latent, e) <= most(r1, h, latent, e) for h in heads for e in entries)
+    for h0, h1 in zip(heads, heads[1:]):
+        assert all(most(r, h0, latent, e) <= most(r, h1, latent, e) for r in rows for e in entries)
+    assert max(most(r, h, latent, e) for r in rows for h in heads for e in entries) < 34 << 20
+    # what a program keeps for its largest batch serves every batch
+    kept = mx.attn_workspace(256, 64, latent, 2048, device="cpu").numel()
+    assert kept >= max(size[r, h, e] for r, h, e in size if r <= 256 and h <= 64 and e <= 2048)
+    for bad in ((-1, 8, latent, 100), (4, 0, latent, 100), (4, 8, 500, 100), (4, 8, latent, -1)):
+        assert most(*bad) == 0
+
+
 def test_wrappers_refuse_host_tensors():
     import torch
     z = torch.zeros
