@@ -156,8 +156,8 @@ struct Parts {
 };
 
 // 16 bytes a lane to LDS, at dst + 16 * lane.
-__device__ __forceinline__ void copy16(__amdgpu_buffer_rsrc_t rs, MXIDX_LDS uint8_t* dst, int offset) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (MXIDX_LDS void*)dst, 16, offset, 0, 0, 0);
+__device__ __forceinline__ void copy16(__amdgpu_buffer_rsrc_t rs, MXIDX_LDS uint8_t* dst, uint32_t offset) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (MXIDX_LDS void*)dst, 16, (int)offset, 0, 0, 0);
 }
 
 // The copy of a tile's rows to LDS, kMine of them by each wave, in kPieces parts that
@@ -192,8 +192,9 @@ struct TileCopy {
                                               int offset, int ln) {
     const int t = t0 + (kPer == 1 ? 0 : ln / C);
     const int row = kPer == 1 ? __builtin_amdgcn_readlane(rows, t) : __builtin_amdgcn_ds_bpermute(4 * t, rows);
+    // unsigned: a row of a cache above 2 GiB may begin below 2^31 and end above
     copy16(buffer_rsrc(src.base, (int)src.bytes), dst + t0 * C * 16,
-           row + offset + (((ln % C) ^ swz<C>(t)) << 4));
+           (uint32_t)row + (uint32_t)offset + (uint32_t)(((ln % C) ^ swz<C>(t)) << 4));
   }
 
   // One row, its latent part and its positional one, from a descriptor of its own.

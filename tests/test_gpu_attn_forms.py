@@ -54,3 +54,32 @@ def test_one_late_token_outweighs_the_others(rows, H, lift):
     got = mx.attn_paged(**_to_dev(c, float("nan")))
     torch.cuda.synchronize()
     _rows_close(got, c, rows, np.unique(np.linspace(0, rows - 1, 7).astype(np.int64)))
+
+
+# rows of one sequence x heads -> 16, 32 and 64 heads a workgroup, the last with 64- and 32-token tiles and
+# with the tokens split
+FORMS = [(3, 12), (200, 16), (3, 32), (200, 30), (130, 128), (520, 64), (60, 128)]
+
+
+@pytest.mark.parametrize("latent", [128, 256, 512])
+@pytest.mark.parametrize("over", [0, 1])
+@pytest.mark.parametrize("rows,H", FORMS)
+@pytest.mark.parametrize("k", [0, 600])
+def test_rows_on_both_sides_of_2_and_4_gib(latent, over, rows, H, k):
+    # the largest cache whose rows 32-bit offsets reach, and one page more: pages around byte 2^31
+    # (one of whose rows begins 128 bytes below it), the last ones and others; NaN in all the rest
+    page_bytes = 64 * (latent + 64) * 2
+    pages = 0xfffe0000 // page_bytes + over
+    middle = (1 << 31) // page_bytes
+    used = np.array([pages - 1, 0, middle, middle + 1, middle - 1, pages - 2, 1, pages // 3], np.int32)
+    n = 500 if rows > 60 else 1400
+    used = np.concatenate([used, np.arange(10, 10 + 22 - len(used), dtype=np.int32)])[:(n + 63) // 64]
+    c = _case(rows + H, [n], next_n=rows, H=H, latent=latent, k=k, q_scale=0.5)
+    d = _to_dev(c)
+    d["cache"] = torch.full((pages, 64, latent + 64), float("nan"), dtype=torch.bfloat16, device="cuda")
+    vals = torch.from_numpy(c["cache"][c["bt"][0]]).to(torch.bfloat16).cuda()
+    d["cache"][torch.from_numpy(used.astype(np.int64)).cuda()] = vals
+    d["block_table"] = dev(used[None])
+    got = mx.attn_paged(**d)
+    torch.cuda.synchronize()
+    _rows_close(got, c, rows, np.unique(np.linspace(0, rows - 1, 9).astype(np.int64)))
