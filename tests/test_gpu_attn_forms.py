@@ -83,3 +83,15 @@ def test_rows_on_both_sides_of_2_and_4_gib(latent, over, rows, H, k):
     got = mx.attn_paged(**d)
     torch.cuda.synchronize()
     _rows_close(got, c, rows, np.unique(np.linspace(0, rows - 1, 9).astype(np.int64)))
+
+
+@pytest.mark.parametrize("latent", [128, 256, 512])
+@pytest.mark.parametrize("H", [5, 16, 17, 32])
+@pytest.mark.parametrize("n,k", [(1100, 0), (1100, 700), (70, 0), (2100, 2048)])
+def test_prefill_of_few_heads(latent, H, n, k):
+    # whole rows of up to 33 tiles in groups of 16 and 32 heads: more rows than workgroups that rows are split for
+    c = _case(H + n, [n, n - 3], next_n=260, H=H, latent=latent, k=k, q_scale=0.5, gathered=True)
+    assert mx.attn_workspace_bytes(520, H, latent, k or c["bt"].shape[1] * 64) == 0
+    got = mx.attn_paged(**_to_dev(c, float("nan")))
+    torch.cuda.synchronize()
+    _rows_close(got, c, 260, np.array([0, 1, 129, 254, 259, 260, 300, 519]))
