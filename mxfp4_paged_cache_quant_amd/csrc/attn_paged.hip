@@ -8,7 +8,7 @@
 // new maximum scales what was summed so far by 2^(m_old - m_new).
 //
 // Work mapping: one workgroup takes HG * 16 heads of one query row over one share of
-// the row's tokens, 64 tokens (a tile; 32 for many rows) at a time.  A wave holds 16
+// the row's tokens, 64 tokens (a tile; 32 for many rows of more than 32 heads) at a time.  A wave holds 16
 // heads: their query in registers and their output sums, HG waves the heads and TH waves
 // the tile's token parts.  All products run on the 16x16x32 bf16 MFMA in the transposed
 // form:
@@ -26,14 +26,17 @@
 // two neighbouring chunks) over all banks.  The query comes the same way, once.
 //
 // What bounds it: with many rows the instruction issue of two waves a SIMD and LDS
-// together (1024 rows x 2048 tokens x 64 heads: of the SIMDs' cycles 42% MFMAs and 30%
-// other vector instructions, LDS 59% busy without a bank conflict), 315-330 us = 890-930
-// TFLOP/s where a large library product reaches 1,306; with few rows the way to the first
-// tile (the row's window, its list, its pages, the rows: four round trips) and the partial
-// sums.  32 heads a wave with the tile's weights passed through LDS halves the LDS reads,
-// but not the instructions (8 waves: 482 us; 4 waves of 512 registers: 512 us; where this
-// form took 367).  A register spilled in the loop is read back behind the copies on their
-// way, so none may be (5 of them: 331 us).
+// together (1024 rows x 2048 tokens x 64 heads: of the SIMDs' cycles 54% MFMAs and 30%
+// other vector instructions, LDS 51% busy without a bank conflict), 363-383 us = 760-805
+// TFLOP/s, the weights' second part not counted, where a large library product reaches 1,306;
+// with few rows the way to the first tile (the row's window, its list, its pages, the rows:
+// four round trips) and the partial sums.  32 heads a wave with the tile's weights passed
+// through LDS halves the LDS reads, but not the instructions (with the weights in one part
+// 8 waves 482 us, 4 waves of 512 registers 512 us, where this form took 367).  A vector register
+// spilled in the loop is read back behind the copies on their way, so none may be (one part: 331
+// us with 5 of them, 312 without).  Scalar ones go to lanes of a vector register, no memory: in the
+// 16- and 32-head forms of latent 512 16 and 26 of them do, read back 0 and 11 times in two tiles.
+// Below, pairs of figures of steps inside the loop are of one part on both sides.
 //
 // Places of a tile that hold no visible token read as zeros and get weight 0, so
 // nothing that a masked place holds reaches a sum.
@@ -42,8 +45,9 @@
 // left (2^-16 of it at most); l and lse take them unrounded.  The output's error is then its own
 // rounding's whatever the call's sizes.  With one part (2^-8) it is 1.24 times that over 2048
 // tokens, and a row that one token dominates is off by that token's rounding, since the
-// reference is no power of two from it.  Two parts are half as many products again: 1024 rows of 2048
-// tokens, 64 heads, 310 -> 363 us; 32 windows of 6600, 128 heads, 90 -> 101; 16 rows of 2048 24 -> 25.
+// reference is no power of two from it.  Two parts are half as many products again: 1024 rows of
+// 2048 tokens, 64 heads, 322 -> 378 us; 32 windows of 6600, 128 heads, 90 -> 102; 64 rows of 2048,
+// 128 heads, 74 -> 79; 16 rows of 2048, 64 heads, 24 -> 25.
 //
 // Few rows: the tokens are split over workgroups, each leaving its unscaled sums with
 // m and l in the workspace, and a second launch joins them.
@@ -425,8 +429,9 @@ __global__ __launch_bounds__(HG * TH * kWave, kTile == 32 ? 2 : 1) void attn_ker
 #pragma unroll
       for (int i = 0; i < Copy::kPieces; ++i) Copy::piece(i, src, tile, wave * kMine, rows, ln);
     };
-    // the query's rows, as if they were a tile's, to LDS: 64 heads to tile1 behind the
-    // list's and pages' loads, and with 128 heads the others to tile0 before the tile
+    // the query's rows, as if they were a tile's, to LDS: as many heads as a tile has tokens to
+    // tile1 behind the list's and pages' loads, and with 32-token tiles the others to tile0
+    // before the tile
     constexpr int kQTiles = (kHeads + kTile - 1) / kTile;
 #pragma unroll
     for (int i = 0; i < kQTiles; ++i) {
@@ -630,20 +635,22 @@ struct Plan {
 };
 
 // Few rows are split over the tokens, up to one workgroup for each CU (two of latent 128, whose
-// tiles leave the LDS room: 32 windows of 8192, 128 heads: 41.7 us, 45.5 with one).  A split
+// tiles leave the LDS room: 32 windows of 8192, 128 heads: 45.8 us, 47.6 with one).  A split
 // costs its share of the workspace's traffic (2 KB a head, written and read), so it takes 4
-// tiles or more (16 rows of 2048 tokens, 32 heads: 21.0 us with 8 splits, 22.9 with 16), or
-// 2 where even 64 workgroups do not come together (one such row: 15.3 us with 16 splits of
-// 32 heads, 16.5 with 8); one row of 131072 tokens, 64 heads, latent 128: 28 us with 128
-// splits, 41 with 64.
-// 64 heads a workgroup read the rows fewest times (32 rows of 2 x 6600 tokens, 128
-// heads: 91 us with 64, 132 with 32; 64 rows of 2048 tokens, 64 heads: 55 and 58); 32
+// tiles or more (16 rows of 2048 tokens, 32 heads: 22.0 us with 8 splits, 23.0 with 16), or
+// 2 where even 64 workgroups do not come together (one row of 64 heads: 15.7 us with 16 splits
+// of 32 heads, 17.7 with 8); one row of 131072 tokens, 64 heads, latent 128: 29 us with 128
+// splits, 42 with 64.
+// 64 heads a workgroup read the rows fewest times (16 x 2 rows of 6600 tokens, 128
+// heads: 101 us with 64, 139 with 32; 64 rows of 2048 tokens, 64 heads: 54 and 56); 32
 // heads spread a call over twice the CUs that would not fill them otherwise (one row:
-// 15.3 us, 17.5 with 64) or fill them with half the partial sums (32 rows of 2048 tokens,
-// 64 heads: 31 us with 4 splits, 34 with 64 heads and 8; 4 rows of 16384: 32 and 38).
+// 15.7 us, 17.9 with 64) or fill them with half the partial sums (32 rows of 2048 tokens,
+// 64 heads: 32 us with 4 splits, 35 with 64 heads and 8; 4 rows of 16384: 32 and 34).
 // Many rows: two workgroups of four waves a CU, 32 tokens at a time, whose phases do not
-// fall together (1024 rows of 2048 tokens, 64 heads: 312-328 us, 325-342 with one of
-// eight waves); with 200 rows, which do not fill both places, 128 us and 112.
+// fall together (1024 rows of 2048 tokens, 64 heads: 377 us, 395 with one of
+// eight waves); with 200 rows, which do not fill both places, 126 us and 114.
+// Groups of 16 and 32 heads keep one form for few rows and many (1024 rows of 2048 tokens: 230 us
+// with 16 heads, 277 with 32, 379 with 64).
 int64_t split_places(int latent) { return latent <= 128 ? 2 * kCus : kCus; }
 
 Plan plan_of(int64_t rows, int H, int latent, int64_t entries) {

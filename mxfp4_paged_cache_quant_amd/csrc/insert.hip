@@ -121,8 +121,8 @@ __device__ __forceinline__ void encode_row(const void* __restrict__ x, int64_t r
 // each product and each sum rounded to fp32 (no fused multiply-add), then the
 // row is encoded as an fp32 row.  A row whose position lies outside the table
 // is encoded unrotated.  rope_dim is a multiple of 16, so each lane's 8
-// elements are all rotated or all not (rope_row8).
-// Row `row` of q (token row / H) rotated, then encoded as an fp32 row.
+// elements are all rotated or all not (rope_row8).  `row` is a row of q, of
+// token row / H.
 template <typename In>
 __device__ __forceinline__ void rope_encode_row(const void* __restrict__ x, int64_t row,
                                                 int64_t stride, int H, const RopeSpec& rs,
