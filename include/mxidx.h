@@ -107,6 +107,7 @@ typedef enum { IDX_BF16 = 0, IDX_F32 = 1 } idx_dtype;
 #define IDX_ATTN_MAX_PAGES ((1 << 26) - 1024)   /* row numbers are 32-bit in the kernel */
 #define IDX_ATTN_MAX_TOKENS 0x7ffffe00           /* places of a row: tiles beyond it still count in 32 bits */
 #define IDX_ATTN_MAX_ROWS (1 << 22)              /* and a launch has fewer than 2^32 lanes */
+#define IDX_GATHER_MAX_TOKENS (1 << 29)          /* of a sequence: a workgroup of 256 lanes a page */
 
 /* Version of this ABI (major * 100 + minor). */
 int idx_version(void);
@@ -654,6 +655,39 @@ int idx_latent_insert(const void* kv, int dtype, int64_t T, int64_t kv_row_strid
                       const void* q_pe, int H, int64_t q_row_stride, int64_t q_head_stride,
                       void* q_out, int64_t out_row_stride, int64_t out_head_stride,
                       hipStream_t stream);
+
+/* MXFP4 latent cache: the latent cache at 400 bytes a token instead of 1,152 (latent 512), its
+ * `latent` first values in the MXFP4 row format above (blocks of 32) and the 64 rotated ones in bf16.
+ *   num_pages pages of page_size * IDX_LATENT_MXFP4_ROW_BYTES(latent) bytes.  Within a page the
+ *   page_size code rows (latent / 2 bytes each) come first in token order, then the page_size scale
+ *   rows (latent / 32 bytes each), then the page_size rows of 64 bf16 values. */
+#define IDX_LATENT_MXFP4_ROW_BYTES(latent) ((latent) / 2 + (latent) / IDX_BLOCK + 2 * IDX_LATENT_ROPE)
+
+/* idx_latent_insert_mxfp4 -- idx_latent_insert into the MXFP4 latent cache: the same arguments,
+ * limits and query rows.
+ *   The latent part is normed in 64 bits, x * rsqrt(mean(x^2) + eps) * weight, and rounded to fp32;
+ *   the codes are those of that row, whatever its scale (norm IDX_NORM_NONE: of kv's values as they
+ *   are), by the MXFP4 row's encode rule.  The positional part is rotated and rounded to bf16 as there.
+ *   eps: double, as it enters a 64-bit sum.  A row of zeros with eps 0 stays zeros.
+ *   cache: [num_pages, page_size * IDX_LATENT_MXFP4_ROW_BYTES(latent)] uint8, 16-byte aligned. */
+int idx_latent_insert_mxfp4(const void* kv, int dtype, int64_t T, int64_t kv_row_stride, int latent,
+                            int norm, const float* weight, double eps, const idx_rope* rope,
+                            const int64_t* slot_mapping, uint8_t* cache, int64_t num_pages, int page_size,
+                            const void* q_pe, int H, int64_t q_row_stride, int64_t q_head_stride,
+                            void* q_out, int64_t out_row_stride, int64_t out_head_stride,
+                            hipStream_t stream);
+
+/* idx_latent_gather_mxfp4 -- MXFP4 latent cache -> contiguous bf16 rows of latent + 64 values, in the
+ * order of idx_gather: the cached contexts of a prefill, whose keys and values are projected from
+ * them (idx_attn_prompt).  Exact: every code times its scale is a bf16.
+ *   block_table, seq_lens, cu_seq_offsets, batch, max_seq_len, total_tokens: as for idx_gather
+ *   (max_seq_len <= IDX_GATHER_MAX_TOKENS); tokens whose page lies outside the cache are skipped.
+ *   out: [total_tokens, latent + 64] bf16, row stride out_row_stride (a multiple of 8), 16-byte
+ *   aligned.  Rows that no token maps to are left untouched. */
+int idx_latent_gather_mxfp4(const uint8_t* cache, int64_t num_pages, int page_size, int latent,
+                            const int32_t* block_table, int64_t bt_row_stride, const int32_t* seq_lens,
+                            const int64_t* cu_seq_offsets, int batch, int64_t max_seq_len,
+                            int64_t total_tokens, void* out, int64_t out_row_stride, hipStream_t stream);
 
 /* idx_attn_paged -- attention of a step's query rows over the paged latent cache
  * (idx_latent_insert's), over the tokens of idx_topk's lists or over whole windows:

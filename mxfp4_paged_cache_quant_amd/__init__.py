@@ -24,6 +24,7 @@ __all__ = [
     "logits_paged_insert_fp8",
     "StepMap", "step_map", "norm_rope", "latent_insert", "attn_paged", "attn_workspace_bytes",
     "attn_workspace_max_bytes", "attn_workspace", "LATENT_ROPE", "LATENT_DIMS",
+    "latent_insert_mxfp4", "latent_gather_mxfp4", "latent_mxfp4_row_bytes",
     "FP8_ROW_BYTES", "FP8_SCALE_F32", "FP8_SCALE_POW2",
     "HEAD_DIM", "ROW_BYTES", "PAGE_SIZE", "TOPK_MAX", "EXPORTS",
 ]
@@ -68,6 +69,7 @@ _c_void_p = ctypes.c_void_p
 _i64 = ctypes.c_int64
 _int = ctypes.c_int
 _float = ctypes.c_float
+_double = ctypes.c_double
 
 # name -> (restype, argtypes); must match include/mxidx.h
 EXPORTS = {
@@ -129,6 +131,11 @@ EXPORTS = {
     "idx_latent_insert": (_int, [_c_void_p, _int, _i64, _i64, _int, _int, _c_void_p, _float,
                                  _c_void_p, _c_void_p, _c_void_p, _i64, _int, _c_void_p, _int, _i64,
                                  _i64, _c_void_p, _i64, _i64, _c_void_p]),
+    "idx_latent_insert_mxfp4": (_int, [_c_void_p, _int, _i64, _i64, _int, _int, _c_void_p, _double,
+                                       _c_void_p, _c_void_p, _c_void_p, _i64, _int, _c_void_p, _int,
+                                       _i64, _i64, _c_void_p, _i64, _i64, _c_void_p]),
+    "idx_latent_gather_mxfp4": (_int, [_c_void_p, _i64, _int, _int, _c_void_p, _i64, _c_void_p,
+                                       _c_void_p, _int, _i64, _i64, _c_void_p, _i64, _c_void_p]),
     "idx_attn_workspace_bytes": (ctypes.c_size_t, [_i64, _int, _int, _i64]),
     "idx_attn_workspace_max_bytes": (ctypes.c_size_t, [_i64, _int, _int, _i64]),
     "idx_attn_paged": (_int, [_c_void_p, _i64, _i64, _i64, _int, _int, _c_void_p, _i64, _int,
@@ -947,13 +954,14 @@ def _call(name, device, stream, *args):
         _check(status, name)
 
 
-def _empty(stream, shape, dtype, device):
-    """A new tensor whose memory belongs to the call's stream."""
+def _empty(stream, shape, dtype, device, zero=False):
+    """A new tensor, of zeros or of anything, whose memory belongs to the call's stream."""
     torch = _torch()
+    make = torch.zeros if zero else torch.empty
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return make(shape, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return make(shape, dtype=dtype, device=device)
 
 
 def _device_of(t, name):
@@ -1104,20 +1112,15 @@ def _latent_cache(device, cache):
     return cp, shape[0], shape[2] - LATENT_ROPE
 
 
-def latent_insert(kv, slot_mapping, cache, cos, sin, mode="neox", positions=None, norm="rms",
-                  weight=None, eps=1e-6, q_pe=None, q_out=None, stream=None):
-    """Latent rows kv [T, latent + 64] (bf16 / fp32) into the latent cache [num_pages, 64,
-    latent + 64] bf16: the latent part RMS-normed (``norm`` "rms", fp32 ``weight`` [latent] or
-    None; or "none"), the last 64 values rotated (cos / sin fp32 [table_rows, 32]), slots < 0
-    skipped.  ``q_pe`` [T, H, 64]: the query's positional part, rotated into ``q_out``
-    [T, H, 64] bf16 (``q[..., latent:]`` of attn_paged's query, say; q_pe itself if that is
-    bf16) in the same launch.  Returns cache, or (cache, q_out) with q_pe."""
+def _latent_insert(call, cache_of, kv, slot_mapping, cache, cos, sin, mode, positions, norm, weight,
+                   eps, q_pe, q_out, stream):
+    """The checked call of idx_latent_insert or idx_latent_insert_mxfp4."""
     torch = _torch()
     device = _device_of(kv, "kv")
     dtype = kv.dtype
     if dtype not in (torch.bfloat16, torch.float32):
         raise MxidxError("kv must be bfloat16 or float32")
-    cp, num_pages, latent = _latent_cache(device, cache)
+    cp, num_pages, latent = cache_of(device, cache)
     shape, kv_strides = kv.shape, kv.stride()
     if len(shape) != 2 or shape[1] != latent + LATENT_ROPE or (shape[0] and kv_strides[1] != 1):
         raise MxidxError(f"kv must be [T, {latent + LATENT_ROPE}] with a contiguous last dim")
@@ -1143,11 +1146,84 @@ def latent_insert(kv, slot_mapping, cache, cos, sin, mode="neox", positions=None
             raise MxidxError("q_pe and q_out must have a contiguous last dim")
     elif q_out is not None:
         raise MxidxError("q_out needs q_pe")
-    _call("idx_latent_insert", device, stream, kv.data_ptr(),
+    _call(call, device, stream, kv.data_ptr(),
           IDX_BF16 if dtype == torch.bfloat16 else IDX_F32, T, kv_strides[0], latent,
           _code({"none": 0, "rms": 1}, norm, "norm"), wp, eps, ctypes.addressof(rope), mp, cp,
           num_pages, PAGE_SIZE, qp, H, qs, qh, op, os_, oh)
     return cache if q_pe is None else (cache, q_out)
+
+
+def latent_insert(kv, slot_mapping, cache, cos, sin, mode="neox", positions=None, norm="rms",
+                  weight=None, eps=1e-6, q_pe=None, q_out=None, stream=None):
+    """Latent rows kv [T, latent + 64] (bf16 / fp32) into the latent cache [num_pages, 64,
+    latent + 64] bf16: the latent part RMS-normed (``norm`` "rms", fp32 ``weight`` [latent] or
+    None; or "none"), the last 64 values rotated (cos / sin fp32 [table_rows, 32]), slots < 0
+    skipped.  ``q_pe`` [T, H, 64]: the query's positional part, rotated into ``q_out``
+    [T, H, 64] bf16 (``q[..., latent:]`` of attn_paged's query, say; q_pe itself if that is
+    bf16) in the same launch.  Returns cache, or (cache, q_out) with q_pe."""
+    return _latent_insert("idx_latent_insert", _latent_cache, kv, slot_mapping, cache, cos, sin, mode,
+                          positions, norm, weight, eps, q_pe, q_out, stream)
+
+
+def latent_mxfp4_row_bytes(latent):
+    """Bytes of a token in the MXFP4 latent cache: codes, scales and 64 bf16 values."""
+    return latent // 2 + latent // 32 + 2 * LATENT_ROPE
+
+
+_LATENT_OF_PAGE = {PAGE_SIZE * latent_mxfp4_row_bytes(n): n for n in LATENT_DIMS}
+
+
+def _latent_mxfp4_cache(device, cache):
+    """(address, num_pages, latent) of an MXFP4 latent cache."""
+    cp = _on(device, cache, "cache", _torch().uint8)
+    shape = cache.shape
+    latent = _LATENT_OF_PAGE.get(shape[1]) if len(shape) == 2 else None
+    if latent is None or not cache.is_contiguous():
+        raise MxidxError("cache must be a contiguous uint8 [num_pages, 64 * latent_mxfp4_row_bytes(latent)], "
+                         f"latent one of {LATENT_DIMS}")
+    return cp, shape[0], latent
+
+
+def latent_insert_mxfp4(kv, slot_mapping, cache, cos, sin, mode="neox", positions=None, norm="rms",
+                        weight=None, eps=1e-6, q_pe=None, q_out=None, stream=None):
+    """latent_insert into the MXFP4 latent cache (uint8 [num_pages, 64 * latent_mxfp4_row_bytes(latent)]):
+    the latent part normed in 64 bits and written as MXFP4 codes and scales, the last 64 values
+    rotated and kept in bf16.  Arguments, query rows and result as latent_insert's."""
+    return _latent_insert("idx_latent_insert_mxfp4", _latent_mxfp4_cache, kv, slot_mapping, cache, cos, sin,
+                          mode, positions, norm, weight, eps, q_pe, q_out, stream)
+
+
+def latent_gather_mxfp4(cache, block_table, seq_lens, cu_seq_offsets, max_seq_len, total_tokens, out=None,
+                        stream=None):
+    """MXFP4 latent cache -> contiguous bf16 rows [total_tokens, latent + 64], exact: token j of sequence b
+    (block_table i32 [B, pages], seq_lens i32 [B]) to row cu_seq_offsets[b] + j (i64, at least B of them:
+    step_map's B + 1 will do).  Rows that no token maps to are zeros in a new ``out`` and stay as
+    they were in a given one."""
+    torch = _torch()
+    device = _device_of(cache, "cache")
+    cp, num_pages, latent = _latent_mxfp4_cache(device, cache)
+    bp = _on(device, block_table, "block_table", torch.int32)
+    shape, strides = block_table.shape, block_table.stride()
+    if len(shape) != 2 or (shape[1] > 1 and strides[1] != 1 and shape[0]):
+        raise MxidxError("block_table must be [B, pages] with unit inner stride")
+    B, pages = shape
+    if max_seq_len > pages * PAGE_SIZE:
+        raise MxidxError("block_table has fewer pages than max_seq_len needs")
+    stride = strides[0] if B > 1 else max(pages, 1)
+    sp = _on(device, seq_lens, "seq_lens", torch.int32, (B,))
+    op = _on(device, cu_seq_offsets, "cu_seq_offsets", torch.int64)
+    if cu_seq_offsets.dim() != 1 or cu_seq_offsets.shape[0] < B or not cu_seq_offsets.is_contiguous():
+        raise MxidxError(f"cu_seq_offsets must be a contiguous int64 of {B} offsets or more")
+    width = latent + LATENT_ROPE
+    if out is None:
+        out = _empty(stream, (total_tokens, width), torch.bfloat16, device, zero=True)
+    rp = _on(device, out, "out", torch.bfloat16)
+    if out.dim() != 2 or out.shape[0] < total_tokens or out.shape[1] != width or \
+            (out.stride(1) != 1 and total_tokens):
+        raise MxidxError(f"out must be [{total_tokens}, {width}] with a contiguous last dim")
+    _call("idx_latent_gather_mxfp4", device, stream, cp, num_pages, PAGE_SIZE, latent, bp, stride, sp, op,
+          B, max_seq_len, total_tokens, rp, out.stride(0))
+    return out
 
 
 def attn_workspace_bytes(rows, heads, latent, entries):

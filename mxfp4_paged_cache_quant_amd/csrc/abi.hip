@@ -640,12 +640,13 @@ int idx_norm_rope(const idx_heads* q, const idx_heads* k, int dtype, int64_t T,
 
 static bool latent_ok(int latent) { return latent == 128 || latent == 256 || latent == 512; }
 
-int idx_latent_insert(const void* kv, int dtype, int64_t T, int64_t kv_row_stride, int latent,
-                      int norm, const float* weight, float eps, const idx_rope* rope,
-                      const int64_t* slot_mapping, void* cache, int64_t num_pages, int page_size,
-                      const void* q_pe, int H, int64_t q_row_stride, int64_t q_head_stride,
-                      void* q_out, int64_t out_row_stride, int64_t out_head_stride,
-                      hipStream_t stream) {
+// idx_latent_insert and idx_latent_insert_mxfp4 (mx).
+static int latent_insert(const void* kv, int dtype, int64_t T, int64_t kv_row_stride, int latent,
+                         int norm, const float* weight, double eps, const idx_rope* rope,
+                         const int64_t* slot_mapping, void* cache, int64_t num_pages, int page_size,
+                         const void* q_pe, int H, int64_t q_row_stride, int64_t q_head_stride,
+                         void* q_out, int64_t out_row_stride, int64_t out_head_stride, bool mx,
+                         hipStream_t stream) {
   int st = check_rope(rope);
   if (st != IDX_OK) return st;
   if (rope->rope_dim != IDX_LATENT_ROPE) return IDX_ERR_ARG;
@@ -660,7 +661,7 @@ int idx_latent_insert(const void* kv, int dtype, int64_t T, int64_t kv_row_strid
   const int al = dtype == IDX_BF16 ? 8 : 4;
   if (!kv || !aligned(kv, 16) || !stride_ok(kv_row_stride, T, latent + IDX_LATENT_ROPE, al))
     return IDX_ERR_ARG;
-  if (norm == IDX_NORM_RMS && (!aligned(weight, 16) || !(eps >= 0.f))) return IDX_ERR_ARG;
+  if (norm == IDX_NORM_RMS && (!aligned(weight, 16) || !(eps >= 0.0))) return IDX_ERR_ARG;
   if (!slot_mapping || !aligned(slot_mapping, 8)) return IDX_ERR_ARG;
   if (num_pages > 0 && (!cache || !aligned(cache, 16))) return IDX_ERR_ARG;
   if (!rope->positions && rope->table_rows < T) return IDX_ERR_ARG;
@@ -680,7 +681,52 @@ int idx_latent_insert(const void* kv, int dtype, int64_t T, int64_t kv_row_strid
                             eps, slot_mapping, cache, num_pages * IDX_PAGE_SIZE,
                             has_q ? q_pe : nullptr, H, q_row_stride, q_head_stride, q_out,
                             out_row_stride, out_head_stride};
-  return launched(mxidx::launch_latent_insert(a, dtype == IDX_F32, latent, rope_spec(rope), stream));
+  return launched(mxidx::launch_latent_insert(a, dtype == IDX_F32, latent, mx, rope_spec(rope), stream));
+}
+
+int idx_latent_insert(const void* kv, int dtype, int64_t T, int64_t kv_row_stride, int latent,
+                      int norm, const float* weight, float eps, const idx_rope* rope,
+                      const int64_t* slot_mapping, void* cache, int64_t num_pages, int page_size,
+                      const void* q_pe, int H, int64_t q_row_stride, int64_t q_head_stride,
+                      void* q_out, int64_t out_row_stride, int64_t out_head_stride,
+                      hipStream_t stream) {
+  return latent_insert(kv, dtype, T, kv_row_stride, latent, norm, weight, eps, rope, slot_mapping, cache,
+                       num_pages, page_size, q_pe, H, q_row_stride, q_head_stride, q_out, out_row_stride,
+                       out_head_stride, false, stream);
+}
+
+int idx_latent_insert_mxfp4(const void* kv, int dtype, int64_t T, int64_t kv_row_stride, int latent,
+                            int norm, const float* weight, double eps, const idx_rope* rope,
+                            const int64_t* slot_mapping, uint8_t* cache, int64_t num_pages, int page_size,
+                            const void* q_pe, int H, int64_t q_row_stride, int64_t q_head_stride,
+                            void* q_out, int64_t out_row_stride, int64_t out_head_stride,
+                            hipStream_t stream) {
+  return latent_insert(kv, dtype, T, kv_row_stride, latent, norm, weight, eps, rope, slot_mapping, cache,
+                       num_pages, page_size, q_pe, H, q_row_stride, q_head_stride, q_out, out_row_stride,
+                       out_head_stride, true, stream);
+}
+
+int idx_latent_gather_mxfp4(const uint8_t* cache, int64_t num_pages, int page_size, int latent,
+                            const int32_t* block_table, int64_t bt_row_stride, const int32_t* seq_lens,
+                            const int64_t* cu_seq_offsets, int batch, int64_t max_seq_len,
+                            int64_t total_tokens, void* out, int64_t out_row_stride, hipStream_t stream) {
+  if (page_size != IDX_PAGE_SIZE || !latent_ok(latent) || num_pages < 0 || num_pages > ((int64_t)1 << 40) ||
+      batch < 0 || batch > IDX_MAX_DECODE_SEQS || max_seq_len < 0 || max_seq_len > IDX_GATHER_MAX_TOKENS ||
+      total_tokens < 0)
+    return IDX_ERR_ARG;
+  if (batch == 0 || max_seq_len == 0 || total_tokens == 0 || num_pages == 0) return IDX_OK;
+  const int64_t pages_per_seq = (max_seq_len + IDX_PAGE_SIZE - 1) / IDX_PAGE_SIZE;
+  if (bt_row_stride < pages_per_seq) return IDX_ERR_ARG;
+  if (!cache || !aligned(cache, 16) || !block_table || !aligned(block_table, 4) || !seq_lens ||
+      !aligned(seq_lens, 4) || !cu_seq_offsets || !aligned(cu_seq_offsets, 8) || !out || !aligned(out, 16) ||
+      !stride_ok(out_row_stride, total_tokens, latent + IDX_LATENT_ROPE, 8))
+    return IDX_ERR_ARG;
+  int st = gate_current();
+  if (st != IDX_OK) return st;
+  return launched(mxidx::launch_latent_gather(
+      {cache, num_pages, block_table, bt_row_stride, seq_lens, cu_seq_offsets, batch, max_seq_len,
+       total_tokens, out, out_row_stride},
+      latent, stream));
 }
 
 // What the two calls below share: sizes that the kernels' grid and indexes take.  A row takes

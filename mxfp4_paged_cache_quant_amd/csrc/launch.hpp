@@ -177,13 +177,13 @@ hipError_t launch_norm_rope(const HeadsSpec& q, const HeadsSpec& k, bool f32, in
                             const RopeSpec& rope, hipStream_t stream);
 
 // Latent rows normed, rotated and written to the paged latent cache (bf16 rows of
-// latent + 64 values); q_pe null: no query rows.
+// latent + 64 values; mx: the MXFP4 pages of latent_mxfp4.hpp); q_pe null: no query rows.
 struct LatentSpec {
   const void* kv;
   int64_t T, kv_row_stride;
   int norm;
   const float* weight;
-  float eps;
+  double eps;              // the bf16 cache's norm takes it in fp32
   const int64_t* slot_mapping;
   void* cache;
   int64_t num_slots;
@@ -193,8 +193,23 @@ struct LatentSpec {
   void* q_out;
   int64_t out_row_stride, out_head_stride;
 };
-hipError_t launch_latent_insert(const LatentSpec& a, bool f32, int latent, const RopeSpec& rope,
+hipError_t launch_latent_insert(const LatentSpec& a, bool f32, int latent, bool mx, const RopeSpec& rope,
                                 hipStream_t stream);
+
+// MXFP4 latent pages -> contiguous bf16 rows (latent_gather.hip); pointers as in idx_latent_gather_mxfp4.
+struct LatentGatherArgs {
+  const uint8_t* cache;
+  int64_t num_pages;
+  const int32_t* block_table;
+  int64_t bt_row_stride;
+  const int32_t* seq_lens;
+  const int64_t* cu_seq_offsets;
+  int batch;
+  int64_t max_seq_len, total_tokens;
+  void* out;
+  int64_t out_row_stride;
+};
+hipError_t launch_latent_gather(const LatentGatherArgs& a, int latent, hipStream_t stream);
 
 // Attention over the paged latent cache (attn_paged.hip); pointers as in
 // idx_attn_paged.  row_seq null: row r belongs to sequence r / rows_per_seq.

@@ -1,12 +1,17 @@
 // Per-head norm and rotary position embedding in one pass: the indexer's query and
 // key rows (idx_norm_rope), and the main cache's latent rows with their paged write
-// and the query's positional part (idx_latent_insert).
+// and the query's positional part (idx_latent_insert, idx_latent_insert_mxfp4).
 //
 // Norm of a row of n values, in fp32:
 //   rms:   y = x * rsqrt(sum x^2 / n + eps) * weight + bias
 //   layer: the same of x - m, m = sum x / n (the mean subtracted before squaring, so
 //          a mean that is large beside the spread loses nothing)
 // then the rotation of rope.hpp, then one rounding to the output's type.
+//
+// Rows that go to the MXFP4 cache are normed in 64 bits and rounded to fp32 before their encode.
+// A value that an fp32 norm leaves in the last place on the other side of a code's border gets the
+// other code, a quarter or more of its size off, in about 4 of 10^7 values; with 64 bits the
+// codes are those of the definition.
 //
 // Work mapping: 8 values a lane, so a row of 128 is 16 lanes, a latent row of 512 a
 // whole wave (256: 32 lanes, 128: 16), a positional part of 64 eight lanes.  The lanes of
@@ -23,14 +28,16 @@
 #include <algorithm>
 
 #include "common.hpp"
+#include "latent_mxfp4.hpp"
 #include "launch.hpp"
+#include "mxfp4_encode.hpp"
 #include "rope.hpp"
 
 namespace mxidx {
 namespace {
 
 constexpr int kRopeLanes = 8;              // lanes of a 64-value positional part
-constexpr int kRopeWidth = 64;
+constexpr int kRopeWidth = kLatentRope;
 
 template <bool kF32>
 __device__ __forceinline__ void load8(const void* base, int64_t off, float (&v)[8]) {
@@ -113,6 +120,73 @@ __device__ __forceinline__ void norm_row8(float (&v)[8], int norm, float eps, co
   for (int i = 0; i < 8; ++i) v[i] = v[i] * r * w[i] + b[i];
 }
 
+// The same of whole and of 64-bit values (lane i of a ring gets lane i - n's).
+template <int n>
+__device__ __forceinline__ int turned16(int x) {
+  return __builtin_amdgcn_update_dpp(0, x, 0x120 + n, 0xf, 0xf, true);
+}
+template <int n>
+__device__ __forceinline__ double ring16(double x) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = (uint32_t)turned16<n>((int)(uint32_t)u), hi = (uint32_t)turned16<n>((int)(uint32_t)(u >> 32));
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+
+// The RMS norm of a row of 8W values held by W lanes, in 64 bits, rounded to fp32.  A row
+// whose mean square and eps are both 0 stays 0.
+template <int W>
+__device__ __forceinline__ void rms_row8_f64(float (&v)[8], double eps, const float (&w)[8]) {
+  double s = 0.0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) s = fma((double)v[i], (double)v[i], s);
+  s += ring16<8>(s);
+  s += ring16<4>(s);
+  s += ring16<2>(s);
+  s += ring16<1>(s);
+#pragma unroll
+  for (int m = 16; m < W; m <<= 1) s += __shfl_xor(s, m);
+  const double x = s * (1.0 / (8 * W)) + eps;
+  // the hardware's reciprocal root (2^-14 or better) and Newton's steps, each of which squares the error
+  double r = __builtin_amdgcn_rsq(x);
+#pragma unroll
+  for (int i = 0; i < 3; ++i) r = fma(0.5 * r, fma(-x * r, r, 1.0), r);
+  if (x == 0.0) r = 0.0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = (float)((double)v[i] * r * (double)w[i]);
+}
+
+// The largest of u over the four lanes of a block of 32 values.
+__device__ __forceinline__ uint32_t quad_max(uint32_t u) {
+  u = max(u, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)u, 0xB1, 0xf, 0xf, true));   // lanes 1, 0, 3, 2
+  return max(u, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)u, 0x4E, 0xf, 0xf, true)); // lanes 2, 3, 0, 1
+}
+
+// A row's latent part as MXFP4, 8 values a lane, into the page at `page`: 4 code bytes a lane, and
+// the scale bytes of 16 lanes' four blocks by the first of them.
+template <int kLatent>
+__device__ __forceinline__ void store_mx(uint8_t* page, int off, int sub, const float (&v)[8], bool on) {
+  using Page = MxPage<kLatent>;
+  uint32_t amax = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) amax = max(amax, __float_as_uint(v[i]) & 0x7fffffffu);
+  amax = quad_max(amax);
+  const int E = block_exponent(amax);
+  const float d = block_divisor(amax, E);
+  uint32_t codes = 0;
+  codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(codes, v[0], v[1], d, 0);
+  codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(codes, v[2], v[3], d, 1);
+  codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(codes, v[4], v[5], d, 2);
+  codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(codes, v[6], v[7], d, 3);
+  // lanes 4, 8 and 12 of a ring hold the next blocks' exponents (a rotation by 16 - n fetches lane n's)
+  const int e = E + 127;
+  const uint32_t scales = (uint32_t)e | (uint32_t)turned16<12>(e) << 8 | (uint32_t)turned16<8>(e) << 16 |
+                          (uint32_t)turned16<4>(e) << 24;
+  if (!on) return;
+  *reinterpret_cast<uint32_t*>(page + off * Page::kCodes + 4 * sub) = codes;
+  if (sub % 16 == 0)
+    *reinterpret_cast<uint32_t*>(page + Page::kScaleBase + off * Page::kScales + sub / 4) = scales;
+}
+
 __device__ __forceinline__ void load_params(const float* p, int sub, float other, float (&v)[8]) {
   if (p) {
     load8<true>(p, 8 * sub, v);
@@ -161,8 +235,8 @@ __global__ __launch_bounds__(256) void norm_rope_kernel(HeadsSpec q, HeadsSpec k
 
 // Blocks [0, q_blocks) rotate the query rows, 8 lanes for a run of heads of one token; the
 // others take kTokens tokens a wave: kLatent / 8 lanes norm the latent part, the first
-// 8 rotate the rest.
-template <bool kF32, int kLatent, int kTokens, int kRun>
+// 8 rotate the rest.  kMx: into the MXFP4 cache.
+template <bool kF32, int kLatent, int kTokens, int kRun, bool kMx>
 __global__ __launch_bounds__(256) void latent_insert_kernel(LatentSpec a, RopeSpec rs, int q_blocks,
                                                             int run_len) {
   if ((int)blockIdx.x < q_blocks) {
@@ -208,9 +282,20 @@ __global__ __launch_bounds__(256) void latent_insert_kernel(LatentSpec a, RopeSp
   }
 #pragma unroll
   for (int i = 0; i < kTokens; ++i) {
-    norm_row8<W>(v[i], a.norm, a.eps, w, b);
+    if constexpr (kMx) {
+      if (a.norm != kNormNone) rms_row8_f64<W>(v[i], a.eps, w);
+    } else {
+      norm_row8<W>(v[i], a.norm, (float)a.eps, w, b);
+    }
     rotate_row8<kRopeLanes>(r[i], rl, angles[i], rs);
     if (slot[i] < 0 || slot[i] >= a.num_slots) continue;
+    if constexpr (kMx) {
+      uint8_t* page = static_cast<uint8_t*>(a.cache) + slot[i] / kPage * MxPage<kLatent>::kBytes;
+      const int off = (int)(slot[i] % kPage);
+      store_mx<kLatent>(page, off, wl, v[i], lane < W);
+      if (lane < kRopeLanes) store8<false>(page + MxPage<kLatent>::kPosBase + off * MxPage<kLatent>::kPos, 8 * lane, r[i]);
+      continue;
+    }
     const int64_t dst = slot[i] * (kLatent + kRopeWidth);
     if (lane < W) store8<false>(a.cache, dst + 8 * lane, v[i]);
     if (lane < kRopeLanes) store8<false>(a.cache, dst + kLatent + 8 * lane, r[i]);
@@ -226,29 +311,29 @@ int run_length(int64_t rows, int lanes) {
 }
 
 // `many`: the call fills the card with runs of kBatch rows and two tokens a wave.
-template <bool kF32, int kLatent>
+template <bool kF32, int kLatent, bool kMx>
 void launch_latent_rows(const LatentSpec& a, const RopeSpec& rs, int q_blocks, int run_len, bool many,
                         hipStream_t stream) {
   const int64_t waves = many ? (a.T + 1) / 2 : a.T;
   const dim3 grid((uint32_t)(q_blocks + (waves + 3) / 4));
   if (many)
-    hipLaunchKernelGGL((latent_insert_kernel<kF32, kLatent, 2, kBatch>), grid, dim3(256), 0, stream, a, rs,
+    hipLaunchKernelGGL((latent_insert_kernel<kF32, kLatent, 2, kBatch, kMx>), grid, dim3(256), 0, stream, a, rs,
                        q_blocks, run_len);
   else
-    hipLaunchKernelGGL((latent_insert_kernel<kF32, kLatent, 1, 1>), grid, dim3(256), 0, stream, a, rs,
+    hipLaunchKernelGGL((latent_insert_kernel<kF32, kLatent, 1, 1, kMx>), grid, dim3(256), 0, stream, a, rs,
                        q_blocks, run_len);
 }
 
-template <bool kF32>
+template <bool kF32, bool kMx>
 hipError_t launch_latent(const LatentSpec& a, int latent, const RopeSpec& rs, hipStream_t stream) {
   const bool many = a.T >= 2 * 256 * 32 || (a.q_pe && run_length(a.T * a.H, kRopeLanes) > 1);
   const int run_len = many && a.q_pe ? std::max(run_length(a.T * a.H, kRopeLanes), kBatch) : 1;
   const int64_t units = a.q_pe ? a.T * ((a.H + run_len - 1) / run_len) : 0;
   const int q_blocks = (int)((units * kRopeLanes + 255) / 256);
   switch (latent) {
-    case 128: launch_latent_rows<kF32, 128>(a, rs, q_blocks, run_len, many, stream); break;
-    case 256: launch_latent_rows<kF32, 256>(a, rs, q_blocks, run_len, many, stream); break;
-    default: launch_latent_rows<kF32, 512>(a, rs, q_blocks, run_len, many, stream); break;
+    case 128: launch_latent_rows<kF32, 128, kMx>(a, rs, q_blocks, run_len, many, stream); break;
+    case 256: launch_latent_rows<kF32, 256, kMx>(a, rs, q_blocks, run_len, many, stream); break;
+    default: launch_latent_rows<kF32, 512, kMx>(a, rs, q_blocks, run_len, many, stream); break;
   }
   return hipGetLastError();
 }
@@ -273,10 +358,12 @@ hipError_t launch_norm_rope(const HeadsSpec& q, const HeadsSpec& k, bool f32, in
   return hipGetLastError();
 }
 
-hipError_t launch_latent_insert(const LatentSpec& a, bool f32, int latent, const RopeSpec& rope,
+hipError_t launch_latent_insert(const LatentSpec& a, bool f32, int latent, bool mx, const RopeSpec& rope,
                                 hipStream_t stream) {
-  return f32 ? launch_latent<true>(a, latent, rope, stream)
-             : launch_latent<false>(a, latent, rope, stream);
+  if (mx) return f32 ? launch_latent<true, true>(a, latent, rope, stream)
+                     : launch_latent<false, true>(a, latent, rope, stream);
+  return f32 ? launch_latent<true, false>(a, latent, rope, stream)
+             : launch_latent<false, false>(a, latent, rope, stream);
 }
 
 }  // namespace mxidx
