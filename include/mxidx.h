@@ -733,6 +733,17 @@ int idx_attn_paged(const void* q, int64_t q_row_stride, int64_t q_head_stride, i
                    float scale, void* out, int64_t out_row_stride, int64_t out_head_stride,
                    float* lse, void* workspace, size_t workspace_bytes, hipStream_t stream);
 
+/* idx_attn_paged_mxfp4 -- idx_attn_paged over the MXFP4 latent cache (idx_latent_insert_mxfp4's): the
+ * same arguments, limits, workspace sizes and arithmetic, the cached rows being what their codes,
+ * scales and positional values stand for (exact in bf16). */
+int idx_attn_paged_mxfp4(const void* q, int64_t q_row_stride, int64_t q_head_stride, int64_t rows, int H,
+                         int latent, const uint8_t* cache, int64_t num_pages, int page_size,
+                         const int32_t* block_table, int64_t bt_row_stride, int B,
+                         const int32_t* row_seq, const int32_t* ks, const int32_t* ke,
+                         const int32_t* indices, int64_t idx_row_stride, int k, int64_t max_tokens,
+                         float scale, void* out, int64_t out_row_stride, int64_t out_head_stride,
+                         float* lse, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -24,7 +24,7 @@ __all__ = [
     "logits_paged_insert_fp8",
     "StepMap", "step_map", "norm_rope", "latent_insert", "attn_paged", "attn_workspace_bytes",
     "attn_workspace_max_bytes", "attn_workspace", "LATENT_ROPE", "LATENT_DIMS",
-    "latent_insert_mxfp4", "latent_gather_mxfp4", "latent_mxfp4_row_bytes",
+    "latent_insert_mxfp4", "latent_gather_mxfp4", "latent_mxfp4_row_bytes", "attn_paged_mxfp4",
     "FP8_ROW_BYTES", "FP8_SCALE_F32", "FP8_SCALE_POW2",
     "HEAD_DIM", "ROW_BYTES", "PAGE_SIZE", "TOPK_MAX", "EXPORTS",
 ]
@@ -142,6 +142,10 @@ EXPORTS = {
                               _c_void_p, _i64, _int, _c_void_p, _c_void_p, _c_void_p, _c_void_p,
                               _i64, _int, _i64, _float, _c_void_p, _i64, _i64, _c_void_p, _c_void_p,
                               ctypes.c_size_t, _c_void_p]),
+    "idx_attn_paged_mxfp4": (_int, [_c_void_p, _i64, _i64, _i64, _int, _int, _c_void_p, _i64, _int,
+                                    _c_void_p, _i64, _int, _c_void_p, _c_void_p, _c_void_p, _c_void_p,
+                                    _i64, _int, _i64, _float, _c_void_p, _i64, _i64, _c_void_p, _c_void_p,
+                                    ctypes.c_size_t, _c_void_p]),
 }
 
 
@@ -1245,19 +1249,12 @@ def attn_workspace(rows, heads, latent, entries, device="cuda"):
                        dtype=torch.uint8, device=device)
 
 
-def attn_paged(q, cache, block_table, ke, scale, indices=None, ks=None, row_seq=None,
-               max_tokens=None, out=None, lse=None, workspace=None, stream=None):
-    """Attention of query rows q [rows, H, latent + 64] (bf16) over the latent cache: returns
-    (out bf16 [rows, H, latent], lse fp32 [rows, H]).
-
-    Row r sees its sequence's tokens 0 .. ke[r] - ks[r] - 1 (ks None: 0), all of them or those
-    of ``indices`` (int32 [rows, k] columns in [ks, ke), topk's output; -1 skipped).
-    ``row_seq`` i32 [rows]: the row's sequence (None: rows / B rows each, in order); rows of no
-    sequence stay as they are.  ``max_tokens`` bounds ke - ks (None: what block_table holds).
-    ``workspace``: attn_workspace's, allocated here when it is not given."""
+def _attn_paged(call, cache_of, q, cache, block_table, ke, scale, indices, ks, row_seq, max_tokens, out, lse,
+                workspace, stream):
+    """The checked call of idx_attn_paged or idx_attn_paged_mxfp4."""
     torch = _torch()
     device = _device_of(q, "q")
-    cp, num_pages, latent = _latent_cache(device, cache)
+    cp, num_pages, latent = cache_of(device, cache)
     bf16, i32 = torch.bfloat16, torch.int32
     qp = _on(device, q, "q", bf16)
     shape, q_strides = q.shape, q.stride()
@@ -1305,7 +1302,29 @@ def attn_paged(q, cache, block_table, ke, scale, indices=None, ks=None, row_seq=
         wp, wb = _on(device, workspace, "workspace", torch.uint8), workspace.numel()
         if not workspace.is_contiguous():      # an expanded view has less memory than numel
             raise MxidxError("workspace must be contiguous")
-    _call("idx_attn_paged", device, stream, qp, q_strides[0], q_strides[1], rows, H, latent, cp,
+    _call(call, device, stream, qp, q_strides[0], q_strides[1], rows, H, latent, cp,
           num_pages, PAGE_SIZE, bp, stride, B, rp, kp, ep, ip, istride, k, max_tokens, scale, op,
           strides[0], strides[1], lp, wp, wb)
     return out, lse
+
+
+def attn_paged(q, cache, block_table, ke, scale, indices=None, ks=None, row_seq=None,
+               max_tokens=None, out=None, lse=None, workspace=None, stream=None):
+    """Attention of query rows q [rows, H, latent + 64] (bf16) over the latent cache: returns
+    (out bf16 [rows, H, latent], lse fp32 [rows, H]).
+
+    Row r sees its sequence's tokens 0 .. ke[r] - ks[r] - 1 (ks None: 0), all of them or those
+    of ``indices`` (int32 [rows, k] columns in [ks, ke), topk's output; -1 skipped).
+    ``row_seq`` i32 [rows]: the row's sequence (None: rows / B rows each, in order); rows of no
+    sequence stay as they are.  ``max_tokens`` bounds ke - ks (None: what block_table holds).
+    ``workspace``: attn_workspace's, allocated here when it is not given."""
+    return _attn_paged("idx_attn_paged", _latent_cache, q, cache, block_table, ke, scale, indices, ks, row_seq,
+                       max_tokens, out, lse, workspace, stream)
+
+
+def attn_paged_mxfp4(q, cache, block_table, ke, scale, indices=None, ks=None, row_seq=None,
+                     max_tokens=None, out=None, lse=None, workspace=None, stream=None):
+    """attn_paged over the MXFP4 latent cache (uint8 [num_pages, 64 * latent_mxfp4_row_bytes(latent)]):
+    the same arguments, workspace (attn_workspace's) and results."""
+    return _attn_paged("idx_attn_paged_mxfp4", _latent_mxfp4_cache, q, cache, block_table, ke, scale, indices, ks,
+                       row_seq, max_tokens, out, lse, workspace, stream)

@@ -746,13 +746,15 @@ size_t idx_attn_workspace_max_bytes(int64_t rows, int H, int latent, int64_t ent
   return (size_t)mxidx::attn_workspace_max_bytes(rows, H, latent, entries);
 }
 
-int idx_attn_paged(const void* q, int64_t q_row_stride, int64_t q_head_stride, int64_t rows, int H,
-                   int latent, const void* cache, int64_t num_pages, int page_size,
-                   const int32_t* block_table, int64_t bt_row_stride, int B,
-                   const int32_t* row_seq, const int32_t* ks, const int32_t* ke,
-                   const int32_t* indices, int64_t idx_row_stride, int k, int64_t max_tokens,
-                   float scale, void* out, int64_t out_row_stride, int64_t out_head_stride,
-                   float* lse, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+// idx_attn_paged and idx_attn_paged_mxfp4 (mx).
+static int attn_paged(const void* q, int64_t q_row_stride, int64_t q_head_stride, int64_t rows, int H,
+                      int latent, const void* cache, int64_t num_pages, int page_size,
+                      const int32_t* block_table, int64_t bt_row_stride, int B,
+                      const int32_t* row_seq, const int32_t* ks, const int32_t* ke,
+                      const int32_t* indices, int64_t idx_row_stride, int k, int64_t max_tokens,
+                      float scale, void* out, int64_t out_row_stride, int64_t out_head_stride,
+                      float* lse, void* workspace, size_t workspace_bytes, bool mx,
+                         hipStream_t stream) {
   if (!attn_sizes_ok(rows, H, latent, max_tokens) || page_size != IDX_PAGE_SIZE || num_pages < 0 ||
       num_pages > IDX_ATTN_MAX_PAGES || B < 0)
     return IDX_ERR_ARG;
@@ -781,7 +783,31 @@ int idx_attn_paged(const void* q, int64_t q_row_stride, int64_t q_head_stride, i
                           bt_row_stride, B, row_seq, row_seq ? 1 : rows / B, ks, ke, indices,
                           idx_row_stride, k, max_tokens, scale, out, out_row_stride,
                           out_head_stride, lse};
-  return launched(mxidx::launch_attn_paged(a, latent, workspace, stream));
+  return launched(mxidx::launch_attn_paged(a, latent, mx, workspace, stream));
+}
+
+int idx_attn_paged(const void* q, int64_t q_row_stride, int64_t q_head_stride, int64_t rows, int H,
+                   int latent, const void* cache, int64_t num_pages, int page_size,
+                   const int32_t* block_table, int64_t bt_row_stride, int B,
+                   const int32_t* row_seq, const int32_t* ks, const int32_t* ke,
+                   const int32_t* indices, int64_t idx_row_stride, int k, int64_t max_tokens,
+                   float scale, void* out, int64_t out_row_stride, int64_t out_head_stride,
+                   float* lse, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  return attn_paged(q, q_row_stride, q_head_stride, rows, H, latent, cache, num_pages, page_size, block_table,
+                    bt_row_stride, B, row_seq, ks, ke, indices, idx_row_stride, k, max_tokens, scale, out,
+                    out_row_stride, out_head_stride, lse, workspace, workspace_bytes, false, stream);
+}
+
+int idx_attn_paged_mxfp4(const void* q, int64_t q_row_stride, int64_t q_head_stride, int64_t rows, int H,
+                         int latent, const uint8_t* cache, int64_t num_pages, int page_size,
+                         const int32_t* block_table, int64_t bt_row_stride, int B,
+                         const int32_t* row_seq, const int32_t* ks, const int32_t* ke,
+                         const int32_t* indices, int64_t idx_row_stride, int k, int64_t max_tokens,
+                         float scale, void* out, int64_t out_row_stride, int64_t out_head_stride,
+                         float* lse, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  return attn_paged(q, q_row_stride, q_head_stride, rows, H, latent, cache, num_pages, page_size, block_table,
+                    bt_row_stride, B, row_seq, ks, ke, indices, idx_row_stride, k, max_tokens, scale, out,
+                    out_row_stride, out_head_stride, lse, workspace, workspace_bytes, true, stream);
 }
 
 }  // extern "C"

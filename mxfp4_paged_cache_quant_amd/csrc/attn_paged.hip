@@ -54,12 +54,13 @@
 #include <algorithm>
 
 #include "common.hpp"
+#include "latent_mxfp4.hpp"
 #include "launch.hpp"
 
 namespace mxidx {
 namespace {
 
-constexpr int kRopeWidth = 64;
+constexpr int kRopeWidth = kLatentRope;
 constexpr int kCus = 256;
 constexpr int kMaxSplits = 128;
 constexpr float kSlack = 8.f;               // weights stay below 2^8 of the reference's
@@ -226,7 +227,60 @@ struct TileCopy {
   }
 };
 
-template <int kLatent, int kTile, int HG, int TH, bool kSmall>
+// The same of a cache in MXFP4: the wave's kMine code rows come to registers, a block's 16 bytes and
+// its scale a lane, and go to the tile as bf16 when the products no longer wait for the tile before;
+// the positional rows go straight to LDS.  Lane t of `rows` holds the number of token t's row.  A place
+// without a row reads row 0's (there is one: a window over a cache without pages is empty) under
+// the scale 1, so that its values are finite: its weight is 0, and a score of its positional part,
+// whatever that holds, is masked.
+template <int kLatent, int kTile, int kMine>
+struct MxCopy {
+  using Page = MxPage<kLatent>;
+  static constexpr int LB = kLatent / kBlock, LC = kLatent / 8, PC = kRopeWidth / 8;
+  static constexpr int kPer = kWave / LB, kLoads = (kMine + kPer - 1) / kPer;      // tokens a load
+  static constexpr int kPosPer = kWave / PC, kPosPieces = kMine / kPosPer;
+  static constexpr int kUnits = 4 * kLoads;            // of the way to LDS: 8 values a lane
+  static_assert(kMine % kPosPer == 0 && (kMine % kPer == 0 || kMine < kPer), "whole instructions");
+
+  uint4 codes[kLoads];
+  uint32_t scale[kLoads];
+  bool ok[kLoads];
+
+  static __device__ __forceinline__ const uint8_t* row_of(const uint8_t* cache, int row, int part, int bytes) {
+    const uint32_t r = row == kNoRow ? 0u : (uint32_t)row;
+    return cache + (int64_t)(r / kPage) * Page::kBytes + part + (int)(r % kPage) * bytes;
+  }
+
+  // The token, from `first` on, that a lane's part of load i belongs to (lanes past the last: its).
+  static __device__ __forceinline__ int token(int i, int ln) {
+    return kMine < kPer ? min(ln / LB, kMine - 1) : i * kPer + ln / LB;
+  }
+
+  __device__ __forceinline__ void load(int i, const uint8_t* cache, int first, int rows, int ln) {
+    const int row = __builtin_amdgcn_ds_bpermute(4 * (first + token(i, ln)), rows);
+    ok[i] = row != kNoRow;
+    codes[i] = *reinterpret_cast<const uint4*>(row_of(cache, row, 0, Page::kCodes) + 16 * (ln % LB));
+    scale[i] = row_of(cache, row, Page::kScaleBase, Page::kScales)[ln % LB];
+  }
+
+  static __device__ __forceinline__ void position(int i, const uint8_t* cache, MXIDX_LDS uint8_t* tile, int first,
+                                                  int rows, int ln) {
+    const int t0 = first + i * kPosPer, t = t0 + ln / PC;
+    const int row = __builtin_amdgcn_ds_bpermute(4 * t, rows);
+    const uint8_t* src = row_of(cache, row, Page::kPosBase, Page::kPos) + (((ln % PC) ^ swz<PC>(t)) << 4);
+    __builtin_amdgcn_global_load_lds((MXIDX_GLOBAL void*)src,
+                                     (MXIDX_LDS void*)(tile + kTile * kLatent * 2 + t0 * PC * 16), 16, 0, 0);
+  }
+
+  __device__ __forceinline__ void unit(int u, MXIDX_LDS uint8_t* tile, int first, int ln) {
+    const int i = u / 4, j = u % 4, t = first + token(i, ln);
+    const uint32_t w = j == 0 ? codes[i].x : j == 1 ? codes[i].y : j == 2 ? codes[i].z : codes[i].w;
+    const uint4 x = mx_decode8(w, mx_scale(ok[i] ? scale[i] : 127u));
+    *(MXIDX_LDS v8s*)(tile + t * (kLatent * 2) + (((4 * (ln % LB) + j) ^ swz<LC>(t)) << 4)) = __builtin_bit_cast(v8s, x);
+  }
+};
+
+template <int kLatent, int kTile, int HG, int TH, bool kSmall, bool kMx>
 __global__ __launch_bounds__(HG * TH * kWave, kTile == 32 ? 2 : 1) void attn_kernel(AttnArgs a, Parts parts) {
   constexpr int kRow = kLatent + kRopeWidth;
   constexpr int kWaves = HG * TH, kHeads = HG * 16;
@@ -236,11 +290,12 @@ __global__ __launch_bounds__(HG * TH * kWave, kTile == 32 ? 2 : 1) void attn_ker
   constexpr int KS = kRow / 32, KL = kLatent / 32;     // contraction steps, latent ones
   constexpr int NV = kLatent / 16;                     // 16-value parts of the output
   constexpr int LC = kLatent / 8;                      // 16-byte chunks of a latent row
-  constexpr int kAhead = kSmall ? 3 : 2;               // operand steps in flight from LDS, as registers allow
+  constexpr int kAhead = kSmall ? 3 : 2;        // operand steps in flight from LDS, as registers allow
   constexpr int kValuesAhead = HG <= 2 ? 4 : kAhead;
   constexpr int kMine = kTile / kWaves;                // rows that a wave copies
   constexpr int kLatentBytes = kTile * kLatent * 2, kTileBytes = kTile * kRow * 2;
   using Copy = TileCopy<kLatent, kTile, kMine, kSmall>;
+  using Mx = MxCopy<kLatent, kTile, kMine>;
   // Two arrays, and the loop below unrolled over them: the compiler then sees that a
   // tile's reads do not touch the one being copied, and does not wait for its copies.
   __shared__ __attribute__((aligned(1024))) uint8_t tile0[kTileBytes];
@@ -261,7 +316,7 @@ __global__ __launch_bounds__(HG * TH * kWave, kTile == 32 ? 2 : 1) void attn_ker
   const int64_t r = r32;
   Row row;
   if (!row_of(a, r, row)) return;
-  const int entries = row.window == 0 ? 0 : a.indices ? a.k : row.window;
+  const int entries = row.window == 0 || (kMx && parts.pages == 0) ? 0 : a.indices ? a.k : row.window;
   const int tiles = (entries + kTile - 1) / kTile;
   const int share = tiles / parts.splits, more = tiles - share * parts.splits;
   const int t0 = split * share + min(split, more);     // the first `more` splits take one more
@@ -283,6 +338,7 @@ __global__ __launch_bounds__(HG * TH * kWave, kTile == 32 ? 2 : 1) void attn_ker
     return ok ? (int)(kSmall ? row * (kRow * 2) : row) : kNoRow;
   };
   const Source cache{static_cast<const char*>(a.cache), parts.cache_bytes, kRow * 2};
+  const uint8_t* mx_cache = static_cast<const uint8_t*>(a.cache);
 
   // The wave's kTokens tokens of a tile against its heads; the pieces of the next tile's
   // copy go between the steps of the first product.
@@ -290,6 +346,7 @@ __global__ __launch_bounds__(HG * TH * kWave, kTile == 32 ? 2 : 1) void attn_ker
                      int rows) __attribute__((always_inline)) {
     const int base = th * kTokens;
     v4f s[NT];
+    Mx raw;                                            // kMx: the next tile's codes
     {
       // LDS offsets of the operands in the tile: the places of the chunks differ
       // between steps by constants xored into few bits (swz), so one register for each
@@ -318,10 +375,16 @@ __global__ __launch_bounds__(HG * TH * kWave, kTile == 32 ? 2 : 1) void attn_ker
 #pragma unroll
         for (int t = 0; t < NT; ++t) s[t] = mfma_bf16(x[k % kAhead][t], q[k], s[t]);
         if (k + kAhead < KS) keys(k + kAhead, x[k % kAhead]);
+        if constexpr (kMx) {
+          if (k < Mx::kLoads) raw.load(k, mx_cache, wave * kMine, rows, ln);
+          if (k >= Mx::kLoads && k < Mx::kLoads + Mx::kPosPieces)
+            Mx::position(k - Mx::kLoads, mx_cache, nxt, wave * kMine, rows, ln);
+        } else {
 #pragma unroll
-        for (int i = 0; i < Copy::kPieces; ++i)
-          if (i * KS / Copy::kPieces == k)
-            Copy::piece(i, cache, nxt, wave * kMine, rows, ln);
+          for (int i = 0; i < Copy::kPieces; ++i)
+            if (i * KS / Copy::kPieces == k)
+              Copy::piece(i, cache, nxt, wave * kMine, rows, ln);
+        }
       }
       __builtin_amdgcn_sched_barrier(0);
     }
@@ -404,6 +467,14 @@ __global__ __launch_bounds__(HG * TH * kWave, kTile == 32 ? 2 : 1) void attn_ker
 #pragma unroll
       for (int i = 0; i < kStep; ++i)
         if (v + i + kValuesAhead < NV) values(v + i + kValuesAhead, y[(v + i) % kValuesAhead]);
+      if constexpr (kMx) {
+        // in the product's second half, when the codes have come
+        constexpr int kFrom = NV / 2 / kStep * kStep, kSlots = (NV - kFrom) / kStep;
+        const int ln = fresh_lane();
+#pragma unroll
+        for (int u = 0; u < Mx::kUnits; ++u)
+          if (kFrom + u * kSlots / Mx::kUnits * kStep == v) raw.unit(u, nxt, wave * kMine, ln);
+      }
     }
     __builtin_amdgcn_sched_barrier(0);
   };
@@ -441,7 +512,22 @@ __global__ __launch_bounds__(HG * TH * kWave, kTile == 32 ? 2 : 1) void attn_ker
                (MXIDX_LDS uint8_t*)(i == 0 ? tile1 : tile0), h < kHeads && head < a.H ? (int)at : kNoRow);
     }
     const int first_rows = rows_of(now, now_page, mask);
-    if (kQTiles == 1) copy_all(cache, (MXIDX_LDS uint8_t*)tile0, first_rows);
+    auto copy_first = [&]() __attribute__((always_inline)) {
+      if constexpr (kMx) {
+        const int ln = fresh_lane();
+        Mx raw;
+#pragma unroll
+        for (int i = 0; i < Mx::kLoads; ++i) raw.load(i, mx_cache, wave * kMine, first_rows, ln);
+#pragma unroll
+        for (int i = 0; i < Mx::kPosPieces; ++i)
+          Mx::position(i, mx_cache, (MXIDX_LDS uint8_t*)tile0, wave * kMine, first_rows, ln);
+#pragma unroll
+        for (int u = 0; u < Mx::kUnits; ++u) raw.unit(u, (MXIDX_LDS uint8_t*)tile0, wave * kMine, ln);
+      } else {
+        copy_all(cache, (MXIDX_LDS uint8_t*)tile0, first_rows);
+      }
+    };
+    if (kQTiles == 1) copy_first();
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
     {
@@ -457,7 +543,7 @@ __global__ __launch_bounds__(HG * TH * kWave, kTile == 32 ? 2 : 1) void attn_ker
     }
     if (kQTiles > 1) {
       __syncthreads();
-      copy_all(cache, (MXIDX_LDS uint8_t*)tile0, first_rows);
+      copy_first();
     }
     // tile t from `cur`, tile t + 1 on its way to `nxt` (behind the last one: zeros)
     auto step = [&](int t, MXIDX_LDS uint8_t* cur, MXIDX_LDS uint8_t* nxt) __attribute__((always_inline)) {
@@ -672,7 +758,7 @@ int64_t align256(int64_t x) { return (x + 255) / 256 * 256; }
 int64_t ml_bytes(int64_t parts) { return align256(parts * 8); }
 int64_t part_bytes(int64_t parts, int latent) { return ml_bytes(parts) + parts * latent * 4; }
 
-template <int kLatent>
+template <int kLatent, bool kMx>
 hipError_t launch(const AttnArgs& a, void* workspace, hipStream_t stream) {
   const Plan p = plan_of(a.rows, a.H, kLatent, a.indices ? a.k : a.max_tokens);
   const int64_t cache_bytes = a.num_pages * kPage * (kLatent + kRopeWidth) * 2;
@@ -687,11 +773,11 @@ hipError_t launch(const AttnArgs& a, void* workspace, hipStream_t stream) {
   const dim3 grid((uint32_t)(a.rows * (p.heads / p.group_heads) * p.splits));
 #define MXIDX_ATTN(heads_, tile_, hg, th)                                                     \
   case heads_ * 64 + tile_:                                                                   \
-    if (small)                                                                               \
-      hipLaunchKernelGGL((attn_kernel<kLatent, tile_, hg, th, true>), grid,                  \
+    if (small && !kMx)                                                                       \
+      hipLaunchKernelGGL((attn_kernel<kLatent, tile_, hg, th, !kMx, kMx>), grid,             \
                          dim3(hg * th * kWave), 0, stream, a, parts);                        \
     else                                                                                     \
-      hipLaunchKernelGGL((attn_kernel<kLatent, tile_, hg, th, false>), grid,                 \
+      hipLaunchKernelGGL((attn_kernel<kLatent, tile_, hg, th, false, kMx>), grid,            \
                          dim3(hg * th * kWave), 0, stream, a, parts);                        \
     break;
   switch (p.group_heads * 64 + p.tile) {
@@ -738,11 +824,11 @@ int64_t attn_workspace_max_bytes(int64_t rows, int H, int latent, int64_t entrie
   return splits <= 1 ? 0 : part_bytes(std::min(split_places(latent) * group, rows * heads * splits), latent);
 }
 
-hipError_t launch_attn_paged(const AttnArgs& a, int latent, void* workspace, hipStream_t stream) {
+hipError_t launch_attn_paged(const AttnArgs& a, int latent, bool mx, void* workspace, hipStream_t stream) {
   switch (latent) {
-    case 128: return launch<128>(a, workspace, stream);
-    case 256: return launch<256>(a, workspace, stream);
-    default: return launch<512>(a, workspace, stream);
+    case 128: return mx ? launch<128, true>(a, workspace, stream) : launch<128, false>(a, workspace, stream);
+    case 256: return mx ? launch<256, true>(a, workspace, stream) : launch<256, false>(a, workspace, stream);
+    default: return mx ? launch<512, true>(a, workspace, stream) : launch<512, false>(a, workspace, stream);
   }
 }
 

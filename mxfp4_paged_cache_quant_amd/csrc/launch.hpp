@@ -212,7 +212,7 @@ struct LatentGatherArgs {
 hipError_t launch_latent_gather(const LatentGatherArgs& a, int latent, hipStream_t stream);
 
 // Attention over the paged latent cache (attn_paged.hip); pointers as in
-// idx_attn_paged.  row_seq null: row r belongs to sequence r / rows_per_seq.
+// idx_attn_paged and idx_attn_paged_mxfp4.  row_seq null: row r belongs to sequence r / rows_per_seq.
 struct AttnArgs {
   const void* q;
   int64_t q_row_stride, q_head_stride, rows;
@@ -239,6 +239,7 @@ struct AttnArgs {
 int64_t attn_workspace_bytes(int64_t rows, int H, int latent, int64_t entries);
 // The same, of any call with up to so many rows, heads and entries.
 int64_t attn_workspace_max_bytes(int64_t rows, int H, int latent, int64_t entries);
-hipError_t launch_attn_paged(const AttnArgs& a, int latent, void* workspace, hipStream_t stream);
+// mx: over MXFP4 pages (latent_mxfp4.hpp).
+hipError_t launch_attn_paged(const AttnArgs& a, int latent, bool mx, void* workspace, hipStream_t stream);
 
 }  // namespace mxidx
