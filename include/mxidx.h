@@ -22,6 +22,9 @@
  *   idx_latent_insert   norm + RoPE of the main cache's latent rows -> paged cache
  *   idx_attn_paged      attention over the paged latent cache: the tokens of
  *                       idx_topk's lists, or whole windows
+ *   idx_latent_insert_mxfp4, idx_latent_gather_mxfp4, idx_attn_paged_mxfp4
+ *                       the latent cache in MXFP4: written, read back, attended
+ *   idx_attn_prompt     causal attention of packed prompts over contiguous keys and values
  *   idx_*_fp8           the FP8 (E4M3) indexer cache the MXFP4 one replaces:
  *                       quantize, insert, gather, dense and paged logits,
  *                       and idx_logits_paged_insert_fp8, its decode step's
@@ -107,6 +110,8 @@ typedef enum { IDX_BF16 = 0, IDX_F32 = 1 } idx_dtype;
 #define IDX_ATTN_MAX_PAGES ((1 << 26) - 1024)   /* row numbers are 32-bit in the kernel */
 #define IDX_ATTN_MAX_TOKENS 0x7ffffe00           /* places of a row: tiles beyond it still count in 32 bits */
 #define IDX_ATTN_MAX_ROWS (1 << 22)              /* and a launch has fewer than 2^32 lanes */
+#define IDX_PROMPT_MAX_STRIDE (1 << 23)          /* elements from one key or value row to the next */
+#define IDX_PROMPT_MAX_WORKSPACE (36ll << 20)    /* enough for every idx_attn_prompt call */
 #define IDX_GATHER_MAX_TOKENS (1 << 29)          /* of a sequence: a workgroup of 256 lanes a page */
 
 /* Version of this ABI (major * 100 + minor). */
@@ -743,6 +748,43 @@ int idx_attn_paged_mxfp4(const void* q, int64_t q_row_stride, int64_t q_head_str
                          const int32_t* indices, int64_t idx_row_stride, int k, int64_t max_tokens,
                          float scale, void* out, int64_t out_row_stride, int64_t out_head_stride,
                          float* lse, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* idx_attn_prompt -- attention of a step's query rows over contiguous keys and values, the requests
+ * of different lengths packed behind one another: whole prompts, the ends of prompts whose beginnings
+ * are cached (read back by idx_latent_gather_mxfp4, say, and projected), or single new tokens.
+ *   s_j = scale * q[t,h] . k[j,h/G],  out[t,h,:] = sum_j softmax_j(s) * v[j,h/G,:],
+ *   lse[t,h] = log sum_j exp(s_j),  G = Hq / Hk
+ * over the visible tokens j.  A row that sees none gets out = 0, lse = -inf.
+ *   seq_lens, query_lens: [B] int32, as for idx_step_map: request b has seq_lens[b] tokens, the last
+ *        query_lens[b] of them this call's rows (0: none).  Its rows begin at row
+ *        sum(query_lens[:b]) of q, its keys and values at row sum(seq_lens[:b]) of k and v.
+ *        Negative lengths count as 0.  Row i of a request stands at position seq_lens[b] -
+ *        query_lens[b] + i (below 0 where it has more rows than tokens: with causal it sees none).
+ *   causal: not 0: a row sees its request's tokens up to its own position; 0: all of them.
+ *   q:   [T, Hq, dk] bf16, row (t, h) at q + t*q_row_stride + h*q_head_stride; rows behind the last
+ *        request's are not read and their out and lse left as they were; rows past T are dropped.
+ *   k, v: [S, Hk, dk] and [S, Hk, dv] bf16, strides as q's, row strides up to
+ *        IDX_PROMPT_MAX_STRIDE; tokens past S count as not there.  May be NULL where S is 0.
+ *        The requests' tokens are finite: where some of a request's rows see a token and others do
+ *        not, its value takes part in the others' products with weight 0.
+ *   Hq a multiple of Hk, 1 <= Hq <= 128; (dk, dv): (64, 64), (128, 128) or (192, 128).  q, k, v 16-byte
+ *        aligned, strides multiples of 8.  T <= IDX_ATTN_MAX_ROWS.
+ *   max_seq_len: host-side upper bound of seq_lens: later tokens are not read.
+ *   out: [T, Hq, dv] bf16, strides multiples of 4, 8-byte aligned; lse: [T, Hq] fp32 or NULL.  They
+ *        overlap no input.
+ *   workspace: device memory of at least idx_attn_prompt_workspace_bytes(T, Hq, Hk, dk, dv, B,
+ *        max_seq_len) bytes, as for idx_attn_paged; IDX_PROMPT_MAX_WORKSPACE are enough for every call.
+ * Products are exact, sums and softmax statistics fp32; the weights take the second product rounded
+ * to bf16, relative to the running maximum (the largest is exactly 1), the statistics unrounded; the
+ * output is rounded once.  Equal calls give equal bits; the order of a row's sums depends on T, Hq, Hk, B
+ * and max_seq_len. */
+size_t idx_attn_prompt_workspace_bytes(int64_t T, int Hq, int Hk, int dk, int dv, int B, int64_t max_seq_len);
+int idx_attn_prompt(const void* q, int64_t q_row_stride, int64_t q_head_stride, int64_t T, int Hq, const void* k,
+                    int64_t k_row_stride, int64_t k_head_stride, const void* v, int64_t v_row_stride,
+                    int64_t v_head_stride, int64_t S, int Hk, int dk, int dv, const int32_t* seq_lens,
+                    const int32_t* query_lens, int B, int64_t max_seq_len, int causal, float scale, void* out,
+                    int64_t out_row_stride, int64_t out_head_stride, float* lse, void* workspace,
+                    size_t workspace_bytes, hipStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -25,6 +25,7 @@ __all__ = [
     "StepMap", "step_map", "norm_rope", "latent_insert", "attn_paged", "attn_workspace_bytes",
     "attn_workspace_max_bytes", "attn_workspace", "LATENT_ROPE", "LATENT_DIMS",
     "latent_insert_mxfp4", "latent_gather_mxfp4", "latent_mxfp4_row_bytes", "attn_paged_mxfp4",
+    "attn_prompt", "attn_prompt_workspace_bytes", "attn_prompt_workspace", "PROMPT_DIMS",
     "FP8_ROW_BYTES", "FP8_SCALE_F32", "FP8_SCALE_POW2",
     "HEAD_DIM", "ROW_BYTES", "PAGE_SIZE", "TOPK_MAX", "EXPORTS",
 ]
@@ -42,6 +43,8 @@ FP8_SCALE_F32, FP8_SCALE_POW2 = 0, 1
 ROPE_NEOX, ROPE_INTERLEAVED = 0, 1
 LATENT_ROPE = 64
 LATENT_DIMS = (128, 256, 512)
+PROMPT_DIMS = ((64, 64), (128, 128), (192, 128))     # (dk, dv) of attn_prompt
+PROMPT_MAX_WORKSPACE = 36 << 20
 
 IDX_BF16, IDX_F32 = 0, 1
 
@@ -146,6 +149,11 @@ EXPORTS = {
                                     _c_void_p, _i64, _int, _c_void_p, _c_void_p, _c_void_p, _c_void_p,
                                     _i64, _int, _i64, _float, _c_void_p, _i64, _i64, _c_void_p, _c_void_p,
                                     ctypes.c_size_t, _c_void_p]),
+    "idx_attn_prompt_workspace_bytes": (ctypes.c_size_t, [_i64, _int, _int, _int, _int, _int, _i64]),
+    "idx_attn_prompt": (_int, [_c_void_p, _i64, _i64, _i64, _int, _c_void_p, _i64, _i64, _c_void_p, _i64,
+                               _i64, _i64, _int, _int, _int, _c_void_p, _c_void_p, _int, _i64, _int,
+                               _float, _c_void_p, _i64, _i64, _c_void_p, _c_void_p, ctypes.c_size_t,
+                               _c_void_p]),
 }
 
 
@@ -958,14 +966,15 @@ def _call(name, device, stream, *args):
         _check(status, name)
 
 
-def _empty(stream, shape, dtype, device, zero=False):
-    """A new tensor, of zeros or of anything, whose memory belongs to the call's stream."""
+def _empty(stream, shape, dtype, device, fill=None):
+    """A new tensor, filled with a number where one is given, whose memory belongs to the call's stream."""
     torch = _torch()
-    make = torch.zeros if zero else torch.empty
-    if stream is None:
-        return make(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        return make(shape, dtype=dtype, device=device)
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return _empty(None, shape, dtype, device, fill)
+    if fill is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    return torch.full(shape, fill, dtype=dtype, device=device)
 
 
 def _device_of(t, name):
@@ -1219,8 +1228,10 @@ def latent_gather_mxfp4(cache, block_table, seq_lens, cu_seq_offsets, max_seq_le
     if cu_seq_offsets.dim() != 1 or cu_seq_offsets.shape[0] < B or not cu_seq_offsets.is_contiguous():
         raise MxidxError(f"cu_seq_offsets must be a contiguous int64 of {B} offsets or more")
     width = latent + LATENT_ROPE
+    if total_tokens < 0:
+        raise MxidxError("total_tokens must not be negative")
     if out is None:
-        out = _empty(stream, (total_tokens, width), torch.bfloat16, device, zero=True)
+        out = _empty(stream, (total_tokens, width), torch.bfloat16, device, fill=0)
     rp = _on(device, out, "out", torch.bfloat16)
     if out.dim() != 2 or out.shape[0] < total_tokens or out.shape[1] != width or \
             (out.stride(1) != 1 and total_tokens):
@@ -1328,3 +1339,64 @@ def attn_paged_mxfp4(q, cache, block_table, ke, scale, indices=None, ks=None, ro
     the same arguments, workspace (attn_workspace's) and results."""
     return _attn_paged("idx_attn_paged_mxfp4", _latent_mxfp4_cache, q, cache, block_table, ke, scale, indices, ks,
                        row_seq, max_tokens, out, lse, workspace, stream)
+
+
+def attn_prompt_workspace_bytes(rows, heads, kv_heads, dk, dv, seqs, max_seq_len):
+    """Workspace bytes of attn_prompt (0: none); PROMPT_MAX_WORKSPACE are enough for every call."""
+    return int(lib().idx_attn_prompt_workspace_bytes(rows, heads, kv_heads, dk, dv, seqs, max_seq_len))
+
+
+def attn_prompt_workspace(device="cuda"):
+    """A workspace for every attn_prompt call: reusable, not by calls that may run at the same time."""
+    return _torch().empty(PROMPT_MAX_WORKSPACE, dtype=_torch().uint8, device=device)
+
+
+def attn_prompt(q, k, v, seq_lens, query_lens, scale, causal=True, max_seq_len=None, out=None, lse=None,
+                workspace=None, stream=None):
+    """Attention of packed requests over contiguous keys and values: q [T, Hq, dk], k [S, Hk, dk],
+    v [S, Hk, dv] (bf16, (dk, dv) one of PROMPT_DIMS, Hq a multiple of Hk): returns (out bf16
+    [T, Hq, dv], lse fp32 [T, Hq]).
+
+    seq_lens / query_lens i32 [B], as step_map's: request b's seq_lens[b] tokens follow the requests'
+    before it in k and v, the last query_lens[b] of them are its rows in q.  ``causal``: a row
+    sees the tokens up to its own (else all of its request's).  Rows behind the last request's
+    are zeros (lse -inf) in a new out and stay as they were in a given one.  ``max_seq_len``
+    bounds seq_lens (None: S).  ``workspace``: attn_prompt_workspace's, allocated here when it is
+    not given."""
+    torch = _torch()
+    device = _device_of(q, "q")
+    bf16 = torch.bfloat16
+    qp, kp, vp = _on(device, q, "q", bf16), _on(device, k, "k", bf16), _on(device, v, "v", bf16)
+    qs, ks, vs = q.shape, k.shape, v.shape
+    if len(qs) != 3 or len(ks) != 3 or len(vs) != 3 or ks[2] != qs[2] or vs[:2] != ks[:2]:
+        raise MxidxError("q, k and v must be [T, Hq, dk], [S, Hk, dk] and [S, Hk, dv]")
+    (T, Hq, dk), (S, Hk, dv) = qs, vs
+    (q0, q1, q2), (k0, k1, k2), (v0, v1, v2) = q.stride(), k.stride(), v.stride()
+    if (T and q2 != 1) or (S and (k2 != 1 or v2 != 1)):
+        raise MxidxError("q, k and v must have a contiguous last dim")
+    B = seq_lens.numel()
+    sp = _on(device, seq_lens, "seq_lens", torch.int32, (B,))
+    np_ = _on(device, query_lens, "query_lens", torch.int32, (B,))
+    if max_seq_len is None:
+        max_seq_len = S
+    if out is None:
+        out = _empty(stream, (T, Hq, dv), bf16, device, fill=0)
+    op = _on(device, out, "out", bf16)
+    o0, o1, o2 = out.stride()
+    if out.shape != (T, Hq, dv) or (o2 != 1 and T):
+        raise MxidxError(f"out must be [{T}, {Hq}, {dv}] with a contiguous last dim")
+    if lse is None:
+        lse = _empty(stream, (T, Hq), torch.float32, device, fill=float("-inf"))
+    lp = _on(device, lse, "lse", torch.float32, (T, Hq))
+    wp, wb = None, 0
+    if workspace is None:
+        need = attn_prompt_workspace_bytes(T, Hq, Hk, dk, dv, B, max_seq_len)
+        if need:
+            workspace = _empty(stream, need, torch.uint8, device)
+    if workspace is not None:
+        wp, wb = _on(device, workspace, "workspace", torch.uint8), workspace.numel()
+        if not workspace.is_contiguous():      # an expanded view has less memory than numel
+            raise MxidxError("workspace must be contiguous")
+    _call("idx_attn_prompt", device, stream, qp, q0, q1, T, Hq, kp, k0, k1, vp, v0, v1, S, Hk, dk, dv, sp, np_, B,
+          max_seq_len, 1 if causal else 0, scale, op, o0, o1, lp, wp, wb)
+    return out, lse

@@ -810,4 +810,47 @@ int idx_attn_paged_mxfp4(const void* q, int64_t q_row_stride, int64_t q_head_str
                     out_row_stride, out_head_stride, lse, workspace, workspace_bytes, true, stream);
 }
 
+// Sizes that the kernel's grid and indexes take; T and B above 0.
+static bool prompt_sizes_ok(int64_t T, int Hq, int Hk, int dk, int dv, int64_t S, int B, int64_t max_seq_len) {
+  const bool dims = (dk == 64 && dv == 64) || (dk == 128 && dv == 128) || (dk == 192 && dv == 128);
+  if (!dims || T < 0 || T > IDX_ATTN_MAX_ROWS || Hq < 1 || Hq > IDX_MAX_HEADS || Hk < 1 || Hq % Hk != 0 || S < 0 ||
+      S > ((int64_t)1 << 40) || B < 0 || B > IDX_MAX_DECODE_SEQS || max_seq_len < 0 || max_seq_len > IDX_ATTN_MAX_TOKENS)
+    return false;
+  return T == 0 || B == 0 || mxidx::prompt_lanes(T, Hq, Hk, B, max_seq_len) < ((int64_t)1 << 32);
+}
+
+size_t idx_attn_prompt_workspace_bytes(int64_t T, int Hq, int Hk, int dk, int dv, int B, int64_t max_seq_len) {
+  if (!prompt_sizes_ok(T, Hq, Hk, dk, dv, 0, B, max_seq_len)) return 0;
+  return (size_t)mxidx::prompt_workspace_bytes(T, Hq, Hk, dv, B, max_seq_len);
+}
+
+int idx_attn_prompt(const void* q, int64_t q_row_stride, int64_t q_head_stride, int64_t T, int Hq, const void* k,
+                    int64_t k_row_stride, int64_t k_head_stride, const void* v, int64_t v_row_stride,
+                    int64_t v_head_stride, int64_t S, int Hk, int dk, int dv, const int32_t* seq_lens,
+                    const int32_t* query_lens, int B, int64_t max_seq_len, int causal, float scale, void* out,
+                    int64_t out_row_stride, int64_t out_head_stride, float* lse, void* workspace,
+                    size_t workspace_bytes, hipStream_t stream) {
+  if (!prompt_sizes_ok(T, Hq, Hk, dk, dv, S, B, max_seq_len)) return IDX_ERR_ARG;
+  if (T == 0 || B == 0) return IDX_OK;        // no row belongs to a request
+  if (!q || !aligned(q, 16) || !stride_ok(q_row_stride, T, dk, 8) || !stride_ok(q_head_stride, Hq, dk, 8))
+    return IDX_ERR_ARG;
+  // a tile's rows are addressed in 32 bits from its first
+  if (S > 0 && (!k || !aligned(k, 16) || !stride_ok(k_row_stride, S, dk, 8) || !stride_ok(k_head_stride, Hk, dk, 8) ||
+                !v || !aligned(v, 16) || !stride_ok(v_row_stride, S, dv, 8) || !stride_ok(v_head_stride, Hk, dv, 8) ||
+                (S > 1 && (k_row_stride > IDX_PROMPT_MAX_STRIDE || v_row_stride > IDX_PROMPT_MAX_STRIDE))))
+    return IDX_ERR_ARG;
+  if (!out || !aligned(out, 8) || !stride_ok(out_row_stride, T, dv, 4) || !stride_ok(out_head_stride, Hq, dv, 4))
+    return IDX_ERR_ARG;
+  if (!seq_lens || !aligned(seq_lens, 4) || !query_lens || !aligned(query_lens, 4) || !aligned(lse, 4))
+    return IDX_ERR_ARG;
+  const size_t need = idx_attn_prompt_workspace_bytes(T, Hq, Hk, dk, dv, B, max_seq_len);
+  if (need > 0 && (!workspace || !aligned(workspace, 256) || workspace_bytes < need)) return IDX_ERR_ARG;
+  int st = gate_current();
+  if (st != IDX_OK) return st;
+  const mxidx::PromptArgs a{q, q_row_stride, q_head_stride, T, Hq, k, S > 1 ? k_row_stride : dk, k_head_stride,
+                            v, S > 1 ? v_row_stride : dv, v_head_stride, S, Hk, seq_lens, query_lens, B, max_seq_len,
+                            causal != 0, scale, out, out_row_stride, out_head_stride, lse};
+  return launched(mxidx::launch_attn_prompt(a, dk, dv, workspace, stream));
+}
+
 }  // extern "C"

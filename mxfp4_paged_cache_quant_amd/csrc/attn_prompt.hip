@@ -1,0 +1,439 @@
+// Attention of packed prompts over contiguous keys and values (idx_attn_prompt): for query row i of
+// a request of `len` tokens, `new` of them rows of this call, and head h of key / value head h / G,
+//   s_j = scale * q[i,h] . k_j,  out = sum_j exp(s_j - m) v_j / l,  l = sum_j exp(s_j - m),
+//   lse = m + log l,  m = max_j s_j
+// over the request's tokens j (causal: those up to position len - new + i).
+//
+// One pass over the tokens with the running maximum and sum (in powers of two): a new maximum
+// scales what was summed so far by 2^(m_old - m_new).
+//
+// Work mapping: a workgroup takes `slots` of one request, 32 a wave: a slot is a query row and one
+// of the G heads that share a key / value head, so that rows of few tokens fill a wave with heads.
+// It walks the request's tokens 64 (a tile) at a time, keys and values going straight to LDS (two
+// tiles, the next one's copies under the current one's products).  Products run on the 32x32x16
+// bf16 MFMA in the transposed form:
+//   S^T = K Q^T   A = 32 tokens of the tile, B = the wave's 32 slots
+//   O^T = V^T P^T A = 32 of the values over 16 tokens, B = the weights
+// so a lane (and the one 32 lanes on) holds one slot throughout: the weights leave the first product
+// in the registers where the second takes them (half h of the lanes: tokens 4h..4h+3 and
+// 8+4h..8+4h+3 of 16), and the running maximum and sum are one register each.
+#include <algorithm>
+
+#include "common.hpp"
+#include "launch.hpp"
+
+namespace mxidx {
+namespace {
+
+constexpr int kTile = 64;                   // tokens at a time
+constexpr int kWaveSlots = 32;
+
+typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
+typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
+typedef short v4s __attribute__((ext_vector_type(4)));
+typedef short v8s __attribute__((ext_vector_type(8)));
+typedef float v16f __attribute__((ext_vector_type(16)));
+#define MXIDX_LDS __attribute__((address_space(3)))
+
+__device__ __forceinline__ v16f mfma32(v8s a, v8s b, v16f c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, a), __builtin_bit_cast(v8bf, b), c, 0, 0, 0);
+}
+
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  const v2bf r = {(__bf16)a, (__bf16)b};
+  return __builtin_bit_cast(uint32_t, r);
+}
+
+// The larger of a lane's value and that of the lane 32 on, and their sum.
+__device__ __forceinline__ float max_halves(float v) {
+  const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+}
+__device__ __forceinline__ float sum_halves(float v) {
+  const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(a[0]) + __uint_as_float(a[1]);
+}
+
+// LDS place of a 16-byte chunk: chunk c of token t's row at c ^ swz(t).  Keys are read a chunk of 32
+// tokens at a time, values four chunks of eight tokens by transposing reads.
+template <int C>                            // chunks of a row: 16 (256 bytes) or 8
+__device__ __forceinline__ int key_swz(int t) { return C == 16 ? t & 15 : (t >> 1) & 7; }
+template <int C>
+__device__ __forceinline__ int value_swz(int t) { return C == 16 ? (t & 3) << 2 : ((t >> 1) & 1) << 2; }
+
+// The inclusive sum over a wave's lanes.
+__device__ __forceinline__ uint32_t wave_scan(uint32_t x) {
+#define MXIDX_ADD(control, rows) x += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, control, rows, 0xf, true)
+  MXIDX_ADD(0x111, 0xf);                    // one, two, four and eight lanes up in rows of 16
+  MXIDX_ADD(0x112, 0xf);
+  MXIDX_ADD(0x114, 0xf);
+  MXIDX_ADD(0x118, 0xf);
+  MXIDX_ADD(0x142, 0xa);                    // the first and third row's sum to the second and fourth
+  MXIDX_ADD(0x143, 0xc);                    // the lower half's to the upper
+#undef MXIDX_ADD
+  return x;
+}
+
+// A request's tile of query rows, and where its rows, keys and values begin.
+struct Found {
+  int64_t row, key;        // the first query row and the first key of the request
+  int n, len, pos0;        // its rows and its keys that there are, the position of its first row
+  int tile;                // -1: no such tile
+};
+
+// Tile `want` of all requests' tiles of `tok` rows, a request's last rows, which see most, first.  Every
+// wave looks for itself, 64 requests at a time.
+__device__ Found find_tile(const PromptArgs& a, int tok, uint32_t want) {
+  const int ln = threadIdx.x & (kWave - 1);
+  const uint32_t T = (uint32_t)a.T;                    // below 2^23: sums of 64 fit 32 bits
+  uint32_t row0 = 0, tile0 = 0;
+  int64_t key0 = 0;
+  Found f;
+  f.tile = -1;
+  for (int b0 = 0; b0 < a.B; b0 += kWave) {
+    const int b = b0 + ln;
+    const int n = b < a.B ? max(a.query_lens[b], 0) : 0, len = b < a.B ? max(a.seq_lens[b], 0) : 0;
+    const uint32_t mine = min((uint32_t)n, T), row_end = wave_scan(mine) + row0, row = row_end - mine;
+    const uint32_t there = row < T ? min(mine, T - row) : 0;
+    const uint32_t tiles = (there + (uint32_t)tok - 1) / (uint32_t)tok, tile_end = wave_scan(tiles) + tile0;
+    // the keys' sum in two halves of 16 bits: 64 of each fit
+    const uint32_t low = wave_scan((uint32_t)len & 0xffffu), high = wave_scan((uint32_t)len >> 16);
+    const int64_t key_end = key0 + ((int64_t)high << 16) + low;
+    const uint64_t hit = __ballot(want < tile_end && want >= tile_end - tiles);
+    if (hit) {
+      const int from = __builtin_ctzll(hit);
+      auto of = [&](uint32_t x) { return (uint32_t)__builtin_amdgcn_readlane((int)x, from); };
+      f.row = of(row);
+      f.len = (int)of((uint32_t)len);
+      f.n = (int)of(there);
+      f.pos0 = f.len - (int)of((uint32_t)n);
+      const int64_t key = key_end - len;
+      f.key = (int64_t)((uint64_t)of((uint32_t)((uint64_t)key >> 32)) << 32 | of((uint32_t)key));
+      f.tile = (int)(of(tile_end) - 1 - want);
+      f.len = (int)min((int64_t)min((int64_t)f.len, a.max_seq_len), max(a.S - f.key, (int64_t)0));
+      return f;
+    }
+    row0 = min((uint32_t)__builtin_amdgcn_readlane((int)row_end, kWave - 1), T);
+    tile0 = (uint32_t)__builtin_amdgcn_readlane((int)tile_end, kWave - 1);
+    key0 += ((int64_t)__builtin_amdgcn_readlane((int)high, kWave - 1) << 16) + (uint32_t)__builtin_amdgcn_readlane((int)low, kWave - 1);
+  }
+  return f;
+}
+
+// Of the split form: for each (row, head, split) the unscaled sums, and (m, l).
+struct PromptParts {
+  float* o;
+  float* ml;
+  int splits, tok, heads, blocks;           // rows of a tile; heads of a block, blocks of a key head's
+  int64_t tiles;                            // at most, of all requests
+};
+
+// C chunks of each of 64 rows to LDS, kWaves waves sharing them: piece i of kPieces of a wave.
+template <int C, int kWaves>
+struct RowCopy {
+  static constexpr int kPer = kWave / C, kPieces = kTile / kPer / kWaves;   // rows an instruction
+  static_assert(kPieces * kPer * kWaves == kTile, "whole instructions");
+  template <bool kKeys>
+  static __device__ __forceinline__ void piece(int i, __amdgpu_buffer_rsrc_t rs, MXIDX_LDS uint8_t* dst,
+                                               uint32_t stride, uint32_t offset, int wave, int ln) {
+    const int t0 = (i * kWaves + wave) * kPer, t = t0 + ln / C;
+    const int c = (ln % C) ^ (kKeys ? key_swz<C>(t) : value_swz<C>(t));
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (MXIDX_LDS void*)(dst + t0 * C * 16), 16,
+                                             (int)((uint32_t)t * stride + offset + (uint32_t)c * 16u), 0, 0, 0);
+  }
+};
+
+template <int kDk, int kDv, int kWaves>
+__global__ __launch_bounds__(kWaves * kWave, kWaves == 1 ? 1 : 2) void prompt_kernel(PromptArgs a, PromptParts parts) {
+  constexpr int kA = kDk >= 128 ? 128 : 0, kB = kDk - kA;       // a key's 256-byte and 128-byte parts
+  static_assert(kB == 0 || kB == 64, "key parts");
+  constexpr int KS = kDk / 16, KA = kA / 16;                    // contraction steps, of the first part
+  constexpr int NV = kDv / 32, VC = kDv / 8;                    // 32-value parts, chunks of a value row
+  constexpr int kKeyA = kTile * kA * 2, kKeyB = kTile * kB * 2, kValue = kTile * kDv * 2;
+  constexpr int kBytes = kKeyA + kKeyB + kValue;
+  __shared__ __attribute__((aligned(1024))) uint8_t tile0[kBytes];
+  __shared__ __attribute__((aligned(1024))) uint8_t tile1[kBytes];
+
+  // each XCD takes a run of neighbouring numbers: the splits and tiles of one head, which read the
+  // same keys and values
+  const uint32_t xcd = blockIdx.x % 8, number = xcd * (gridDim.x / 8) + min(xcd, gridDim.x % 8) + blockIdx.x / 8;
+  const uint32_t unit = number / (uint32_t)parts.splits;
+  const int split = (int)(number - unit * (uint32_t)parts.splits);
+  const uint32_t hb = unit / (uint32_t)parts.tiles;
+  const int kv_head = (int)(hb / (uint32_t)parts.blocks), block = (int)(hb - kv_head * (uint32_t)parts.blocks);
+  const Found f = find_tile(a, parts.tok, unit - hb * (uint32_t)parts.tiles);
+  if (f.tile < 0) return;
+
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), ln = threadIdx.x & (kWave - 1);
+  const int half = ln >> 5, n = ln & 31;
+  const int G = a.Hq / a.Hk, h0 = block * parts.heads, heads = min(parts.heads, G - h0);
+  // this lane's slot: past the last row or head a live one's, not written
+  const int slot = wave * kWaveSlots + n;
+  const int row_in = slot / parts.heads, head_in = slot - row_in * parts.heads;
+  const int i0 = f.tile * parts.tok, last = min(i0 + parts.tok, f.n) - 1;
+  const int i = min(i0 + row_in, last);
+  const bool live = i0 + row_in <= last && head_in < heads;
+  const int64_t row = f.row + i;
+  const int head = kv_head * G + h0 + min(head_in, heads - 1);
+  auto limit = [&](int at) { return a.causal ? max(min(f.pos0 + at + 1, f.len), 0) : f.len; };   // visible: below it
+  const int lim = limit(i);
+  const int wave_lo = __builtin_amdgcn_readfirstlane(limit(min(i0 + wave * kWaveSlots / parts.heads, last)));
+  const int wave_hi = __builtin_amdgcn_readfirstlane(limit(min(i0 + (wave * kWaveSlots + kWaveSlots - 1) / parts.heads, last)));
+  const int end = __builtin_amdgcn_readfirstlane(limit(last));
+  const int tiles = (end + kTile - 1) / kTile, share = tiles / parts.splits, more = tiles - share * parts.splits;
+  const int t0 = split * share + min(split, more), t1 = t0 + share + (split < more ? 1 : 0);
+
+  v8s q[KS];                                           // step s: values 16s + 8 half .. +7
+  {
+    const uint16_t* src = static_cast<const uint16_t*>(a.q) + row * a.q_row_stride + head * a.q_head_stride + 8 * half;
+#pragma unroll
+    for (int k = 0; k < KS; ++k) q[k] = *reinterpret_cast<const v8s*>(src + 16 * k);
+  }
+  // scores in powers of two; a negative scale by the query's sign, so that a larger product is a larger score
+  const float scale2 = fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1.17549435e-38f);
+  if (a.scale < 0.f) {
+#pragma unroll
+    for (int k = 0; k < KS; ++k) q[k] ^= (short)0x8000;
+  }
+
+  v16f o[NV];
+#pragma unroll
+  for (int v = 0; v < NV; ++v)
+#pragma unroll
+    for (int j = 0; j < 16; ++j) o[v][j] = 0.f;
+  float m = neg_inf(), l = 0.f;                        // l: this lane's tokens only
+
+  const char* kbase = static_cast<const char*>(a.k) + (f.key * a.k_row_stride + kv_head * a.k_head_stride) * 2;
+  const char* vbase = static_cast<const char*>(a.v) + (f.key * a.v_row_stride + kv_head * a.v_head_stride) * 2;
+  const uint32_t kstride = (uint32_t)(a.k_row_stride * 2), vstride = (uint32_t)(a.v_row_stride * 2);
+  auto copy = [&](int t, MXIDX_LDS uint8_t* tile) __attribute__((always_inline)) {
+    // rows past the request's last are out of the descriptors' range and read as zeros
+    const int left = min(f.len - t * kTile, kTile);
+    const __amdgpu_buffer_rsrc_t kr =
+        buffer_rsrc(kbase + (int64_t)t * kTile * kstride, (int)((uint32_t)(left - 1) * kstride + kDk * 2));
+    const __amdgpu_buffer_rsrc_t vr =
+        buffer_rsrc(vbase + (int64_t)t * kTile * vstride, (int)((uint32_t)(left - 1) * vstride + kDv * 2));
+    if constexpr (kA > 0) {
+#pragma unroll
+      for (int i = 0; i < RowCopy<16, kWaves>::kPieces; ++i)
+        RowCopy<16, kWaves>::template piece<true>(i, kr, tile, kstride, 0, wave, ln);
+    }
+    if constexpr (kB > 0) {
+#pragma unroll
+      for (int i = 0; i < RowCopy<8, kWaves>::kPieces; ++i)
+        RowCopy<8, kWaves>::template piece<true>(i, kr, tile + kKeyA, kstride, kA * 2, wave, ln);
+    }
+#pragma unroll
+    for (int i = 0; i < RowCopy<VC, kWaves>::kPieces; ++i)
+      RowCopy<VC, kWaves>::template piece<false>(i, vr, tile + kKeyA + kKeyB, vstride, 0, wave, ln);
+  };
+
+  auto compute = [&](int t, MXIDX_LDS const uint8_t* tile) __attribute__((always_inline)) {
+    const int first = t * kTile;
+    if (first >= wave_hi) return;                      // uniform: no slot sees the tile
+    v16f s[2];
+#pragma unroll
+    for (int p = 0; p < 2; ++p)
+#pragma unroll
+      for (int j = 0; j < 16; ++j) s[p][j] = 0.f;
+#pragma unroll
+    for (int k = 0; k < KS; ++k)
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        const int tok = 32 * p + n;
+        const int at = k < KA ? tok * 256 + (((2 * k + half) ^ key_swz<16>(tok)) << 4)
+                              : kKeyA + tok * 128 + (((2 * (k - KA) + half) ^ key_swz<8>(tok)) << 4);
+        s[p] = mfma32(*(MXIDX_LDS const v8s*)(tile + at), q[k], s[p]);
+      }
+    // s[p][j]: token first + 32p + 8 (j / 4) + 4 half + j % 4
+    if (first + kTile > wave_lo) {
+#pragma unroll
+      for (int p = 0; p < 2; ++p)
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          if (first + 32 * p + 8 * (j / 4) + 4 * half + j % 4 >= lim) s[p][j] = neg_inf();
+    }
+    float top = neg_inf();
+#pragma unroll
+    for (int p = 0; p < 2; ++p)
+#pragma unroll
+      for (int j = 0; j < 16; ++j) top = fmaxf(top, s[p][j]);
+    top = max_halves(top) * scale2;
+    const float m2 = fmaxf(m, top);
+    if (__any(m2 > m)) {
+      const float fac = m2 > m && m != neg_inf() ? __builtin_amdgcn_exp2f(m - m2) : 1.f;
+      l *= fac;
+#pragma unroll
+      for (int v = 0; v < NV; ++v) o[v] *= fac;
+    }
+    m = m2;
+    const float ref = m == neg_inf() ? 0.f : m;
+    uint32_t w[4][4];                                  // 16-token step u: its weights, two a register
+#pragma unroll
+    for (int p = 0; p < 2; ++p)
+#pragma unroll
+      for (int j = 0; j < 16; j += 2) {
+        const float x = __builtin_amdgcn_exp2f(fmaf(s[p][j], scale2, -ref));
+        const float y = __builtin_amdgcn_exp2f(fmaf(s[p][j + 1], scale2, -ref));
+        l += x + y;
+        w[2 * p + j / 8][(j % 8) / 2] = pack2(x, y);
+      }
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        // lane 4j + c of a 16-lane group reads token 4 half + j, values 4c..4c+3 of its 16
+        v4s x[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int tok = 16 * u + 8 * e + 4 * half + ((ln & 15) >> 2);
+          const int chunk = 4 * v + 2 * ((ln >> 4) & 1) + ((ln & 3) >> 1);
+          x[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((MXIDX_LDS v4s*)(
+              tile + kKeyA + kKeyB + tok * (kDv * 2) + ((chunk ^ value_swz<VC>(tok)) << 4) + 8 * (ln & 1)));
+        }
+        o[v] = mfma32(__builtin_shufflevector(x[0], x[1], 0, 1, 2, 3, 4, 5, 6, 7),
+                      __builtin_bit_cast(v8s, uint4{w[u][0], w[u][1], w[u][2], w[u][3]}), o[v]);
+      }
+  };
+
+  if (t0 < t1) copy(t0, (MXIDX_LDS uint8_t*)tile0);
+  auto step = [&](int t, MXIDX_LDS uint8_t* cur, MXIDX_LDS uint8_t* nxt) __attribute__((always_inline)) {
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    if (t + 1 < t1) copy(t + 1, nxt);
+    compute(t, cur);
+  };
+  for (int t = t0; t < t1; t += 2) {
+    step(t, (MXIDX_LDS uint8_t*)tile0, (MXIDX_LDS uint8_t*)tile1);
+    if (t + 1 < t1) step(t + 1, (MXIDX_LDS uint8_t*)tile1, (MXIDX_LDS uint8_t*)tile0);
+  }
+
+  l = sum_halves(l);
+  if (!live) return;
+  const int64_t at = row * a.Hq + head;
+  if (parts.splits == 1) {
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    if (a.lse && half == 0) a.lse[at] = l == 0.f ? neg_inf() : m * 0.6931471805599453f + logf(l);
+    uint16_t* dst = static_cast<uint16_t*>(a.out) + row * a.out_row_stride + head * a.out_head_stride + 4 * half;
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+      for (int j = 0; j < 16; j += 4)
+        *reinterpret_cast<uint2*>(dst + 32 * v + 2 * j) =
+            make_uint2(pack2(o[v][j] * inv, o[v][j + 1] * inv), pack2(o[v][j + 2] * inv, o[v][j + 3] * inv));
+  } else {
+    const int64_t part = at * parts.splits + split;
+    if (half == 0) *reinterpret_cast<float2*>(parts.ml + 2 * part) = make_float2(m, l);
+    if (l == 0.f) return;                              // the join does not read its sums
+    float* dst = parts.o + part * kDv + 4 * half;
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+      for (int j = 0; j < 16; j += 4)
+        *reinterpret_cast<float4*>(dst + 32 * v + 2 * j) = make_float4(o[v][j], o[v][j + 1], o[v][j + 2], o[v][j + 3]);
+  }
+}
+
+// The splits' sums of one (row, head), kDv / 4 lanes of 4 values each.
+template <int kDv>
+__global__ __launch_bounds__(256) void prompt_join_kernel(PromptArgs a, PromptParts parts) {
+  constexpr int W = kDv / 4;
+  __shared__ int64_t wave_rows[4];
+  // the rows that there are: those behind the last request's stay as they were
+  int64_t rows = 0;
+  for (int b = threadIdx.x; b < a.B; b += 256) rows += max(a.query_lens[b], 0);
+#pragma unroll
+  for (int d = 1; d < kWave; d <<= 1) rows += __shfl_xor(rows, d);
+  if (threadIdx.x % kWave == 0) wave_rows[threadIdx.x / kWave] = rows;
+  __syncthreads();
+  rows = min(wave_rows[0] + wave_rows[1] + wave_rows[2] + wave_rows[3], a.T);
+  const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) / W;
+  const int i = threadIdx.x % W;
+  const int64_t row = at / a.Hq;
+  const int head = (int)(at - row * a.Hq);
+  if (row >= rows) return;
+  const int64_t first = at * parts.splits;
+  float m = neg_inf();
+  for (int s = 0; s < parts.splits; ++s) m = fmaxf(m, parts.ml[2 * (first + s)]);
+  const float ref = m == neg_inf() ? 0.f : m;
+  v4f o = {0.f, 0.f, 0.f, 0.f};
+  float l = 0.f;
+  for (int s = 0; s < parts.splits; ++s) {
+    const float2 ml = *reinterpret_cast<const float2*>(parts.ml + 2 * (first + s));
+    if (ml.y == 0.f) continue;                         // nothing seen: no sums written
+    const float f = __builtin_amdgcn_exp2f(ml.x - ref);
+    l += f * ml.y;
+    o += f * *reinterpret_cast<const v4f*>(parts.o + (first + s) * kDv + 4 * i);
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + row * a.out_row_stride + head * a.out_head_stride + 4 * i) =
+      make_uint2(pack2(o[0] * inv, o[1] * inv), pack2(o[2] * inv, o[3] * inv));
+  if (a.lse && i == 0) a.lse[at] = l == 0.f ? neg_inf() : m * 0.6931471805599453f + logf(l);
+}
+
+struct Plan {
+  int waves;               // of a workgroup, 32 slots each
+  int heads, blocks;       // heads of a slot block, blocks of a key head's group
+  int tok;                 // rows of a tile
+  int64_t tiles;           // at most, of all requests
+  int splits;
+};
+
+Plan plan_of(int64_t T, int Hq, int Hk, int B, int64_t max_seq_len) {
+  Plan p;
+  const int G = Hq / Hk;
+  const int64_t seqs = std::min<int64_t>(B, T), each = (T + seqs - 1) / std::max<int64_t>(seqs, 1);   // rows of a request
+  p.waves = each * G <= kWaveSlots ? 1 : 4;
+  const int slots = p.waves * kWaveSlots;
+  p.heads = std::min(G, slots);
+  p.blocks = (G + p.heads - 1) / p.heads;
+  p.tok = slots / p.heads;
+  p.tiles = T / p.tok + seqs;
+  const int64_t units = p.tiles * Hk * p.blocks, places = p.waves == 1 ? 1024 : 512;
+  const int64_t tiles = (max_seq_len + kTile - 1) / kTile;
+  p.splits = (int)std::max<int64_t>(1, std::min<int64_t>({places / std::max<int64_t>(units, 1), (tiles + 3) / 4, 64}));
+  return p;
+}
+
+int64_t align256(int64_t x) { return (x + 255) / 256 * 256; }
+
+template <int kDk, int kDv>
+hipError_t launch(const PromptArgs& a, void* workspace, hipStream_t stream) {
+  const Plan p = plan_of(a.T, a.Hq, a.Hk, a.B, a.max_seq_len);
+  PromptParts parts{nullptr, nullptr, p.splits, p.tok, p.heads, p.blocks, p.tiles};
+  if (p.splits > 1) {
+    parts.ml = static_cast<float*>(workspace);
+    parts.o = reinterpret_cast<float*>(static_cast<char*>(workspace) + align256(a.T * a.Hq * p.splits * 8));
+  }
+  const dim3 grid((uint32_t)(p.tiles * a.Hk * p.blocks * p.splits));
+  if (p.waves == 1)
+    hipLaunchKernelGGL((prompt_kernel<kDk, kDv, 1>), grid, dim3(kWave), 0, stream, a, parts);
+  else
+    hipLaunchKernelGGL((prompt_kernel<kDk, kDv, 4>), grid, dim3(4 * kWave), 0, stream, a, parts);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || p.splits == 1) return e;
+  const dim3 join((uint32_t)((a.T * a.Hq * (kDv / 4) + 255) / 256));
+  hipLaunchKernelGGL((prompt_join_kernel<kDv>), join, dim3(256), 0, stream, a, parts);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+int64_t prompt_workspace_bytes(int64_t T, int Hq, int Hk, int dv, int B, int64_t max_seq_len) {
+  if (T == 0 || B == 0) return 0;
+  const Plan p = plan_of(T, Hq, Hk, B, max_seq_len);
+  return p.splits == 1 ? 0 : align256(T * Hq * p.splits * 8) + T * Hq * p.splits * dv * 4;
+}
+
+int64_t prompt_lanes(int64_t T, int Hq, int Hk, int B, int64_t max_seq_len) {
+  const Plan p = plan_of(T, Hq, Hk, B, max_seq_len);
+  return p.tiles * Hk * p.blocks * p.splits * p.waves * kWave;
+}
+
+hipError_t launch_attn_prompt(const PromptArgs& a, int dk, int dv, void* workspace, hipStream_t stream) {
+  if (dk == 64 && dv == 64) return launch<64, 64>(a, workspace, stream);
+  if (dk == 128 && dv == 128) return launch<128, 128>(a, workspace, stream);
+  return launch<192, 128>(a, workspace, stream);
+}
+
+}  // namespace mxidx

@@ -242,4 +242,29 @@ int64_t attn_workspace_max_bytes(int64_t rows, int H, int latent, int64_t entrie
 // mx: over MXFP4 pages (latent_mxfp4.hpp).
 hipError_t launch_attn_paged(const AttnArgs& a, int latent, bool mx, void* workspace, hipStream_t stream);
 
+// Attention of packed prompts over contiguous keys and values (attn_prompt.hip); pointers as in
+// idx_attn_prompt.
+struct PromptArgs {
+  const void* q;
+  int64_t q_row_stride, q_head_stride, T;
+  int Hq;
+  const void* k;
+  int64_t k_row_stride, k_head_stride;
+  const void* v;
+  int64_t v_row_stride, v_head_stride, S;
+  int Hk;
+  const int32_t* seq_lens;
+  const int32_t* query_lens;
+  int B;
+  int64_t max_seq_len;
+  bool causal;
+  float scale;
+  void* out;
+  int64_t out_row_stride, out_head_stride;
+  float* lse;
+};
+int64_t prompt_workspace_bytes(int64_t T, int Hq, int Hk, int dv, int B, int64_t max_seq_len);
+int64_t prompt_lanes(int64_t T, int Hq, int Hk, int B, int64_t max_seq_len);   // of the launch
+hipError_t launch_attn_prompt(const PromptArgs& a, int dk, int dv, void* workspace, hipStream_t stream);
+
 }  // namespace mxidx

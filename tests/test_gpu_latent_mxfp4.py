@@ -265,5 +265,5 @@ def test_refusals_of_the_wrappers():
                    dict(out=torch.zeros((2, 192), **bf)), dict(out=torch.zeros((1, 320), **bf)),
                    dict(out=torch.zeros((2, 320), device="cuda")), dict(out=torch.zeros((320, 2), **bf).t()),
                    dict(max_seq_len=-1)):
-        with pytest.raises((mx.MxidxError, RuntimeError)):
+        with pytest.raises(mx.MxidxError):
             mx.latent_gather_mxfp4(**{**ok, **change})
