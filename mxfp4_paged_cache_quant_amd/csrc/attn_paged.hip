@@ -70,6 +70,7 @@ typedef __bf16 v4bf __attribute__((ext_vector_type(4)));
 typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
 typedef short v4s __attribute__((ext_vector_type(4)));
 typedef short v8s __attribute__((ext_vector_type(8)));
+typedef int v4i __attribute__((ext_vector_type(4)));
 #define MXIDX_LDS __attribute__((address_space(3)))
 #define MXIDX_GLOBAL __attribute__((address_space(1)))
 
@@ -227,56 +228,99 @@ struct TileCopy {
   }
 };
 
-// The same of a cache in MXFP4: the wave's kMine code rows come to registers, a block's 16 bytes and
-// its scale a lane, and go to the tile as bf16 when the products no longer wait for the tile before;
-// the positional rows go straight to LDS.  Lane t of `rows` holds the number of token t's row.  A place
-// without a row reads row 0's (there is one: a window over a cache without pages is empty) under
-// the scale 1, so that its values are finite: its weight is 0, and a score of its positional part,
-// whatever that holds, is masked.
-template <int kLatent, int kTile, int kMine>
+// The same of a cache in MXFP4.  The wave's kMine code rows go straight to a buffer in LDS of their own,
+// a block's 16 bytes a lane, two tiles ahead; each lane then takes what it copied, its block's scale
+// in a register, to the next tile as bf16 while the second product runs.  The positional rows go
+// straight to the tile.  Lane t of `rows` holds token t's row: where 32-bit offsets reach the whole cache
+// (kSmall) its page's byte there, a multiple of 256, plus its place in the page; else its number.
+// A place without a row is out of the descriptor's range and reads as zeros; in the other form it
+// reads row 0's (there is one: a window over a cache without pages is empty) under the scale 1,
+// so that its values are finite: its weight is 0, and a score of its positional part, whatever that
+// holds, is masked.
+template <int kLatent, int kTile, int kMine, bool kSmall>
 struct MxCopy {
   using Page = MxPage<kLatent>;
+  using Bytes = MXIDX_GLOBAL const uint8_t*;
   static constexpr int LB = kLatent / kBlock, LC = kLatent / 8, PC = kRopeWidth / 8;
   static constexpr int kPer = kWave / LB, kLoads = (kMine + kPer - 1) / kPer;      // tokens a load
   static constexpr int kPosPer = kWave / PC, kPosPieces = kMine / kPosPer;
-  static constexpr int kUnits = 4 * kLoads;            // of the way to LDS: 8 values a lane
+  static constexpr int kRawBytes = kLoads * kWave * 16;                            // of the wave
   static_assert(kMine % kPosPer == 0 && (kMine % kPer == 0 || kMine < kPer), "whole instructions");
+  static_assert(Page::kBytes % 256 == 0 && Page::kBytes < 65536, "a row's place fits its page's lowest bits");
 
-  uint4 codes[kLoads];
   uint32_t scale[kLoads];
-  bool ok[kLoads];
+  v4i codes;
 
-  static __device__ __forceinline__ const uint8_t* row_of(const uint8_t* cache, int row, int part, int bytes) {
-    const uint32_t r = row == kNoRow ? 0u : (uint32_t)row;
-    return cache + (int64_t)(r / kPage) * Page::kBytes + part + (int)(r % kPage) * bytes;
+  static __device__ __forceinline__ int row_code(bool ok, uint32_t page, uint32_t place) {
+    return !ok ? kNoRow : (int)(kSmall ? page * (uint32_t)Page::kBytes + place : page * kPage + place);
   }
 
   // The token, from `first` on, that a lane's part of load i belongs to (lanes past the last: its).
-  static __device__ __forceinline__ int token(int i, int ln) {
-    return kMine < kPer ? min(ln / LB, kMine - 1) : i * kPer + ln / LB;
+  static __device__ __forceinline__ int token(int i, uint32_t ln) {
+    return kMine < kPer ? min((int)(ln / LB), kMine - 1) : i * kPer + (int)(ln / LB);
   }
 
-  __device__ __forceinline__ void load(int i, const uint8_t* cache, int first, int rows, int ln) {
-    const int row = __builtin_amdgcn_ds_bpermute(4 * (first + token(i, ln)), rows);
-    ok[i] = row != kNoRow;
-    codes[i] = *reinterpret_cast<const uint4*>(row_of(cache, row, 0, Page::kCodes) + 16 * (ln % LB));
-    scale[i] = row_of(cache, row, Page::kScaleBase, Page::kScales)[ln % LB];
+  // Byte `at` of the row's part that begins at `part` of its page, `bytes` a row.
+  static __device__ __forceinline__ uint32_t offset(int row, uint32_t bytes, uint32_t at) {
+    const uint32_t place = (uint32_t)row & (kPage - 1);
+    return ((uint32_t)row & ~(uint32_t)(kPage - 1)) + place * bytes + at;
+  }
+  static __device__ __forceinline__ Bytes address(Bytes cache, int row, uint32_t bytes, uint32_t at) {
+    asm volatile("" : "+s"(cache));                    // added to the offset where it is: no copy of it kept in lanes
+    const uint32_t r = row == kNoRow ? 0u : (uint32_t)row;
+    return cache + (int64_t)(r / kPage) * Page::kBytes + ((r % kPage) * bytes + at);
   }
 
-  static __device__ __forceinline__ void position(int i, const uint8_t* cache, MXIDX_LDS uint8_t* tile, int first,
-                                                  int rows, int ln) {
-    const int t0 = first + i * kPosPer, t = t0 + ln / PC;
+  // 16 bytes a lane to LDS, at dst + 16 * lane.
+  static __device__ __forceinline__ void copy(const Source& src, int row, uint32_t bytes, uint32_t at,
+                                              MXIDX_LDS uint8_t* dst) {
+    if constexpr (kSmall)
+      copy16(buffer_rsrc(src.base, (int)src.bytes), dst, offset(row, bytes, at));
+    else
+      __builtin_amdgcn_global_load_lds((MXIDX_GLOBAL void*)address((Bytes)src.base, row, bytes, at),
+                                       (MXIDX_LDS void*)dst, 16, 0, 0);
+  }
+
+  __device__ __forceinline__ void load(const Source& src, MXIDX_LDS uint8_t* raw, int first, int rows, uint32_t ln) {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int row = __builtin_amdgcn_ds_bpermute(4 * (first + token(i, ln)), rows);
+      const uint32_t at = Page::kScaleBase + ln % LB;
+      if constexpr (kSmall) {
+        scale[i] = __builtin_amdgcn_raw_buffer_load_b8(buffer_rsrc(src.base, (int)src.bytes),
+                                                       (int)offset(row, Page::kScales, at), 0, 0);
+      } else {
+        const uint32_t s = *address((Bytes)src.base, row, Page::kScales, at);
+        scale[i] = row == kNoRow ? 127u : s;
+      }
+      copy(src, row, Page::kCodes, 16 * (ln % LB), raw + i * (kWave * 16));
+    }
+  }
+
+  static __device__ __forceinline__ void position(int i, const Source& src, MXIDX_LDS uint8_t* tile, int first,
+                                                  int rows, uint32_t ln) {
+    const int t0 = first + i * kPosPer, t = t0 + (int)(ln / PC);
     const int row = __builtin_amdgcn_ds_bpermute(4 * t, rows);
-    const uint8_t* src = row_of(cache, row, Page::kPosBase, Page::kPos) + (((ln % PC) ^ swz<PC>(t)) << 4);
-    __builtin_amdgcn_global_load_lds((MXIDX_GLOBAL void*)src,
-                                     (MXIDX_LDS void*)(tile + kTile * kLatent * 2 + t0 * PC * 16), 16, 0, 0);
+    copy(src, row, Page::kPos, Page::kPosBase + (((ln % PC) ^ (uint32_t)swz<PC>(t)) << 4),
+         tile + kTile * kLatent * 2 + t0 * PC * 16);
   }
 
-  __device__ __forceinline__ void unit(int u, MXIDX_LDS uint8_t* tile, int first, int ln) {
-    const int i = u / 4, j = u % 4, t = first + token(i, ln);
-    const uint32_t w = j == 0 ? codes[i].x : j == 1 ? codes[i].y : j == 2 ? codes[i].z : codes[i].w;
-    const uint4 x = mx_decode8(w, mx_scale(ok[i] ? scale[i] : 127u));
-    *(MXIDX_LDS v8s*)(tile + t * (kLatent * 2) + (((4 * (ln % LB) + j) ^ swz<LC>(t)) << 4)) = __builtin_bit_cast(v8s, x);
+  __device__ __forceinline__ void take(int i, MXIDX_LDS const uint8_t* raw, uint32_t ln) {
+    codes = *(MXIDX_LDS const v4i*)(raw + i * (kWave * 16) + 16 * ln);
+  }
+
+  // Load i's codes to the tile: chunks 4c .. 4c+3 of the token's row, those of every second run of four
+  // blocks in another order, so that eight lanes' 16 bytes fall on different banks.
+  __device__ __forceinline__ void write(int i, MXIDX_LDS uint8_t* tile, int first, uint32_t ln) const {
+    const uint32_t c = ln % LB, turn = (c >> 2) & 1;
+    const int t = first + token(i, ln);
+    const uint32_t at = (uint32_t)t * (kLatent * 2) + (((4 * c + turn) ^ (uint32_t)swz<LC>(t)) << 4);
+    const float s = mx_scale(scale[i]);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint4 x = mx_decode8((uint32_t)(turn ? codes[j ^ 1] : codes[j]), s);
+      *(MXIDX_LDS v8s*)(tile + (at ^ (uint32_t)(j << 4))) = __builtin_bit_cast(v8s, x);
+    }
   }
 };
 
@@ -290,18 +334,23 @@ __global__ __launch_bounds__(HG * TH * kWave, kTile == 32 ? 2 : 1) void attn_ker
   constexpr int KS = kRow / 32, KL = kLatent / 32;     // contraction steps, latent ones
   constexpr int NV = kLatent / 16;                     // 16-value parts of the output
   constexpr int LC = kLatent / 8;                      // 16-byte chunks of a latent row
-  constexpr int kAhead = kSmall ? 3 : 2;        // operand steps in flight from LDS, as registers allow
+  constexpr int kAhead = kSmall && !(kMx && HG > 2) ? 3 : 2;        // operand steps in flight from LDS, as registers allow
   constexpr int kValuesAhead = HG <= 2 ? 4 : kAhead;
   constexpr int kMine = kTile / kWaves;                // rows that a wave copies
   constexpr int kLatentBytes = kTile * kLatent * 2, kTileBytes = kTile * kRow * 2;
   using Copy = TileCopy<kLatent, kTile, kMine, kSmall>;
-  using Mx = MxCopy<kLatent, kTile, kMine>;
+  using Mx = MxCopy<kLatent, kTile, kMine, kSmall>;
   // Two arrays, and the loop below unrolled over them: the compiler then sees that a
   // tile's reads do not touch the one being copied, and does not wait for its copies.
   __shared__ __attribute__((aligned(1024))) uint8_t tile0[kTileBytes];
   __shared__ __attribute__((aligned(1024))) uint8_t tile1[kTileBytes];
   static_assert(kTile <= kWave && 2 * kTileBytes <= 156 * 1024, "a lane for each token; two tiles fit the LDS");
-  __shared__ float2 stats[TH][kHeads];                 // the waves' (m, l)
+  // kMx: the codes of a tile.  With latent 512 the three arrays are the whole LDS of a CU, or of half of one
+  // with 32-token tiles, so that the waves' statistics take the codes' place in the end.
+  constexpr int kStatBytes = TH * kHeads * (int)sizeof(float2);
+  __shared__ __attribute__((aligned(1024))) uint8_t last[kMx ? kWaves * Mx::kRawBytes : kStatBytes];
+  static_assert(sizeof(last) >= kStatBytes, "the statistics' place");
+  float2(*stats)[kHeads] = reinterpret_cast<float2(*)[kHeads]>(last);   // the waves' (m, l)
 
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int hg = wave % HG, th = wave / HG;
@@ -334,11 +383,13 @@ __global__ __launch_bounds__(HG * TH * kWave, kTile == 32 ? 2 : 1) void attn_ker
   auto rows_of = [&](int p, int page, uint64_t& mask) __attribute__((always_inline)) {
     const bool ok = p >= 0 && page >= 0 && page < parts.pages;
     mask = __ballot(ok);
+    if constexpr (kMx) return Mx::row_code(ok, (uint32_t)page, (uint32_t)p & (kPage - 1));
     const uint32_t row = (uint32_t)page * kPage + ((uint32_t)p & (kPage - 1));
     return ok ? (int)(kSmall ? row * (kRow * 2) : row) : kNoRow;
   };
   const Source cache{static_cast<const char*>(a.cache), parts.cache_bytes, kRow * 2};
-  const uint8_t* mx_cache = static_cast<const uint8_t*>(a.cache);
+  MXIDX_LDS uint8_t* raw = (MXIDX_LDS uint8_t*)last + wave * Mx::kRawBytes;
+  Mx mx;                                               // kMx: the scales of the codes there
 
   // The wave's kTokens tokens of a tile against its heads; the pieces of the next tile's
   // copy go between the steps of the first product.
@@ -346,7 +397,12 @@ __global__ __launch_bounds__(HG * TH * kWave, kTile == 32 ? 2 : 1) void attn_ker
                      int rows) __attribute__((always_inline)) {
     const int base = th * kTokens;
     v4f s[NT];
-    Mx raw;                                            // kMx: the next tile's codes
+    if constexpr (kMx) {
+      const int ln = fresh_lane();
+#pragma unroll
+      for (int i = 0; i < Mx::kPosPieces; ++i) Mx::position(i, cache, nxt, wave * kMine, rows, ln);
+      __builtin_amdgcn_sched_barrier(0);
+    }
     {
       // LDS offsets of the operands in the tile: the places of the chunks differ
       // between steps by constants xored into few bits (swz), so one register for each
@@ -375,11 +431,7 @@ __global__ __launch_bounds__(HG * TH * kWave, kTile == 32 ? 2 : 1) void attn_ker
 #pragma unroll
         for (int t = 0; t < NT; ++t) s[t] = mfma_bf16(x[k % kAhead][t], q[k], s[t]);
         if (k + kAhead < KS) keys(k + kAhead, x[k % kAhead]);
-        if constexpr (kMx) {
-          if (k < Mx::kLoads) raw.load(k, mx_cache, wave * kMine, rows, ln);
-          if (k >= Mx::kLoads && k < Mx::kLoads + Mx::kPosPieces)
-            Mx::position(k - Mx::kLoads, mx_cache, nxt, wave * kMine, rows, ln);
-        } else {
+        if constexpr (!kMx) {
 #pragma unroll
           for (int i = 0; i < Copy::kPieces; ++i)
             if (i * KS / Copy::kPieces == k)
@@ -468,12 +520,14 @@ __global__ __launch_bounds__(HG * TH * kWave, kTile == 32 ? 2 : 1) void attn_ker
       for (int i = 0; i < kStep; ++i)
         if (v + i + kValuesAhead < NV) values(v + i + kValuesAhead, y[(v + i) % kValuesAhead]);
       if constexpr (kMx) {
-        // in the product's second half, when the codes have come
-        constexpr int kFrom = NV / 2 / kStep * kStep, kSlots = (NV - kFrom) / kStep;
-        const int ln = fresh_lane();
+        // the next tile's codes on their way, in the product's second half
+        constexpr int kShare = NV / 2 / Mx::kLoads, kHalf = kShare / 2;
+        static_assert(kHalf % kStep == 0 && kHalf > 0, "a step of its own for each");
 #pragma unroll
-        for (int u = 0; u < Mx::kUnits; ++u)
-          if (kFrom + u * kSlots / Mx::kUnits * kStep == v) raw.unit(u, nxt, wave * kMine, ln);
+        for (int i = 0; i < Mx::kLoads; ++i) {
+          if (v == NV / 2 + i * kShare) mx.take(i, raw, fresh_lane());
+          if (v == NV / 2 + i * kShare + kHalf) mx.write(i, nxt, wave * kMine, fresh_lane());
+        }
       }
     }
     __builtin_amdgcn_sched_barrier(0);
@@ -515,14 +569,16 @@ __global__ __launch_bounds__(HG * TH * kWave, kTile == 32 ? 2 : 1) void attn_ker
     auto copy_first = [&]() __attribute__((always_inline)) {
       if constexpr (kMx) {
         const int ln = fresh_lane();
-        Mx raw;
-#pragma unroll
-        for (int i = 0; i < Mx::kLoads; ++i) raw.load(i, mx_cache, wave * kMine, first_rows, ln);
+        mx.load(cache, raw, wave * kMine, first_rows, ln);
 #pragma unroll
         for (int i = 0; i < Mx::kPosPieces; ++i)
-          Mx::position(i, mx_cache, (MXIDX_LDS uint8_t*)tile0, wave * kMine, first_rows, ln);
+          Mx::position(i, cache, (MXIDX_LDS uint8_t*)tile0, wave * kMine, first_rows, ln);
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 #pragma unroll
-        for (int u = 0; u < Mx::kUnits; ++u) raw.unit(u, (MXIDX_LDS uint8_t*)tile0, wave * kMine, ln);
+        for (int i = 0; i < Mx::kLoads; ++i) {
+          mx.take(i, raw, ln);
+          mx.write(i, (MXIDX_LDS uint8_t*)tile0, wave * kMine, ln);
+        }
       } else {
         copy_all(cache, (MXIDX_LDS uint8_t*)tile0, first_rows);
       }
@@ -545,18 +601,42 @@ __global__ __launch_bounds__(HG * TH * kWave, kTile == 32 ? 2 : 1) void attn_ker
       __syncthreads();
       copy_first();
     }
+    // kMx: the codes of the tile behind the next one computed, on their way while that is
+    int rows = kNoRow;
+    uint64_t next_mask = 0;
+    auto load_codes = [&](int t) __attribute__((always_inline)) {
+      rows = rows_of(t < t1 ? next : -1, page, next_mask);
+      // in this place: the count of the step's wait relies on it
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_sched_barrier(0);
+      if (t < t1) mx.load(cache, raw, wave * kMine, rows, fresh_lane());
+      __builtin_amdgcn_sched_barrier(0);
+      asm volatile("" ::: "memory");
+    };
+    if constexpr (kMx) load_codes(t0 + 1);
     // tile t from `cur`, tile t + 1 on its way to `nxt` (behind the last one: zeros)
     auto step = [&](int t, MXIDX_LDS uint8_t* cur, MXIDX_LDS uint8_t* nxt) __attribute__((always_inline)) {
-      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-      __syncthreads();
-      uint64_t next_mask;
-      const int rows = rows_of(t + 1 < t1 ? next : -1, page, next_mask);
+      if constexpr (kMx) {
+        // but for the next tile's codes and scales, whose loads are the youngest (a barrier of the
+        // language would wait for them too)
+        if (t + 1 < t1)
+          asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(2 * Mx::kLoads) : "memory");
+        else
+          asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+      } else {
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __syncthreads();
+      }
+      if constexpr (!kMx) rows = rows_of(t + 1 < t1 ? next : -1, page, next_mask);
       next = token_of(a, row, far, place(t + 2));
       page = token_page(a, row, next);
       far = entry(t + 3);
       seen |= mask != 0;
       compute(cur, mask, nxt, rows);
       mask = next_mask;
+      if constexpr (kMx) load_codes(t + 2);
     };
     for (int t = t0; t < t1; t += 2) {
       step(t, (MXIDX_LDS uint8_t*)tile0, (MXIDX_LDS uint8_t*)tile1);
@@ -569,6 +649,7 @@ __global__ __launch_bounds__(HG * TH * kWave, kTile == 32 ? 2 : 1) void attn_ker
   const int ln = threadIdx.x & (kWave - 1), n = ln & 15, g = ln >> 4;
   l += __shfl_xor(l, 16);
   l += __shfl_xor(l, 32);
+  if constexpr (kMx) __syncthreads();                  // the codes before have been read
   if (g == 0) stats[th][hg * 16 + n] = make_float2(m, l);
   __syncthreads();                                     // and the last tile's reads are done
   float f = 1.f;
@@ -761,7 +842,7 @@ int64_t part_bytes(int64_t parts, int latent) { return ml_bytes(parts) + parts *
 template <int kLatent, bool kMx>
 hipError_t launch(const AttnArgs& a, void* workspace, hipStream_t stream) {
   const Plan p = plan_of(a.rows, a.H, kLatent, a.indices ? a.k : a.max_tokens);
-  const int64_t cache_bytes = a.num_pages * kPage * (kLatent + kRopeWidth) * 2;
+  const int64_t cache_bytes = a.num_pages * (kMx ? mx_page_bytes(kLatent) : kPage * (kLatent + kRopeWidth) * 2);
   const int64_t q_bytes = ((a.H - 1) * a.q_head_stride + kLatent + kRopeWidth) * 2;
   const bool small = cache_bytes <= kReach && q_bytes <= kReach;
   Parts parts{nullptr, nullptr, p.splits, p.heads, (int)a.num_pages,
@@ -773,8 +854,8 @@ hipError_t launch(const AttnArgs& a, void* workspace, hipStream_t stream) {
   const dim3 grid((uint32_t)(a.rows * (p.heads / p.group_heads) * p.splits));
 #define MXIDX_ATTN(heads_, tile_, hg, th)                                                     \
   case heads_ * 64 + tile_:                                                                   \
-    if (small && !kMx)                                                                       \
-      hipLaunchKernelGGL((attn_kernel<kLatent, tile_, hg, th, !kMx, kMx>), grid,             \
+    if (small)                                                                               \
+      hipLaunchKernelGGL((attn_kernel<kLatent, tile_, hg, th, true, kMx>), grid,             \
                          dim3(hg * th * kWave), 0, stream, a, parts);                        \
     else                                                                                     \
       hipLaunchKernelGGL((attn_kernel<kLatent, tile_, hg, th, false, kMx>), grid,            \

@@ -22,11 +22,9 @@ struct MxPage {
 
 constexpr int mx_page_bytes(int latent) { return kPage * (latent / 2 + latent / kBlock + kLatentRope * 2); }
 
-// 2^(s - 127) of a scale byte s, as the conversions take it (they read the exponent alone; 0 stands
-// for 2^-127).
-__device__ __forceinline__ float mx_scale(uint32_t s) {
-  return __uint_as_float(s == 0 ? 0x00400000u : s << 23);
-}
+// 2^(s - 127) of a scale byte s, as the conversions take it: they read the exponent's bits alone, 0
+// among them as 2^-127.
+__device__ __forceinline__ float mx_scale(uint32_t s) { return __uint_as_float(s << 23); }
 
 // 8 codes (a dword) to 8 bf16 values, exact: two significant bits times a power of two from
 // 2^-127 on, whose smallest half-steps are subnormal and still a bf16.
