@@ -27,6 +27,11 @@ namespace {
 
 constexpr int kTile = 64;                   // tokens at a time
 constexpr int kWaveSlots = 32;
+#ifndef AHEAD
+#define AHEAD 3
+#define VAHEAD 4
+#endif
+constexpr int kAhead = AHEAD, kValuesAhead = VAHEAD;
 
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
@@ -236,15 +241,28 @@ __global__ __launch_bounds__(kWaves * kWave, kWaves == 1 ? 1 : 2) void prompt_ke
     for (int p = 0; p < 2; ++p)
 #pragma unroll
       for (int j = 0; j < 16; ++j) s[p][j] = 0.f;
-#pragma unroll
-    for (int k = 0; k < KS; ++k)
+    // kAhead steps' operands are on their way while one is used
+    auto keys = [&](int k, v8s (&x)[2]) __attribute__((always_inline)) {
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
         const int tok = 32 * p + n;
-        const int at = k < KA ? tok * 256 + (((2 * k + half) ^ key_swz<16>(tok)) << 4)
-                              : kKeyA + tok * 128 + (((2 * (k - KA) + half) ^ key_swz<8>(tok)) << 4);
-        s[p] = mfma32(*(MXIDX_LDS const v8s*)(tile + at), q[k], s[p]);
+        x[p] = *(MXIDX_LDS const v8s*)(tile + (k < KA ? tok * 256 + (((2 * k + half) ^ key_swz<16>(tok)) << 4)
+                                                      : kKeyA + tok * 128 + (((2 * (k - KA) + half) ^ key_swz<8>(tok)) << 4)));
       }
+    };
+    {
+      v8s x[kAhead][2];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) keys(k, x[k]);
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int p = 0; p < 2; ++p) s[p] = mfma32(x[k % kAhead][p], q[k], s[p]);
+        if (k + kAhead < KS) keys(k + kAhead, x[k % kAhead]);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
     // s[p][j]: token first + 32p + 8 (j / 4) + 4 half + j % 4
     if (first + kTile > wave_lo) {
 #pragma unroll
@@ -278,22 +296,30 @@ __global__ __launch_bounds__(kWaves * kWave, kWaves == 1 ? 1 : 2) void prompt_ke
         l += x + y;
         w[2 * p + j / 8][(j % 8) / 2] = pack2(x, y);
       }
+    // lane 4j + c of a 16-lane group reads token 4 half + j, values 4c..4c+3 of its 16
+    auto values = [&](int i, v4s (&x)[2]) __attribute__((always_inline)) {
+      const int u = i / NV, v = i % NV;
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
-#pragma unroll
-      for (int v = 0; v < NV; ++v) {
-        // lane 4j + c of a 16-lane group reads token 4 half + j, values 4c..4c+3 of its 16
-        v4s x[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int tok = 16 * u + 8 * e + 4 * half + ((ln & 15) >> 2);
-          const int chunk = 4 * v + 2 * ((ln >> 4) & 1) + ((ln & 3) >> 1);
-          x[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((MXIDX_LDS v4s*)(
-              tile + kKeyA + kKeyB + tok * (kDv * 2) + ((chunk ^ value_swz<VC>(tok)) << 4) + 8 * (ln & 1)));
-        }
-        o[v] = mfma32(__builtin_shufflevector(x[0], x[1], 0, 1, 2, 3, 4, 5, 6, 7),
-                      __builtin_bit_cast(v8s, uint4{w[u][0], w[u][1], w[u][2], w[u][3]}), o[v]);
+      for (int e = 0; e < 2; ++e) {
+        const int tok = 16 * u + 8 * e + 4 * half + ((ln & 15) >> 2);
+        const int chunk = 4 * v + 2 * ((ln >> 4) & 1) + ((ln & 3) >> 1);
+        x[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((MXIDX_LDS v4s*)(
+            tile + kKeyA + kKeyB + tok * (kDv * 2) + ((chunk ^ value_swz<VC>(tok)) << 4) + 8 * (ln & 1)));
       }
+    };
+    v4s y[kValuesAhead][2];
+#pragma unroll
+    for (int i = 0; i < kValuesAhead; ++i) values(i, y[i]);
+#pragma unroll
+    for (int i = 0; i < 4 * NV; ++i) {
+      __builtin_amdgcn_sched_barrier(0);
+      const int u = i / NV, v = i % NV;
+      const v4s(&x)[2] = y[i % kValuesAhead];
+      o[v] = mfma32(__builtin_shufflevector(x[0], x[1], 0, 1, 2, 3, 4, 5, 6, 7),
+                    __builtin_bit_cast(v8s, uint4{w[u][0], w[u][1], w[u][2], w[u][3]}), o[v]);
+      if (i + kValuesAhead < 4 * NV) values(i + kValuesAhead, y[i % kValuesAhead]);
+    }
+    __builtin_amdgcn_sched_barrier(0);
   };
 
   if (t0 < t1) copy(t0, (MXIDX_LDS uint8_t*)tile0);
