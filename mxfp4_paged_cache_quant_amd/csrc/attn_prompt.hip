@@ -27,11 +27,8 @@ namespace {
 
 constexpr int kTile = 64;                   // tokens at a time
 constexpr int kWaveSlots = 32;
-#ifndef AHEAD
-#define AHEAD 3
-#define VAHEAD 4
-#endif
-constexpr int kAhead = AHEAD, kValuesAhead = VAHEAD;
+constexpr int kAhead = 3, kValuesAhead = 4;   // operand steps of the products on their way
+constexpr int kMinShare = 4;                // tiles that a share of a split row walks at least
 
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
@@ -79,32 +76,77 @@ __device__ __forceinline__ uint32_t wave_scan(uint32_t x) {
   return x;
 }
 
-// A request's tile of query rows, and where its rows, keys and values begin.
+// How the rows are dealt out.  Slots are blocks of `heads` heads by `tok` rows (a tile); without shares each
+// tile of a head block is one item, of a workgroup.  With them a head block has `items`, more than it
+// has tiles, and the requests' tiles are cut into shares of about equal length, whatever the requests'
+// lengths: each leaves for each of its slots unscaled sums and (m, l), which a second launch joins.
+struct PromptParts {
+  float* o;                // [head block, item, slot, kDv]
+  float* ml;
+  int tok, heads, blocks;  // rows of a tile; heads of a block, blocks of a key head's
+  uint32_t tiles, items;   // of a head block: tiles at most, items
+  bool shares;
+};
+
+// A request's tile of query rows, where its rows, keys and values begin, and its share or shares.
 struct Found {
   int64_t row, key;        // the first query row and the first key of the request
   int n, len, pos0;        // its rows and its keys that there are, the position of its first row
   int tile;                // -1: no such tile
+  int share, shares;
+  uint32_t item;           // the tile's first
 };
 
-// Tile `want` of all requests' tiles of `tok` rows, a request's last rows, which see most, first.  Every
+// Item (kByItem) or tile `want` of all requests', a request's last rows, which see most, first.  Every
 // wave looks for itself, 64 requests at a time.
-__device__ Found find_tile(const PromptArgs& a, int tok, uint32_t want) {
+template <bool kByItem>
+__device__ Found find(const PromptArgs& a, const PromptParts& parts, uint32_t want) {
   const int ln = threadIdx.x & (kWave - 1);
-  const uint32_t T = (uint32_t)a.T;                    // below 2^23: sums of 64 fit 32 bits
-  uint32_t row0 = 0, tile0 = 0;
+  const uint32_t T = (uint32_t)a.T, tok = (uint32_t)parts.tok;   // T below 2^23: sums of 64 fit 32 bits
+  uint32_t row0 = 0, tile0 = 0, item0 = 0;
   int64_t key0 = 0;
+  int n, len;
+  uint32_t row, row_end, there, tiles;
+  auto load = [&](int b0) {
+    const int b = b0 + ln;
+    n = b < a.B ? max(a.query_lens[b], 0) : 0;
+    len = b < a.B ? max(a.seq_lens[b], 0) : 0;
+    const uint32_t mine = min((uint32_t)n, T);
+    row_end = wave_scan(mine) + row0;
+    row = row_end - mine;
+    there = row < T ? min(mine, T - row) : 0;
+    tiles = (there + tok - 1) / tok;
+  };
+  auto key_tiles = [&]() { return (uint32_t)((min((int64_t)len, a.max_seq_len) + kTile - 1) / kTile); };
+  auto last_of = [](uint32_t x) { return (uint32_t)__builtin_amdgcn_readlane((int)x, kWave - 1); };
+  uint32_t length = ~0u;                               // of a share
+  if (parts.shares) {
+    // sum(tiles * ceil(key tiles / length)) <= sum(tiles * key tiles) / length + sum(tiles) <= items; the sums
+    // are whole numbers below 2^53
+    double work = 0.0;
+    uint32_t all = 0;
+    for (int b0 = 0; b0 < a.B; b0 += kWave) {
+      load(b0);
+      work += (double)tiles * (double)key_tiles();
+      all += last_of(wave_scan(tiles));
+      row0 = min(last_of(row_end), T);
+    }
+#pragma unroll
+    for (int d = 1; d < kWave; d <<= 1) work += __shfl_xor(work, d);
+    const double room = (double)(parts.items - all);
+    length = max((uint32_t)kMinShare, (uint32_t)((work + room - 1.0) / room));
+    row0 = 0;
+  }
   Found f;
   f.tile = -1;
   for (int b0 = 0; b0 < a.B; b0 += kWave) {
-    const int b = b0 + ln;
-    const int n = b < a.B ? max(a.query_lens[b], 0) : 0, len = b < a.B ? max(a.seq_lens[b], 0) : 0;
-    const uint32_t mine = min((uint32_t)n, T), row_end = wave_scan(mine) + row0, row = row_end - mine;
-    const uint32_t there = row < T ? min(mine, T - row) : 0;
-    const uint32_t tiles = (there + (uint32_t)tok - 1) / (uint32_t)tok, tile_end = wave_scan(tiles) + tile0;
+    load(b0);
+    const uint32_t shares = parts.shares ? max((key_tiles() + length - 1) / length, 1u) : 1u, items = tiles * shares;
+    const uint32_t tile_end = wave_scan(tiles) + tile0, item_end = wave_scan(items) + item0;
     // the keys' sum in two halves of 16 bits: 64 of each fit
     const uint32_t low = wave_scan((uint32_t)len & 0xffffu), high = wave_scan((uint32_t)len >> 16);
-    const int64_t key_end = key0 + ((int64_t)high << 16) + low;
-    const uint64_t hit = __ballot(want < tile_end && want >= tile_end - tiles);
+    const uint32_t end = kByItem ? item_end : tile_end, mine = kByItem ? items : tiles;
+    const uint64_t hit = __ballot(want < end && want >= end - mine);
     if (hit) {
       const int from = __builtin_ctzll(hit);
       auto of = [&](uint32_t x) { return (uint32_t)__builtin_amdgcn_readlane((int)x, from); };
@@ -112,26 +154,23 @@ __device__ Found find_tile(const PromptArgs& a, int tok, uint32_t want) {
       f.len = (int)of((uint32_t)len);
       f.n = (int)of(there);
       f.pos0 = f.len - (int)of((uint32_t)n);
-      const int64_t key = key_end - len;
+      const int64_t key = key0 + ((int64_t)high << 16) + low - len;
       f.key = (int64_t)((uint64_t)of((uint32_t)((uint64_t)key >> 32)) << 32 | of((uint32_t)key));
-      f.tile = (int)(of(tile_end) - 1 - want);
-      f.len = (int)min((int64_t)min((int64_t)f.len, a.max_seq_len), max(a.S - f.key, (int64_t)0));
+      f.len = (int)min(min((int64_t)f.len, a.max_seq_len), max(a.S - f.key, (int64_t)0));
+      f.shares = (int)of(shares);
+      const uint32_t in = want - of(end - mine), turn = kByItem ? in / (uint32_t)f.shares : in;   // tiles from the last
+      f.share = kByItem ? (int)(in - turn * (uint32_t)f.shares) : 0;
+      f.item = of(item_end - items) + turn * (uint32_t)f.shares;
+      f.tile = (int)(of(tiles) - 1 - turn);
       return f;
     }
-    row0 = min((uint32_t)__builtin_amdgcn_readlane((int)row_end, kWave - 1), T);
-    tile0 = (uint32_t)__builtin_amdgcn_readlane((int)tile_end, kWave - 1);
-    key0 += ((int64_t)__builtin_amdgcn_readlane((int)high, kWave - 1) << 16) + (uint32_t)__builtin_amdgcn_readlane((int)low, kWave - 1);
+    row0 = min(last_of(row_end), T);
+    tile0 = last_of(tile_end);
+    item0 = last_of(item_end);
+    key0 += ((int64_t)last_of(high) << 16) + last_of(low);
   }
   return f;
 }
-
-// Of the split form: for each (row, head, split) the unscaled sums, and (m, l).
-struct PromptParts {
-  float* o;
-  float* ml;
-  int splits, tok, heads, blocks;           // rows of a tile; heads of a block, blocks of a key head's
-  int64_t tiles;                            // at most, of all requests
-};
 
 // C chunks of each of 64 rows to LDS, kWaves waves sharing them: piece i of kPieces of a wave.
 template <int C, int kWaves>
@@ -159,14 +198,12 @@ __global__ __launch_bounds__(kWaves * kWave, kWaves == 1 ? 1 : 2) void prompt_ke
   __shared__ __attribute__((aligned(1024))) uint8_t tile0[kBytes];
   __shared__ __attribute__((aligned(1024))) uint8_t tile1[kBytes];
 
-  // each XCD takes a run of neighbouring numbers: the splits and tiles of one head, which read the
+  // each XCD takes a run of neighbouring numbers: the shares and tiles of one head, which read the
   // same keys and values
   const uint32_t xcd = blockIdx.x % 8, number = xcd * (gridDim.x / 8) + min(xcd, gridDim.x % 8) + blockIdx.x / 8;
-  const uint32_t unit = number / (uint32_t)parts.splits;
-  const int split = (int)(number - unit * (uint32_t)parts.splits);
-  const uint32_t hb = unit / (uint32_t)parts.tiles;
+  const uint32_t hb = number / parts.items;
   const int kv_head = (int)(hb / (uint32_t)parts.blocks), block = (int)(hb - kv_head * (uint32_t)parts.blocks);
-  const Found f = find_tile(a, parts.tok, unit - hb * (uint32_t)parts.tiles);
+  const Found f = find<true>(a, parts, number - hb * parts.items);
   if (f.tile < 0) return;
 
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), ln = threadIdx.x & (kWave - 1);
@@ -185,8 +222,8 @@ __global__ __launch_bounds__(kWaves * kWave, kWaves == 1 ? 1 : 2) void prompt_ke
   const int wave_lo = __builtin_amdgcn_readfirstlane(limit(min(i0 + wave * kWaveSlots / parts.heads, last)));
   const int wave_hi = __builtin_amdgcn_readfirstlane(limit(min(i0 + (wave * kWaveSlots + kWaveSlots - 1) / parts.heads, last)));
   const int end = __builtin_amdgcn_readfirstlane(limit(last));
-  const int tiles = (end + kTile - 1) / kTile, share = tiles / parts.splits, more = tiles - share * parts.splits;
-  const int t0 = split * share + min(split, more), t1 = t0 + share + (split < more ? 1 : 0);
+  const int tiles = (end + kTile - 1) / kTile, each = tiles / f.shares, more = tiles - each * f.shares;
+  const int t0 = f.share * each + min(f.share, more), t1 = t0 + each + (f.share < more ? 1 : 0);
 
   v8s q[KS];                                           // step s: values 16s + 8 half .. +7
   {
@@ -336,10 +373,9 @@ __global__ __launch_bounds__(kWaves * kWave, kWaves == 1 ? 1 : 2) void prompt_ke
 
   l = sum_halves(l);
   if (!live) return;
-  const int64_t at = row * a.Hq + head;
-  if (parts.splits == 1) {
+  if (f.shares == 1) {
     const float inv = l == 0.f ? 0.f : 1.f / l;
-    if (a.lse && half == 0) a.lse[at] = l == 0.f ? neg_inf() : m * 0.6931471805599453f + logf(l);
+    if (a.lse && half == 0) a.lse[row * a.Hq + head] = l == 0.f ? neg_inf() : m * 0.6931471805599453f + logf(l);
     uint16_t* dst = static_cast<uint16_t*>(a.out) + row * a.out_row_stride + head * a.out_head_stride + 4 * half;
 #pragma unroll
     for (int v = 0; v < NV; ++v)
@@ -348,7 +384,7 @@ __global__ __launch_bounds__(kWaves * kWave, kWaves == 1 ? 1 : 2) void prompt_ke
         *reinterpret_cast<uint2*>(dst + 32 * v + 2 * j) =
             make_uint2(pack2(o[v][j] * inv, o[v][j + 1] * inv), pack2(o[v][j + 2] * inv, o[v][j + 3] * inv));
   } else {
-    const int64_t part = at * parts.splits + split;
+    const int64_t part = ((int64_t)hb * parts.items + f.item + f.share) * (kWaves * kWaveSlots) + slot;
     if (half == 0) *reinterpret_cast<float2*>(parts.ml + 2 * part) = make_float2(m, l);
     if (l == 0.f) return;                              // the join does not read its sums
     float* dst = parts.o + part * kDv + 4 * half;
@@ -360,49 +396,70 @@ __global__ __launch_bounds__(kWaves * kWave, kWaves == 1 ? 1 : 2) void prompt_ke
   }
 }
 
-// The splits' sums of one (row, head), kDv / 4 lanes of 4 values each.
-template <int kDv>
+// The shares' sums of a tile's slots: kDv / 4 lanes of 4 values take every kGroups-th share, kBatch loads
+// together (past the last one, its sums again), and with more groups than one LDS joins those, in
+// groups of one slot.
+template <int kDv, int kSlots, int kGroups>
 __global__ __launch_bounds__(256) void prompt_join_kernel(PromptArgs a, PromptParts parts) {
-  constexpr int W = kDv / 4;
-  __shared__ int64_t wave_rows[4];
-  // the rows that there are: those behind the last request's stay as they were
-  int64_t rows = 0;
-  for (int b = threadIdx.x; b < a.B; b += 256) rows += max(a.query_lens[b], 0);
-#pragma unroll
-  for (int d = 1; d < kWave; d <<= 1) rows += __shfl_xor(rows, d);
-  if (threadIdx.x % kWave == 0) wave_rows[threadIdx.x / kWave] = rows;
-  __syncthreads();
-  rows = min(wave_rows[0] + wave_rows[1] + wave_rows[2] + wave_rows[3], a.T);
-  const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) / W;
-  const int i = threadIdx.x % W;
-  const int64_t row = at / a.Hq;
-  const int head = (int)(at - row * a.Hq);
-  if (row >= rows) return;
-  const int64_t first = at * parts.splits;
-  float m = neg_inf();
-  for (int s = 0; s < parts.splits; ++s) m = fmaxf(m, parts.ml[2 * (first + s)]);
-  const float ref = m == neg_inf() ? 0.f : m;
+  constexpr int W = kDv / 4, kAt = 256 / W / kGroups, kBatch = 4;     // slots of a workgroup
+  __shared__ v4f sums[kGroups][kAt][W];
+  __shared__ float2 stats[kGroups][kAt];
+  const uint32_t per = kSlots / kAt, unit = blockIdx.x / per, hb = unit / parts.tiles;
+  const Found f = find<false>(a, parts, unit - hb * parts.tiles);
+  if (f.tile < 0 || f.shares == 1) return;
+  const int i = threadIdx.x % W, which = threadIdx.x / W, group = which % kGroups, at = which / kGroups;
+  const int slot = (int)(blockIdx.x - unit * per) * kAt + at;
+  const int row_in = slot / parts.heads, head_in = slot - row_in * parts.heads;
+  const int kv_head = (int)(hb / (uint32_t)parts.blocks), block = (int)(hb - kv_head * (uint32_t)parts.blocks);
+  const int G = a.Hq / a.Hk, h0 = block * parts.heads, i0 = f.tile * parts.tok;
+  const bool live = row_in < parts.tok && i0 + row_in < f.n && head_in < min(parts.heads, G - h0);
+  const int64_t first = ((int64_t)hb * parts.items + f.item) * kSlots + slot;
   v4f o = {0.f, 0.f, 0.f, 0.f};
-  float l = 0.f;
-  for (int s = 0; s < parts.splits; ++s) {
-    const float2 ml = *reinterpret_cast<const float2*>(parts.ml + 2 * (first + s));
-    if (ml.y == 0.f) continue;                         // nothing seen: no sums written
-    const float f = __builtin_amdgcn_exp2f(ml.x - ref);
-    l += f * ml.y;
-    o += f * *reinterpret_cast<const v4f*>(parts.o + (first + s) * kDv + 4 * i);
+  float m = neg_inf(), l = 0.f;
+  auto add = [&](float m2, float l2, const v4f& x) __attribute__((always_inline)) {
+    if (l2 == 0.f) return;                             // nothing seen: no sums written
+    const float top = fmaxf(m, m2), old = __builtin_amdgcn_exp2f(m - top), f2 = __builtin_amdgcn_exp2f(m2 - top);
+    o = o * old + x * f2;
+    l = l * old + l2 * f2;
+    m = top;
+  };
+  if (live) {
+    for (int s0 = group; s0 < f.shares; s0 += kBatch * kGroups) {
+      float2 ml[kBatch];
+      v4f x[kBatch];
+#pragma unroll
+      for (int s = 0; s < kBatch; ++s) {
+        const int64_t p = first + (int64_t)min(s0 + s * kGroups, f.shares - 1) * kSlots;
+        ml[s] = *reinterpret_cast<const float2*>(parts.ml + 2 * p);
+        x[s] = *reinterpret_cast<const v4f*>(parts.o + p * kDv + 4 * i);
+      }
+#pragma unroll
+      for (int s = 0; s < kBatch; ++s)
+        if (s0 + s * kGroups < f.shares) add(ml[s].x, ml[s].y, x[s]);
+    }
   }
+  if constexpr (kGroups > 1) {
+    sums[group][at][i] = o;
+    if (i == 0) stats[group][at] = make_float2(m, l);
+    __syncthreads();
+    if (group > 0) return;
+#pragma unroll
+    for (int g = 1; g < kGroups; ++g) add(stats[g][at].x, stats[g][at].y, sums[g][at][i]);
+  }
+  if (!live) return;
+  const int64_t row = f.row + i0 + row_in;
+  const int head = kv_head * G + h0 + head_in;
   const float inv = l == 0.f ? 0.f : 1.f / l;
   *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + row * a.out_row_stride + head * a.out_head_stride + 4 * i) =
       make_uint2(pack2(o[0] * inv, o[1] * inv), pack2(o[2] * inv, o[3] * inv));
-  if (a.lse && i == 0) a.lse[at] = l == 0.f ? neg_inf() : m * 0.6931471805599453f + logf(l);
+  if (a.lse && i == 0) a.lse[row * a.Hq + head] = l == 0.f ? neg_inf() : m * 0.6931471805599453f + logf(l);
 }
 
 struct Plan {
   int waves;               // of a workgroup, 32 slots each
   int heads, blocks;       // heads of a slot block, blocks of a key head's group
   int tok;                 // rows of a tile
-  int64_t tiles;           // at most, of all requests
-  int splits;
+  int64_t groups, tiles, items;   // head blocks; of one: tiles at most, items
 };
 
 Plan plan_of(int64_t T, int Hq, int Hk, int B, int64_t max_seq_len) {
@@ -414,46 +471,59 @@ Plan plan_of(int64_t T, int Hq, int Hk, int B, int64_t max_seq_len) {
   p.heads = std::min(G, slots);
   p.blocks = (G + p.heads - 1) / p.heads;
   p.tok = slots / p.heads;
+  p.groups = (int64_t)Hk * p.blocks;
   p.tiles = T / p.tok + seqs;
-  const int64_t units = p.tiles * Hk * p.blocks, places = p.waves == 1 ? 1024 : 512;
-  const int64_t tiles = (max_seq_len + kTile - 1) / kTile;
-  p.splits = (int)std::max<int64_t>(1, std::min<int64_t>({places / std::max<int64_t>(units, 1), (tiles + 3) / 4, 64}));
+  const int64_t room = (p.waves == 1 ? 1024 : 512) / p.groups;
+  p.items = max_seq_len > kMinShare * kTile && room > p.tiles ? room : p.tiles;
   return p;
 }
 
 int64_t align256(int64_t x) { return (x + 255) / 256 * 256; }
 
+// Of the shares' statistics and sums, where there are shares.
+int64_t ml_bytes(const Plan& p) { return align256(p.groups * p.items * p.waves * kWaveSlots * 8); }
+int64_t part_bytes(const Plan& p, int dv) {
+  return p.items == p.tiles ? 0 : ml_bytes(p) + p.groups * p.items * p.waves * kWaveSlots * dv * 4;
+}
+
 template <int kDk, int kDv>
 hipError_t launch(const PromptArgs& a, void* workspace, hipStream_t stream) {
   const Plan p = plan_of(a.T, a.Hq, a.Hk, a.B, a.max_seq_len);
-  PromptParts parts{nullptr, nullptr, p.splits, p.tok, p.heads, p.blocks, p.tiles};
-  if (p.splits > 1) {
+  PromptParts parts{nullptr, nullptr, p.tok, p.heads, p.blocks, (uint32_t)p.tiles, (uint32_t)p.items, p.items != p.tiles};
+  if (parts.shares) {
     parts.ml = static_cast<float*>(workspace);
-    parts.o = reinterpret_cast<float*>(static_cast<char*>(workspace) + align256(a.T * a.Hq * p.splits * 8));
+    parts.o = reinterpret_cast<float*>(static_cast<char*>(workspace) + ml_bytes(p));
   }
-  const dim3 grid((uint32_t)(p.tiles * a.Hk * p.blocks * p.splits));
+  const dim3 grid((uint32_t)(p.groups * p.items));
   if (p.waves == 1)
     hipLaunchKernelGGL((prompt_kernel<kDk, kDv, 1>), grid, dim3(kWave), 0, stream, a, parts);
   else
     hipLaunchKernelGGL((prompt_kernel<kDk, kDv, 4>), grid, dim3(4 * kWave), 0, stream, a, parts);
   hipError_t e = hipGetLastError();
-  if (e != hipSuccess || p.splits == 1) return e;
-  const dim3 join((uint32_t)((a.T * a.Hq * (kDv / 4) + 255) / 256));
-  hipLaunchKernelGGL((prompt_join_kernel<kDv>), join, dim3(256), 0, stream, a, parts);
+  if (e != hipSuccess || !parts.shares) return e;
+  const bool many = p.items >= 8 * p.tiles;            // shares of a tile
+  const int slots = p.waves * kWaveSlots, at = 256 / (kDv / 4) / (many ? 8 : 1);
+  const dim3 join((uint32_t)(p.groups * p.tiles * (slots / at)));
+#define MXIDX_JOIN(slots_, groups_) \
+  hipLaunchKernelGGL((prompt_join_kernel<kDv, slots_, groups_>), join, dim3(256), 0, stream, a, parts)
+  if (p.waves == 1) {
+    if (many) MXIDX_JOIN(32, 8); else MXIDX_JOIN(32, 1);
+  } else {
+    if (many) MXIDX_JOIN(128, 8); else MXIDX_JOIN(128, 1);
+  }
+#undef MXIDX_JOIN
   return hipGetLastError();
 }
 
 }  // namespace
 
 int64_t prompt_workspace_bytes(int64_t T, int Hq, int Hk, int dv, int B, int64_t max_seq_len) {
-  if (T == 0 || B == 0) return 0;
-  const Plan p = plan_of(T, Hq, Hk, B, max_seq_len);
-  return p.splits == 1 ? 0 : align256(T * Hq * p.splits * 8) + T * Hq * p.splits * dv * 4;
+  return T == 0 || B == 0 ? 0 : part_bytes(plan_of(T, Hq, Hk, B, max_seq_len), dv);
 }
 
 int64_t prompt_lanes(int64_t T, int Hq, int Hk, int B, int64_t max_seq_len) {
   const Plan p = plan_of(T, Hq, Hk, B, max_seq_len);
-  return p.tiles * Hk * p.blocks * p.splits * p.waves * kWave;
+  return p.groups * p.items * p.waves * kWave;
 }
 
 hipError_t launch_attn_prompt(const PromptArgs& a, int dk, int dv, void* workspace, hipStream_t stream) {
