@@ -70,7 +70,6 @@ typedef __bf16 v4bf __attribute__((ext_vector_type(4)));
 typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
 typedef short v4s __attribute__((ext_vector_type(4)));
 typedef short v8s __attribute__((ext_vector_type(8)));
-typedef int v4i __attribute__((ext_vector_type(4)));
 #define MXIDX_LDS __attribute__((address_space(3)))
 #define MXIDX_GLOBAL __attribute__((address_space(1)))
 
@@ -237,19 +236,22 @@ struct TileCopy {
 // reads row 0's (there is one: a window over a cache without pages is empty) under the scale 1,
 // so that its values are finite: its weight is 0, and a score of its positional part, whatever that
 // holds, is masked.
-template <int kLatent, int kTile, int kMine, bool kSmall>
+template <int kLatent, int kTile, int kMine, bool kSmall, bool kWide>
 struct MxCopy {
   using Page = MxPage<kLatent>;
   using Bytes = MXIDX_GLOBAL const uint8_t*;
   static constexpr int LB = kLatent / kBlock, LC = kLatent / 8, PC = kRopeWidth / 8;
   static constexpr int kPer = kWave / LB, kLoads = (kMine + kPer - 1) / kPer;      // tokens a load
   static constexpr int kPosPer = kWave / PC, kPosPieces = kMine / kPosPer;
+  static constexpr int kYoungest = kWide ? 2 * kLoads : kLoads + 1;                // instructions of load()
   static constexpr int kRawBytes = kLoads * kWave * 16;                            // of the wave
-  static_assert(kMine % kPosPer == 0 && (kMine % kPer == 0 || kMine < kPer), "whole instructions");
+  static constexpr int SD = LB / 4;                    // dwords of a token's scales
+  static constexpr int kDwords = kWide ? 4 : 2;        // of a lane's four on their way at a time
+  static_assert(kMine % kPosPer == 0 && (kMine % kPer == 0 || kMine < kPer) && kMine * SD <= kWave, "whole instructions");
   static_assert(Page::kBytes % 256 == 0 && Page::kBytes < 65536, "a row's place fits its page's lowest bits");
 
-  uint32_t scale[kLoads];
-  v4i codes;
+  uint32_t scales[kWide ? kLoads : 1], scale, codes[kDwords];
+  uint32_t from, to;
 
   static __device__ __forceinline__ int row_code(bool ok, uint32_t page, uint32_t place) {
     return !ok ? kNoRow : (int)(kSmall ? page * (uint32_t)Page::kBytes + place : page * kPage + place);
@@ -281,18 +283,25 @@ struct MxCopy {
                                        (MXIDX_LDS void*)dst, 16, 0, 0);
   }
 
+  // The scales and the codes.
   __device__ __forceinline__ void load(const Source& src, MXIDX_LDS uint8_t* raw, int first, int rows, uint32_t ln) {
+    auto scale_at = [&](int row, uint32_t at) __attribute__((always_inline)) {
+      if constexpr (kSmall) {
+        const int o = (int)offset(row, Page::kScales, Page::kScaleBase + at);
+        if constexpr (kWide) return (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(buffer_rsrc(src.base, (int)src.bytes), o, 0, 0);
+        else return (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(buffer_rsrc(src.base, (int)src.bytes), o, 0, 0);
+      } else {
+        const Bytes p = address((Bytes)src.base, row, Page::kScales, Page::kScaleBase + at);
+        const uint32_t s = kWide ? (uint32_t)*p : *(MXIDX_GLOBAL const uint32_t*)p;
+        return row == kNoRow ? 0x7f7f7f7fu : s;
+      }
+    };
+    if constexpr (!kWide)
+      scales[0] = scale_at(__builtin_amdgcn_ds_bpermute(4 * (first + min((int)(ln / SD), kMine - 1)), rows), 4 * (ln % SD));
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
       const int row = __builtin_amdgcn_ds_bpermute(4 * (first + token(i, ln)), rows);
-      const uint32_t at = Page::kScaleBase + ln % LB;
-      if constexpr (kSmall) {
-        scale[i] = __builtin_amdgcn_raw_buffer_load_b8(buffer_rsrc(src.base, (int)src.bytes),
-                                                       (int)offset(row, Page::kScales, at), 0, 0);
-      } else {
-        const uint32_t s = *address((Bytes)src.base, row, Page::kScales, at);
-        scale[i] = row == kNoRow ? 127u : s;
-      }
+      if constexpr (kWide) scales[i] = scale_at(row, ln % LB);
       copy(src, row, Page::kCodes, 16 * (ln % LB), raw + i * (kWave * 16));
     }
   }
@@ -305,21 +314,37 @@ struct MxCopy {
          tile + kTile * kLatent * 2 + t0 * PC * 16);
   }
 
-  __device__ __forceinline__ void take(int i, MXIDX_LDS const uint8_t* raw, uint32_t ln) {
-    codes = *(MXIDX_LDS const v4i*)(raw + i * (kWave * 16) + 16 * ln);
+  // A lane's way from the buffer to the tile: it takes the dwords of its 16 bytes in an order of its own
+  // (dword j ^ turn as the j-th), so that sixteen lanes' stores of 16 bytes fall on all banks.  The
+  // tokens of load i differ from those of load 0 in bits of their own, and swz is linear in bits.
+  __device__ __forceinline__ void prepare(int first, uint32_t ln) {
+    const uint32_t c = ln % LB, turn = LB == 16 ? (ln >> 2) & 3 : LB == 8 ? (ln >> 2) & 1 : (ln >> 3) & 1;
+    const int t = first + token(0, ln);
+    from = 16 * ln + 4 * turn;
+    to = (uint32_t)t * (kLatent * 2) + (((4 * c + turn) ^ (uint32_t)swz<LC>(t)) << 4);
   }
 
-  // Load i's codes to the tile: chunks 4c .. 4c+3 of the token's row, those of every second run of four
-  // blocks in another order, so that eight lanes' 16 bytes fall on different banks.
-  __device__ __forceinline__ void write(int i, MXIDX_LDS uint8_t* tile, int first, uint32_t ln) const {
-    const uint32_t c = ln % LB, turn = (c >> 2) & 1;
-    const int t = first + token(i, ln);
-    const uint32_t at = (uint32_t)t * (kLatent * 2) + (((4 * c + turn) ^ (uint32_t)swz<LC>(t)) << 4);
-    const float s = mx_scale(scale[i]);
+  // Turn i's dwords of their load, and with its first ones the block's scale.
+  __device__ __forceinline__ void take(int i, MXIDX_LDS const uint8_t* raw, uint32_t ln) {
+    const int load = i * kDwords / 4, j0 = i * kDwords % 4;
+    if constexpr (kWide) {
+      scale = scales[load];
+    } else if (j0 == 0) {
+      const int four = __builtin_amdgcn_ds_bpermute(4 * (token(load, ln) * SD + (int)(ln % LB / 4)), (int)scales[0]);
+      scale = __builtin_amdgcn_ubfe((uint32_t)four, 8 * (ln % 4), 8);
+    }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint4 x = mx_decode8((uint32_t)(turn ? codes[j ^ 1] : codes[j]), s);
-      *(MXIDX_LDS v8s*)(tile + (at ^ (uint32_t)(j << 4))) = __builtin_bit_cast(v8s, x);
+    for (int j = 0; j < kDwords; ++j)
+      codes[j] = *(MXIDX_LDS const uint32_t*)(raw + (from ^ (4u * (j0 + j))) + load * (kWave * 16));
+  }
+
+  __device__ __forceinline__ void write(int i, MXIDX_LDS uint8_t* tile) const {
+    const int load = i * kDwords / 4, j0 = i * kDwords % 4;
+#pragma unroll
+    for (int j = 0; j < kDwords; ++j) {
+      *(MXIDX_LDS v8s*)(tile + (to ^ (uint32_t)((swz<LC>(load * kPer) ^ (j0 + j)) << 4)) + load * kPer * (kLatent * 2)) =
+          __builtin_bit_cast(v8s, mx_decode8(codes[j], mx_scale(scale)));
+      if constexpr (!kWide) __builtin_amdgcn_sched_barrier(0);   // one after the other: their values take four registers
     }
   }
 };
@@ -339,7 +364,7 @@ __global__ __launch_bounds__(HG * TH * kWave, kTile == 32 ? 2 : 1) void attn_ker
   constexpr int kMine = kTile / kWaves;                // rows that a wave copies
   constexpr int kLatentBytes = kTile * kLatent * 2, kTileBytes = kTile * kRow * 2;
   using Copy = TileCopy<kLatent, kTile, kMine, kSmall>;
-  using Mx = MxCopy<kLatent, kTile, kMine, kSmall>;
+  using Mx = MxCopy<kLatent, kTile, kMine, kSmall, (HG <= 2)>;
   // Two arrays, and the loop below unrolled over them: the compiler then sees that a
   // tile's reads do not touch the one being copied, and does not wait for its copies.
   __shared__ __attribute__((aligned(1024))) uint8_t tile0[kTileBytes];
@@ -420,22 +445,41 @@ __global__ __launch_bounds__(HG * TH * kWave, kTile == 32 ? 2 : 1) void attn_ker
           x[t] = *(MXIDX_LDS const v8s*)(buf + at);
         }
       };
-      v8s x[kAhead][NT];
-#pragma unroll
-      for (int k = 0; k < kAhead; ++k) keys(k, x[k]);
 #pragma unroll
       for (int t = 0; t < NT; ++t) s[t] = v4f{0.f, 0.f, 0.f, 0.f};
+      if constexpr (kMx && HG > 2) {
+        // operand by operand, so that three of them do: two whole steps ahead spill a register of the query
+        auto key_of = [&](int e) __attribute__((always_inline)) {
+          const int k = e / NT, t = e % NT;
+          return *(MXIDX_LDS const v8s*)(buf + (k < KL ? (key ^ ((k & 3) << 6)) + (k >> 2) * 256 + t * 16 * (kLatent * 2)
+                                                       : (pos ^ ((k - KL) << 6)) + t * 16 * (kRopeWidth * 2)));
+        };
+        constexpr int kRing = 3;
+        v8s x[kRing];
 #pragma unroll
-      for (int k = 0; k < KS; ++k) {
-        __builtin_amdgcn_sched_barrier(0);
+        for (int e = 0; e < kRing; ++e) x[e] = key_of(e);
 #pragma unroll
-        for (int t = 0; t < NT; ++t) s[t] = mfma_bf16(x[k % kAhead][t], q[k], s[t]);
-        if (k + kAhead < KS) keys(k + kAhead, x[k % kAhead]);
-        if constexpr (!kMx) {
+        for (int e = 0; e < KS * NT; ++e) {
+          __builtin_amdgcn_sched_barrier(0);
+          s[e % NT] = mfma_bf16(x[e % kRing], q[e / NT], s[e % NT]);
+          if (e + kRing < KS * NT) x[e % kRing] = key_of(e + kRing);
+        }
+      } else {
+        v8s x[kAhead][NT];
 #pragma unroll
-          for (int i = 0; i < Copy::kPieces; ++i)
-            if (i * KS / Copy::kPieces == k)
-              Copy::piece(i, cache, nxt, wave * kMine, rows, ln);
+        for (int k = 0; k < kAhead; ++k) keys(k, x[k]);
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+          for (int t = 0; t < NT; ++t) s[t] = mfma_bf16(x[k % kAhead][t], q[k], s[t]);
+          if (k + kAhead < KS) keys(k + kAhead, x[k % kAhead]);
+          if constexpr (!kMx) {
+#pragma unroll
+            for (int i = 0; i < Copy::kPieces; ++i)
+              if (i * KS / Copy::kPieces == k)
+                Copy::piece(i, cache, nxt, wave * kMine, rows, ln);
+          }
         }
       }
       __builtin_amdgcn_sched_barrier(0);
@@ -521,12 +565,17 @@ __global__ __launch_bounds__(HG * TH * kWave, kTile == 32 ? 2 : 1) void attn_ker
         if (v + i + kValuesAhead < NV) values(v + i + kValuesAhead, y[(v + i) % kValuesAhead]);
       if constexpr (kMx) {
         // the next tile's codes on their way, in the product's second half
-        constexpr int kShare = NV / 2 / Mx::kLoads, kHalf = kShare / 2;
-        static_assert(kHalf % kStep == 0 && kHalf > 0, "a step of its own for each");
+        // kDwords at a time
+        constexpr int kTurns = 4 / Mx::kDwords * Mx::kLoads, kShare = NV / 2 / kTurns;
+        static_assert(kShare >= kStep && kShare % kStep == 0, "a step of its own for each turn");
 #pragma unroll
-        for (int i = 0; i < Mx::kLoads; ++i) {
-          if (v == NV / 2 + i * kShare) mx.take(i, raw, fresh_lane());
-          if (v == NV / 2 + i * kShare + kHalf) mx.write(i, nxt, wave * kMine, fresh_lane());
+        for (int i = 0; i < kTurns; ++i) {
+          if (v == NV / 2 + i * kShare) {
+            const uint32_t ln = (uint32_t)fresh_lane();
+            if (i == 0) mx.prepare(wave * kMine, ln);
+            mx.take(i, raw, ln);
+          }
+          if (v == NV / 2 + i * kShare + (kShare > kStep ? kShare / 2 : 0)) mx.write(i, nxt);
         }
       }
     }
@@ -574,10 +623,11 @@ __global__ __launch_bounds__(HG * TH * kWave, kTile == 32 ? 2 : 1) void attn_ker
         for (int i = 0; i < Mx::kPosPieces; ++i)
           Mx::position(i, cache, (MXIDX_LDS uint8_t*)tile0, wave * kMine, first_rows, ln);
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        mx.prepare(wave * kMine, ln);
 #pragma unroll
-        for (int i = 0; i < Mx::kLoads; ++i) {
+        for (int i = 0; i < 4 / Mx::kDwords * Mx::kLoads; ++i) {
           mx.take(i, raw, ln);
-          mx.write(i, (MXIDX_LDS uint8_t*)tile0, wave * kMine, ln);
+          mx.write(i, (MXIDX_LDS uint8_t*)tile0);
         }
       } else {
         copy_all(cache, (MXIDX_LDS uint8_t*)tile0, first_rows);
@@ -620,7 +670,7 @@ __global__ __launch_bounds__(HG * TH * kWave, kTile == 32 ? 2 : 1) void attn_ker
         // but for the next tile's codes and scales, whose loads are the youngest (a barrier of the
         // language would wait for them too)
         if (t + 1 < t1)
-          asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(2 * Mx::kLoads) : "memory");
+          asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(Mx::kYoungest) : "memory");
         else
           asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
         __builtin_amdgcn_s_barrier();
