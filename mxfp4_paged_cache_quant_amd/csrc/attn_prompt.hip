@@ -88,13 +88,26 @@ struct PromptParts {
   bool shares;
 };
 
+__device__ __forceinline__ float wave_sum(float x) {
+#define MXIDX_ADD(control, rows) \
+  x += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), control, rows, 0xf, true))
+  MXIDX_ADD(0x111, 0xf);
+  MXIDX_ADD(0x112, 0xf);
+  MXIDX_ADD(0x114, 0xf);
+  MXIDX_ADD(0x118, 0xf);
+  MXIDX_ADD(0x142, 0xa);
+  MXIDX_ADD(0x143, 0xc);
+#undef MXIDX_ADD
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), kWave - 1));
+}
+
 // A request's tile of query rows, where its rows, keys and values begin, and its share or shares.
 struct Found {
   int64_t row, key;        // the first query row and the first key of the request
   int n, len, pos0;        // its rows and its keys that there are, the position of its first row
   int tile;                // -1: no such tile
   int share, shares;
-  uint32_t item;           // the tile's first
+  uint32_t item, step;     // the tile's first item, and from one of its shares' to the next
 };
 
 // Item (kByItem) or tile `want` of all requests', a request's last rows, which see most, first.  Every
@@ -121,20 +134,18 @@ __device__ Found find(const PromptArgs& a, const PromptParts& parts, uint32_t wa
   auto last_of = [](uint32_t x) { return (uint32_t)__builtin_amdgcn_readlane((int)x, kWave - 1); };
   uint32_t length = ~0u;                               // of a share
   if (parts.shares) {
-    // sum(tiles * ceil(key tiles / length)) <= sum(tiles * key tiles) / length + sum(tiles) <= items; the sums
-    // are whole numbers below 2^53
-    double work = 0.0;
+    // sum(tiles * ceil(key tiles / length)) <= sum(tiles * key tiles) / length + sum(tiles) <= items; the
+    // products' and sums' roundings, each of 2^-24, come to less than 2^-8
+    float work = 0.f;
     uint32_t all = 0;
     for (int b0 = 0; b0 < a.B; b0 += kWave) {
       load(b0);
-      work += (double)tiles * (double)key_tiles();
+      work += wave_sum((float)tiles * (float)key_tiles());
       all += last_of(wave_scan(tiles));
       row0 = min(last_of(row_end), T);
     }
-#pragma unroll
-    for (int d = 1; d < kWave; d <<= 1) work += __shfl_xor(work, d);
-    const double room = (double)(parts.items - all);
-    length = max((uint32_t)kMinShare, (uint32_t)((work + room - 1.0) / room));
+    const float each = work / (float)(parts.items - all) * (1.f + 0x1p-8f);
+    length = max((uint32_t)kMinShare, (uint32_t)ceilf(each));
     row0 = 0;
   }
   Found f;
@@ -158,10 +169,12 @@ __device__ Found find(const PromptArgs& a, const PromptParts& parts, uint32_t wa
       f.key = (int64_t)((uint64_t)of((uint32_t)((uint64_t)key >> 32)) << 32 | of((uint32_t)key));
       f.len = (int)min(min((int64_t)f.len, a.max_seq_len), max(a.S - f.key, (int64_t)0));
       f.shares = (int)of(shares);
-      const uint32_t in = want - of(end - mine), turn = kByItem ? in / (uint32_t)f.shares : in;   // tiles from the last
-      f.share = kByItem ? (int)(in - turn * (uint32_t)f.shares) : 0;
-      f.item = of(item_end - items) + turn * (uint32_t)f.shares;
-      f.tile = (int)(of(tiles) - 1 - turn);
+      // a request's items: the tiles' first shares, their second ones ..., so that neighbours read the same keys
+      f.step = of(tiles);
+      const uint32_t in = want - of(end - mine), share = in / f.step, turn = in - share * f.step;   // tiles from the last
+      f.share = (int)share;
+      f.item = of(item_end - items) + turn;
+      f.tile = (int)(f.step - 1 - turn);
       return f;
     }
     row0 = min(last_of(row_end), T);
@@ -200,8 +213,12 @@ __global__ __launch_bounds__(kWaves * kWave, kWaves == 1 ? 1 : 2) void prompt_ke
 
   // each XCD takes a run of neighbouring numbers: the shares and tiles of one head, which read the
   // same keys and values
-  const uint32_t xcd = blockIdx.x % 8, number = xcd * (gridDim.x / 8) + min(xcd, gridDim.x % 8) + blockIdx.x / 8;
+  const uint32_t xcd = blockIdx.x % 8, turn = blockIdx.x / 8;
+  // (of four where there are shares: fewer than the items may be taken, and none of the XCDs gets the rest)
+  const uint32_t number = parts.shares ? (turn / 4 * 8 + xcd) * 4 + turn % 4
+                                       : xcd * (gridDim.x / 8) + min(xcd, gridDim.x % 8) + turn;
   const uint32_t hb = number / parts.items;
+  if (hb >= (uint32_t)a.Hk * parts.blocks) return;     // the grid is whole runs
   const int kv_head = (int)(hb / (uint32_t)parts.blocks), block = (int)(hb - kv_head * (uint32_t)parts.blocks);
   const Found f = find<true>(a, parts, number - hb * parts.items);
   if (f.tile < 0) return;
@@ -384,7 +401,7 @@ __global__ __launch_bounds__(kWaves * kWave, kWaves == 1 ? 1 : 2) void prompt_ke
         *reinterpret_cast<uint2*>(dst + 32 * v + 2 * j) =
             make_uint2(pack2(o[v][j] * inv, o[v][j + 1] * inv), pack2(o[v][j + 2] * inv, o[v][j + 3] * inv));
   } else {
-    const int64_t part = ((int64_t)hb * parts.items + f.item + f.share) * (kWaves * kWaveSlots) + slot;
+    const int64_t part = ((int64_t)hb * parts.items + f.item + f.share * f.step) * (kWaves * kWaveSlots) + slot;
     if (half == 0) *reinterpret_cast<float2*>(parts.ml + 2 * part) = make_float2(m, l);
     if (l == 0.f) return;                              // the join does not read its sums
     float* dst = parts.o + part * kDv + 4 * half;
@@ -401,7 +418,7 @@ __global__ __launch_bounds__(kWaves * kWave, kWaves == 1 ? 1 : 2) void prompt_ke
 // groups of one slot.
 template <int kDv, int kSlots, int kGroups>
 __global__ __launch_bounds__(256) void prompt_join_kernel(PromptArgs a, PromptParts parts) {
-  constexpr int W = kDv / 4, kAt = 256 / W / kGroups, kBatch = 4;     // slots of a workgroup
+  constexpr int W = kDv / 4, kAt = 256 / W / kGroups, kBatch = kGroups > 1 ? 8 : 4;     // slots of a workgroup
   __shared__ v4f sums[kGroups][kAt][W];
   __shared__ float2 stats[kGroups][kAt];
   const uint32_t per = kSlots / kAt, unit = blockIdx.x / per, hb = unit / parts.tiles;
@@ -429,7 +446,7 @@ __global__ __launch_bounds__(256) void prompt_join_kernel(PromptArgs a, PromptPa
       v4f x[kBatch];
 #pragma unroll
       for (int s = 0; s < kBatch; ++s) {
-        const int64_t p = first + (int64_t)min(s0 + s * kGroups, f.shares - 1) * kSlots;
+        const int64_t p = first + (int64_t)min(s0 + s * kGroups, f.shares - 1) * f.step * kSlots;
         ml[s] = *reinterpret_cast<const float2*>(parts.ml + 2 * p);
         x[s] = *reinterpret_cast<const v4f*>(parts.o + p * kDv + 4 * i);
       }
@@ -480,6 +497,10 @@ Plan plan_of(int64_t T, int Hq, int Hk, int B, int64_t max_seq_len) {
 
 int64_t align256(int64_t x) { return (x + 255) / 256 * 256; }
 
+int64_t workgroups(const Plan& p) {
+  return p.items == p.tiles ? p.groups * p.items : (p.groups * p.items + 31) / 32 * 32;
+}
+
 // Of the shares' statistics and sums, where there are shares.
 int64_t ml_bytes(const Plan& p) { return align256(p.groups * p.items * p.waves * kWaveSlots * 8); }
 int64_t part_bytes(const Plan& p, int dv) {
@@ -494,14 +515,14 @@ hipError_t launch(const PromptArgs& a, void* workspace, hipStream_t stream) {
     parts.ml = static_cast<float*>(workspace);
     parts.o = reinterpret_cast<float*>(static_cast<char*>(workspace) + ml_bytes(p));
   }
-  const dim3 grid((uint32_t)(p.groups * p.items));
+  const dim3 grid((uint32_t)workgroups(p));
   if (p.waves == 1)
     hipLaunchKernelGGL((prompt_kernel<kDk, kDv, 1>), grid, dim3(kWave), 0, stream, a, parts);
   else
     hipLaunchKernelGGL((prompt_kernel<kDk, kDv, 4>), grid, dim3(4 * kWave), 0, stream, a, parts);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || !parts.shares) return e;
-  const bool many = p.items >= 8 * p.tiles;            // shares of a tile
+  const bool many = p.items >= 24 * p.tiles;            // shares of a tile
   const int slots = p.waves * kWaveSlots, at = 256 / (kDv / 4) / (many ? 8 : 1);
   const dim3 join((uint32_t)(p.groups * p.tiles * (slots / at)));
 #define MXIDX_JOIN(slots_, groups_) \
@@ -523,7 +544,7 @@ int64_t prompt_workspace_bytes(int64_t T, int Hq, int Hk, int dv, int B, int64_t
 
 int64_t prompt_lanes(int64_t T, int Hq, int Hk, int B, int64_t max_seq_len) {
   const Plan p = plan_of(T, Hq, Hk, B, max_seq_len);
-  return p.groups * p.items * p.waves * kWave;
+  return workgroups(p) * p.waves * kWave;
 }
 
 hipError_t launch_attn_prompt(const PromptArgs& a, int dk, int dv, void* workspace, hipStream_t stream) {
