@@ -145,7 +145,7 @@ __device__ Found find(const PromptArgs& a, const PromptParts& parts, uint32_t wa
       row0 = min(last_of(row_end), T);
     }
     const float each = work / (float)(parts.items - all) * (1.f + 0x1p-8f);
-    length = max((uint32_t)kMinShare, (uint32_t)ceilf(each));
+    length = max((uint32_t)kMinShare, (uint32_t)ceilf(fminf(each, 0x1p30f)));
     row0 = 0;
   }
   Found f;
