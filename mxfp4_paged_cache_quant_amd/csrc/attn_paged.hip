@@ -870,7 +870,11 @@ struct Plan {
 // with 16 heads, 277 with 32, 379 with 64).
 int64_t split_places(int latent) { return latent <= 128 ? 2 * kCus : kCus; }
 
-Plan plan_of(int64_t rows, int H, int latent, int64_t entries) {
+// Over the MXFP4 cache (mx) windows of up to 5, 4 and 3 tiles of latent 128, 256 and 512 are not split:
+// the second launch costs as much as the tiles that it saves (one row of 8 heads, 129 tokens, in a
+// graph and called one by one: 6.9 / 9.3 us, 8.0 / 12.1 split, latent 128; 8.6 / 9.4 and 9.8 / 11.9,
+// 256; 12.0 / 12.0 and 12.4 / 12.8, 512; of 385 tokens, latent 256, 13.4 / 13.4 and 10.2 / 11.9).
+Plan plan_of(int64_t rows, int H, int latent, int64_t entries, bool mx = false) {
   Plan p;
   const int64_t tiles = (entries + 63) / 64, quarter = std::min<int64_t>((tiles + 3) / 4, kMaxSplits);
   const int64_t places = split_places(latent);
@@ -880,6 +884,7 @@ Plan plan_of(int64_t rows, int H, int latent, int64_t entries) {
   p.tile = p.group_heads == 64 && units >= 2 * kCus ? 32 : 64;
   const int64_t shares = units * quarter <= 64 ? std::min<int64_t>((tiles + 1) / 2, kMaxSplits) : quarter;
   p.splits = (int)std::max<int64_t>(1, std::min(places / std::max<int64_t>(units, 1), shares));
+  if (mx && tiles <= (latent == 128 ? 5 : latent == 256 ? 4 : 3)) p.splits = 1;
   return p;
 }
 
@@ -891,7 +896,7 @@ int64_t part_bytes(int64_t parts, int latent) { return ml_bytes(parts) + parts *
 
 template <int kLatent, bool kMx>
 hipError_t launch(const AttnArgs& a, void* workspace, hipStream_t stream) {
-  const Plan p = plan_of(a.rows, a.H, kLatent, a.indices ? a.k : a.max_tokens);
+  const Plan p = plan_of(a.rows, a.H, kLatent, a.indices ? a.k : a.max_tokens, kMx);
   const int64_t cache_bytes = a.num_pages * (kMx ? mx_page_bytes(kLatent) : kPage * (kLatent + kRopeWidth) * 2);
   const int64_t q_bytes = ((a.H - 1) * a.q_head_stride + kLatent + kRopeWidth) * 2;
   const bool small = cache_bytes <= kReach && q_bytes <= kReach;

@@ -237,3 +237,32 @@ def test_refusals_of_the_wrapper():
                    dict(max_tokens=129), dict(ke=args["ke"].long())):
         with pytest.raises(mx.MxidxError):
             mx.attn_paged_mxfp4(**{**args, **change})
+
+
+def test_two_graphs_share_a_workspace():
+    cs, ws, graphs = [_case(30, [900, 40], H=40, latent=256), _case(31, [700], H=64, latent=512, k=600)], None, []
+    ws = mx.attn_workspace(2, 64, 512, 1024)
+    ws = torch.full((max(ws.numel(), mx.attn_workspace_max_bytes(2, 64, 256, 1024)),), 0xFF, dtype=torch.uint8, device="cuda")
+    for c in cs:
+        a = _args(c)
+        mx.attn_paged_mxfp4(**a, workspace=ws)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got = mx.attn_paged_mxfp4(**a, workspace=ws)
+        graphs.append((g, got, a))
+    for rep in range(3):
+        for (g, got, _), c in zip(graphs, cs):
+            ws.fill_(0xFF)
+            g.replay()
+            torch.cuda.synchronize()
+            _close(got, _oracle(c), rep)
+
+
+@pytest.mark.parametrize("latent", [128, 256, 512])
+@pytest.mark.parametrize("H", [8, 32, 128])
+def test_short_windows_split_and_whole(latent, H):
+    # both sides of the sizes up to which a row is not split, for one row and for three
+    for n in (65, 128, 129, 192, 193, 256, 257, 320, 321):
+        _check(_case(n, [n], H=H, latent=latent))
+    _check(_case(7, [321, 64, 200], H=H, latent=latent, k=190))

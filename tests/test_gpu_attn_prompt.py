@@ -266,3 +266,22 @@ def test_refusals_of_the_wrapper():
                    dict(q=q[..., 1:65]), dict(k=k.cpu())):
         with pytest.raises(mx.MxidxError):
             mx.attn_prompt(**{**a, **change})
+
+
+def test_two_graphs_share_a_workspace():
+    cs = [_case(30, [900, 40], [2, 5], 8, 2), _case(31, [300, 700, 5], [40, 1, 5], 4, 2, (192, 128))]
+    ws, graphs = mx.attn_prompt_workspace(), []
+    for c in cs:
+        a = _args(c)
+        mx.attn_prompt(**a, workspace=ws)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got = mx.attn_prompt(**a, workspace=ws)
+        graphs.append((g, got, a))
+    ws.fill_(0xFF)
+    for rep in range(3):
+        for (g, got, _), c in zip(graphs, cs):
+            g.replay()
+            torch.cuda.synchronize()
+            _close(got, _oracle(c), rep)
