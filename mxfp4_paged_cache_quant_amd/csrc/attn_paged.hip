@@ -236,21 +236,21 @@ struct TileCopy {
 // reads row 0's (there is one: a window over a cache without pages is empty) under the scale 1,
 // so that its values are finite: its weight is 0, and a score of its positional part, whatever that
 // holds, is masked.
-template <int kLatent, int kTile, int kMine, bool kSmall, bool kWide>
+template <int kLatent, int kTile, int kMine, bool kSmall, bool kSpare>
 struct MxCopy {
   using Page = MxPage<kLatent>;
   using Bytes = MXIDX_GLOBAL const uint8_t*;
   static constexpr int LB = kLatent / kBlock, LC = kLatent / 8, PC = kRopeWidth / 8;
   static constexpr int kPer = kWave / LB, kLoads = (kMine + kPer - 1) / kPer;      // tokens a load
   static constexpr int kPosPer = kWave / PC, kPosPieces = kMine / kPosPer;
-  static constexpr int kYoungest = kWide ? 2 * kLoads : kLoads + 1;                // instructions of load()
+  static constexpr int kYoungest = kSpare ? 2 * kLoads : kLoads + 1;                // instructions of load()
   static constexpr int kRawBytes = kLoads * kWave * 16;                            // of the wave
   static constexpr int SD = LB / 4;                    // dwords of a token's scales
-  static constexpr int kDwords = kWide ? 4 : 2;        // of a lane's four on their way at a time
+static constexpr int kDwords = 4 * kLoads;           // a lane's
   static_assert(kMine % kPosPer == 0 && (kMine % kPer == 0 || kMine < kPer) && kMine * SD <= kWave, "whole instructions");
   static_assert(Page::kBytes % 256 == 0 && Page::kBytes < 65536, "a row's place fits its page's lowest bits");
 
-  uint32_t scales[kWide ? kLoads : 1], scale, codes[kDwords];
+  uint32_t scales[kSpare ? kLoads : 1], scale, codes[2];
   uint32_t from, to;
 
   static __device__ __forceinline__ int row_code(bool ok, uint32_t page, uint32_t place) {
@@ -288,20 +288,20 @@ struct MxCopy {
     auto scale_at = [&](int row, uint32_t at) __attribute__((always_inline)) {
       if constexpr (kSmall) {
         const int o = (int)offset(row, Page::kScales, Page::kScaleBase + at);
-        if constexpr (kWide) return (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(buffer_rsrc(src.base, (int)src.bytes), o, 0, 0);
+        if constexpr (kSpare) return (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(buffer_rsrc(src.base, (int)src.bytes), o, 0, 0);
         else return (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(buffer_rsrc(src.base, (int)src.bytes), o, 0, 0);
       } else {
         const Bytes p = address((Bytes)src.base, row, Page::kScales, Page::kScaleBase + at);
-        const uint32_t s = kWide ? (uint32_t)*p : *(MXIDX_GLOBAL const uint32_t*)p;
+        const uint32_t s = kSpare ? (uint32_t)*p : *(MXIDX_GLOBAL const uint32_t*)p;
         return row == kNoRow ? 0x7f7f7f7fu : s;
       }
     };
-    if constexpr (!kWide)
+    if constexpr (!kSpare)
       scales[0] = scale_at(__builtin_amdgcn_ds_bpermute(4 * (first + min((int)(ln / SD), kMine - 1)), rows), 4 * (ln % SD));
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
       const int row = __builtin_amdgcn_ds_bpermute(4 * (first + token(i, ln)), rows);
-      if constexpr (kWide) scales[i] = scale_at(row, ln % LB);
+      if constexpr (kSpare) scales[i] = scale_at(row, ln % LB);
       copy(src, row, Page::kCodes, 16 * (ln % LB), raw + i * (kWave * 16));
     }
   }
@@ -324,28 +324,18 @@ struct MxCopy {
     to = (uint32_t)t * (kLatent * 2) + (((4 * c + turn) ^ (uint32_t)swz<LC>(t)) << 4);
   }
 
-  // Turn i's dwords of their load, and with its first ones the block's scale.
-  __device__ __forceinline__ void take(int i, MXIDX_LDS const uint8_t* raw, uint32_t ln) {
-    const int load = i * kDwords / 4, j0 = i * kDwords % 4;
-    if constexpr (kWide) {
-      scale = scales[load];
-    } else if (j0 == 0) {
-      const int four = __builtin_amdgcn_ds_bpermute(4 * (token(load, ln) * SD + (int)(ln % LB / 4)), (int)scales[0]);
+  // Dword u % 4 of load u / 4, and with a load's first one its block's scale.
+  __device__ __forceinline__ void take(int u, MXIDX_LDS const uint8_t* raw, uint32_t ln) {
+    if (!kSpare && u % 4 == 0) {
+      const int four = __builtin_amdgcn_ds_bpermute(4 * (token(u / 4, ln) * SD + (int)(ln % LB / 4)), (int)scales[0]);
       scale = __builtin_amdgcn_ubfe((uint32_t)four, 8 * (ln % 4), 8);
     }
-#pragma unroll
-    for (int j = 0; j < kDwords; ++j)
-      codes[j] = *(MXIDX_LDS const uint32_t*)(raw + (from ^ (4u * (j0 + j))) + load * (kWave * 16));
+    codes[u % 2] = *(MXIDX_LDS const uint32_t*)(raw + (from ^ (4u * (u % 4))) + u / 4 * (kWave * 16));
   }
 
-  __device__ __forceinline__ void write(int i, MXIDX_LDS uint8_t* tile) const {
-    const int load = i * kDwords / 4, j0 = i * kDwords % 4;
-#pragma unroll
-    for (int j = 0; j < kDwords; ++j) {
-      *(MXIDX_LDS v8s*)(tile + (to ^ (uint32_t)((swz<LC>(load * kPer) ^ (j0 + j)) << 4)) + load * kPer * (kLatent * 2)) =
-          __builtin_bit_cast(v8s, mx_decode8(codes[j], mx_scale(scale)));
-      if constexpr (!kWide) __builtin_amdgcn_sched_barrier(0);   // one after the other: their values take four registers
-    }
+  __device__ __forceinline__ void write(int u, MXIDX_LDS uint8_t* tile) const {
+    *(MXIDX_LDS v8s*)(tile + (to ^ (uint32_t)((swz<LC>(u / 4 * kPer) ^ (u % 4)) << 4)) + u / 4 * kPer * (kLatent * 2)) =
+        __builtin_bit_cast(v8s, mx_decode8(codes[u % 2], mx_scale(kSpare ? scales[u / 4] : scale)));
   }
 };
 
@@ -364,7 +354,8 @@ __global__ __launch_bounds__(HG * TH * kWave, kTile == 32 ? 2 : 1) void attn_ker
   constexpr int kMine = kTile / kWaves;                // rows that a wave copies
   constexpr int kLatentBytes = kTile * kLatent * 2, kTileBytes = kTile * kRow * 2;
   using Copy = TileCopy<kLatent, kTile, kMine, kSmall>;
-  using Mx = MxCopy<kLatent, kTile, kMine, kSmall, (HG <= 2)>;
+  constexpr bool kSpare = HG <= 2;                     // registers: these forms have a SIMD's to a wave
+  using Mx = MxCopy<kLatent, kTile, kMine, kSmall, kSpare>;
   // Two arrays, and the loop below unrolled over them: the compiler then sees that a
   // tile's reads do not touch the one being copied, and does not wait for its copies.
   __shared__ __attribute__((aligned(1024))) uint8_t tile0[kTileBytes];
@@ -548,6 +539,10 @@ __global__ __launch_bounds__(HG * TH * kWave, kTile == 32 ? 2 : 1) void attn_ker
         return mfma_bf16(__builtin_shufflevector(z[0], z[NT - 1], 0, 1, 2, 3, 4, 5, 6, 7),
                          __builtin_bit_cast(v8s, uint4{by[0][0], by[0][1], by[NT - 1][0], by[NT - 1][1]}), c);
     };
+    if constexpr (kMx && kSpare) {
+      mx.prepare(wave * kMine, (uint32_t)fresh_lane());
+      mx.take(0, raw, 0);
+    }
 #pragma unroll
     for (int v = 0; v < kValuesAhead; ++v) values(v, y[v]);
     // parts of the output at a time: two where a wave is alone on its SIMD, so that no sum waits
@@ -564,18 +559,33 @@ __global__ __launch_bounds__(HG * TH * kWave, kTile == 32 ? 2 : 1) void attn_ker
       for (int i = 0; i < kStep; ++i)
         if (v + i + kValuesAhead < NV) values(v + i + kValuesAhead, y[(v + i) % kValuesAhead]);
       if constexpr (kMx) {
-        // the next tile's codes on their way, in the product's second half
-        // kDwords at a time
-        constexpr int kTurns = 4 / Mx::kDwords * Mx::kLoads, kShare = NV / 2 / kTurns;
-        static_assert(kShare >= kStep && kShare % kStep == 0, "a step of its own for each turn");
-#pragma unroll
-        for (int i = 0; i < kTurns; ++i) {
-          if (v == NV / 2 + i * kShare) {
-            const uint32_t ln = (uint32_t)fresh_lane();
-            if (i == 0) mx.prepare(wave * kMine, ln);
-            mx.take(i, raw, ln);
+        // the next tile's codes on their way.  With registers to spare a dword at a time all along the
+        // product, each read a step before it is written (1024 rows of 2048 tokens, 16 heads: 256 us, 270
+        // with four at a time in its second half); else two at a time in its second half, written one after
+        // the other, as their values take four registers each
+        if constexpr (kSpare) {
+          constexpr int kGap = NV / Mx::kDwords;
+          static_assert(kGap % kStep == 0 && kGap > 0, "a step of its own for each");
+          if (v % kGap == 0) {
+            if (v / kGap + 1 < Mx::kDwords) mx.take(v / kGap + 1, raw, 0);
+            mx.write(v / kGap, nxt);
           }
-          if (v == NV / 2 + i * kShare + (kShare > kStep ? kShare / 2 : 0)) mx.write(i, nxt);
+        } else {
+          constexpr int kGap = NV / Mx::kDwords;       // half a product for twice as many
+          static_assert(kGap > kStep && kGap % (2 * kStep) == 0, "steps of their own");
+          const int u = 2 * ((v - NV / 2) / kGap);
+          if (v >= NV / 2 && (v - NV / 2) % kGap == 0) {
+            const uint32_t ln = (uint32_t)fresh_lane();
+            if (u == 0) mx.prepare(wave * kMine, ln);
+            mx.take(u, raw, ln);
+            mx.take(u + 1, raw, ln);
+          }
+          if (v >= NV / 2 && (v - NV / 2) % kGap == kGap / 2) {
+            mx.write(u, nxt);
+            __builtin_amdgcn_sched_barrier(0);
+            mx.write(u + 1, nxt);
+            __builtin_amdgcn_sched_barrier(0);
+          }
         }
       }
     }
@@ -625,9 +635,9 @@ __global__ __launch_bounds__(HG * TH * kWave, kTile == 32 ? 2 : 1) void attn_ker
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         mx.prepare(wave * kMine, ln);
 #pragma unroll
-        for (int i = 0; i < 4 / Mx::kDwords * Mx::kLoads; ++i) {
-          mx.take(i, raw, ln);
-          mx.write(i, (MXIDX_LDS uint8_t*)tile0);
+        for (int u = 0; u < Mx::kDwords; ++u) {
+          mx.take(u, raw, ln);
+          mx.write(u, (MXIDX_LDS uint8_t*)tile0);
         }
       } else {
         copy_all(cache, (MXIDX_LDS uint8_t*)tile0, first_rows);
