@@ -17,6 +17,22 @@
 // so a lane (and the one 32 lanes on) holds one slot throughout: the weights leave the first product
 // in the registers where the second takes them (half h of the lanes: tokens 4h..4h+3 and
 // 8+4h..8+4h+3 of 16), and the running maximum and sum are one register each.
+//
+// The weights go to the second product rounded to bf16 (2^-8), relative to the running maximum itself, so
+// that a token that dominates a row weighs exactly 1; l and lse take them unrounded.  The output's
+// error is 1.1-1.2 times its own rounding's.  A second part of the weights, as the attention over the
+// cache has it, would be half as many products again where the products are what bounds the kernel.
+//
+// What bounds it: with many rows the card's power.  A prompt of 16384 tokens, 16 heads of 192 / 128,
+// takes 1.25-1.3 ms = 1,050-1,100 TFLOP/s at 1.4-1.7 GHz, where a large library product reaches
+// 1,310-1,400 (inputs of zeros: 0.9 ms); of the SIMDs' cycles 60% are MFMAs, and no LDS access
+// meets a bank conflict.  Steps: operands kept three and four steps ahead (1286 -> 1247 us; heads of
+// 64, four prompts of 4000, 191 -> 169); two to four steps ahead, values read before the weights
+// are there, and a wave priority for the products: all within 1%.  Scores a tile ahead of the weights in
+// one wave (its registers are full): 298 and 303 us for a prompt of 8192 tokens, 16 heads of 128.  Eight
+// waves a workgroup: 3% faster there, 40% slower for heads of 64, 2% for packed prompts of 1000.
+// With few rows over many tokens it is HBM: 64 rows, 32 heads of 128 on 4, over 1000-8192 tokens each
+// 120 us = 5.0 TB/s, where a large copy makes 4.7-4.9.
 #include <algorithm>
 
 #include "common.hpp"
@@ -479,6 +495,14 @@ struct Plan {
   int64_t groups, tiles, items;   // head blocks; of one: tiles at most, items
 };
 
+// One wave a workgroup where a request's rows and a group's heads come to 32 slots, four else (64 requests,
+// one row each, 32 heads on 4: 121 us, 152 with four waves; 16 requests of 5 rows, 40 slots: 57 and
+// 61 with one).  Shares where the tiles alone leave workgroups' places free and windows are longer
+// than one share: two workgroups of four waves a CU, whose LDS they fill (one: 129 us for 4 requests
+// of 61 rows over 16000-65536 tokens, 122 so), or four of one wave, in two turns (64 requests of
+// one row: 138 us with two a CU, 121 with four, 127 with eight).  A share walks 4 tiles or more
+// (one row over 65536 tokens: 34 us, 44 with 8; three prompts of up to 129 tokens: 8 us, 14 with 2,
+// for the second launch).
 Plan plan_of(int64_t T, int Hq, int Hk, int B, int64_t max_seq_len) {
   Plan p;
   const int G = Hq / Hk;
@@ -522,7 +546,9 @@ hipError_t launch(const PromptArgs& a, void* workspace, hipStream_t stream) {
     hipLaunchKernelGGL((prompt_kernel<kDk, kDv, 4>), grid, dim3(4 * kWave), 0, stream, a, parts);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || !parts.shares) return e;
-  const bool many = p.items >= 24 * p.tiles;            // shares of a tile
+  // eight groups of lanes a slot where a tile may have many shares, up to 1024 of them (one row over
+  // 65536 tokens: 25.2 us, 26.9 with batches of four), else a slot to each (4 requests of 61 rows: 113, 122)
+  const bool many = p.items >= 24 * p.tiles;
   const int slots = p.waves * kWaveSlots, at = 256 / (kDv / 4) / (many ? 8 : 1);
   const dim3 join((uint32_t)(p.groups * p.tiles * (slots / at)));
 #define MXIDX_JOIN(slots_, groups_) \

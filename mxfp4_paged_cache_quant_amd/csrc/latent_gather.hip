@@ -5,7 +5,9 @@
 // 8 values (a dword) a lane, so that a wave's stores are whole rows; eight lanes copy its
 // positional part.  kBatch of a wave's rows are loaded before the first is written.
 //
-// Bound by HBM, mostly by its writes (400 B read and 1152 B written a token at latent 512).
+// Bound by HBM, mostly by its writes (400 B read and 1152 B written a token at latent 512): 122,880
+// tokens of eight requests 43.3 us = 4.4 TB/s, where a large copy makes 4.7-4.9; 110,000 tokens of
+// 200 requests, latent 128, 13.6 us = 4.7 TB/s.
 #include "common.hpp"
 #include "latent_mxfp4.hpp"
 #include "launch.hpp"
