@@ -786,6 +786,15 @@ int idx_attn_prompt(const void* q, int64_t q_row_stride, int64_t q_head_stride, 
                     int64_t out_row_stride, int64_t out_head_stride, float* lse, void* workspace,
                     size_t workspace_bytes, hipStream_t stream);
 
+/* idx_call -- one of the calls of a serving step (idx_step_map and those below it) with its arguments
+ * in an array, for bindings whose time grows with the number of arguments.
+ *   idx_entry(name): the call's number, -1 if there is none of that name.
+ *   words: count 8-byte words in the order of the call's arguments, the stream the last: pointers, integers as
+ *   int64_t, float and double as double.  IDX_ERR_ARG also for another count than the call's and for
+ *   an integer that its argument does not hold. */
+int idx_entry(const char* name);
+int idx_call(int entry, const void* words, int count);
+
 #ifdef __cplusplus
 }
 #endif

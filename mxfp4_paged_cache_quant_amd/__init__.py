@@ -12,6 +12,7 @@ Build the library with ``python -m mxfp4_paged_cache_quant_amd.build``.
 import collections
 import ctypes
 import os
+import struct
 
 __all__ = [
     "MxidxError", "lib", "lib_path", "version", "init",
@@ -154,6 +155,8 @@ EXPORTS = {
                                _i64, _i64, _int, _int, _int, _c_void_p, _c_void_p, _int, _i64, _int,
                                _float, _c_void_p, _i64, _i64, _c_void_p, _c_void_p, ctypes.c_size_t,
                                _c_void_p]),
+    "idx_entry": (_int, [ctypes.c_char_p]),
+    "idx_call": (_int, [_int, ctypes.c_char_p, _int]),
 }
 
 
@@ -945,9 +948,20 @@ def _on(device, t, name, dtype, shape=None):
     raise MxidxError(f"{name} must be contiguous of shape {shape}, got {tuple(t.shape)}")
 
 
+_PACKED = {}
+
+
+def _packed(name):
+    """(number, packer of the arguments' 8-byte words, their count) of a call."""
+    words = "".join("d" if t in (_float, _double) else "q" for t in EXPORTS[name][1])
+    _PACKED[name] = lib().idx_entry(name.encode()), struct.Struct("=" + words).pack, len(words)
+    return _PACKED[name]
+
+
 def _call(name, device, stream, *args):
     """One call of the library with `device` current, on `stream` (None: that device's
-    current stream)."""
+    current stream).  Null pointers are 0; the arguments go over packed (idx_call): one by one their
+    conversion takes as long as the launch."""
     torch = _torch()
     index = device.index
     if stream is None:
@@ -956,12 +970,17 @@ def _call(name, device, stream, *args):
         raise MxidxError(f"{name}: the stream belongs to {stream.device}, the tensors to {device}")
     else:
         raw = stream.cuda_stream
-    fn = getattr(lib(), name)
+    entry, pack, count = _PACKED.get(name) or _packed(name)
+    try:
+        words = pack(*args, raw)
+    except struct.error as e:
+        raise MxidxError(f"{name}: {e}") from None
+    call = _LIB.idx_call
     if torch._C._cuda_getDevice() == index:
-        status = fn(*args, raw)
+        status = call(entry, words, count)
     else:
         with torch.cuda.device(device):
-            status = fn(*args, raw)
+            status = call(entry, words, count)
     if status != 0:
         _check(status, name)
 
@@ -990,7 +1009,7 @@ def _rope_args(device, cos, sin, rope_dim, mode, positions, tokens):
     table = (cos.shape[0], rope_dim // 2)
     cp = _on(device, cos, "cos", torch.float32, table)
     sp = _on(device, sin, "sin", torch.float32, table)
-    pp = None if positions is None else _on(device, positions, "positions", torch.int64, (tokens,))
+    pp = 0 if positions is None else _on(device, positions, "positions", torch.int64, (tokens,))
     return _Rope(cp, sp, table[0], pp, rope_dim, _code(_MODES, mode, "mode"))
 
 
@@ -1023,7 +1042,7 @@ def step_map(seq_lens, query_lens, block_table, num_rows, free_pages=None, free_
         raise MxidxError("block_table must be [B, pages] with unit inner stride")
     pages = shape[1]
     stride = strides[0] if B > 1 else max(pages, 1)
-    fp = ip = None
+    fp = ip = 0
     free = 0
     if free_pages is not None:
         if free_start is None:
@@ -1077,8 +1096,8 @@ def _heads_block(device, stream, x, out, norm, weight, bias, eps, name, tokens, 
             raise MxidxError(f"{name} and {name}_out must have a contiguous last dim")
         if op == xp and out_strides != strides:
             raise MxidxError(f"{name}_out may be {name} itself only with the same strides")
-    wp = None if weight is None else _on(device, weight, f"{name}_weight", _torch().float32, (HEAD_DIM,))
-    bp = None if bias is None else _on(device, bias, f"{name}_bias", _torch().float32, (HEAD_DIM,))
+    wp = 0 if weight is None else _on(device, weight, f"{name}_weight", _torch().float32, (HEAD_DIM,))
+    bp = 0 if bias is None else _on(device, bias, f"{name}_bias", _torch().float32, (HEAD_DIM,))
     return _Heads(xp, op, strides[0], strides[1] if len(shape) == 3 else HEAD_DIM, out_strides[0],
                   out_strides[1] if len(shape) == 3 else HEAD_DIM, heads,
                   _code(_NORMS, norm, f"{name}_norm"), wp, bp, eps), out
@@ -1107,8 +1126,8 @@ def norm_rope(q, k, cos, sin, rope_dim, mode="neox", positions=None, q_norm="non
         qb, q_out = _heads_block(device, stream, q, q_out, q_norm, q_weight, q_bias, eps, "q", T, dtype)
     if k is not None:
         kb, k_out = _heads_block(device, stream, k, k_out, k_norm, k_weight, k_bias, eps, "k", T, dtype)
-    _call("idx_norm_rope", device, stream, None if qb is None else ctypes.addressof(qb),
-          None if kb is None else ctypes.addressof(kb), IDX_BF16 if dtype == torch.bfloat16 else IDX_F32,
+    _call("idx_norm_rope", device, stream, 0 if qb is None else ctypes.addressof(qb),
+          0 if kb is None else ctypes.addressof(kb), IDX_BF16 if dtype == torch.bfloat16 else IDX_F32,
           T, ctypes.addressof(rope))
     return (None if q is None else q_out), (None if k is None else k_out)
 
@@ -1139,9 +1158,9 @@ def _latent_insert(call, cache_of, kv, slot_mapping, cache, cos, sin, mode, posi
         raise MxidxError(f"kv must be [T, {latent + LATENT_ROPE}] with a contiguous last dim")
     T = shape[0]
     mp = _on(device, slot_mapping, "slot_mapping", torch.int64, (T,))
-    wp = None if weight is None else _on(device, weight, "weight", torch.float32, (latent,))
+    wp = 0 if weight is None else _on(device, weight, "weight", torch.float32, (latent,))
     rope = _rope_args(device, cos, sin, LATENT_ROPE, mode, positions, T)
-    qp = op = None
+    qp = op = 0
     H = qs = qh = os_ = oh = 0
     if q_pe is not None:
         qp = _on(device, q_pe, "q_pe", dtype)
@@ -1283,9 +1302,9 @@ def _attn_paged(call, cache_of, q, cache, block_table, ke, scale, indices, ks, r
     elif max_tokens > pages * PAGE_SIZE:
         raise MxidxError("block_table has fewer pages than max_tokens needs")
     ep = _on(device, ke, "ke", i32, (rows,))
-    kp = None if ks is None else _on(device, ks, "ks", i32, (rows,))
-    rp = None if row_seq is None else _on(device, row_seq, "row_seq", i32, (rows,))
-    ip, istride, k = None, 0, 0
+    kp = 0 if ks is None else _on(device, ks, "ks", i32, (rows,))
+    rp = 0 if row_seq is None else _on(device, row_seq, "row_seq", i32, (rows,))
+    ip, istride, k = 0, 0, 0
     if indices is not None:
         ip = _on(device, indices, "indices", i32)
         shape, strides = indices.shape, indices.stride()
@@ -1304,7 +1323,7 @@ def _attn_paged(call, cache_of, q, cache, block_table, ke, scale, indices, ks, r
     if lse is None:
         lse = _empty(stream, (rows, H), torch.float32, device)
     lp = _on(device, lse, "lse", torch.float32, (rows, H))
-    wp, wb = None, 0
+    wp, wb = 0, 0
     if workspace is None:
         need = attn_workspace_bytes(rows, H, latent, k if indices is not None else max_tokens)
         if need:
@@ -1388,7 +1407,7 @@ def attn_prompt(q, k, v, seq_lens, query_lens, scale, causal=True, max_seq_len=N
     if lse is None:
         lse = _empty(stream, (T, Hq), torch.float32, device, fill=float("-inf"))
     lp = _on(device, lse, "lse", torch.float32, (T, Hq))
-    wp, wb = None, 0
+    wp, wb = 0, 0
     if workspace is None:
         need = attn_prompt_workspace_bytes(T, Hq, Hk, dk, dv, B, max_seq_len)
         if need:

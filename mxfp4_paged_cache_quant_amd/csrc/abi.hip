@@ -4,6 +4,9 @@
 #include <atomic>
 #include <cstdlib>
 #include <cstring>
+#include <tuple>
+#include <type_traits>
+#include <utility>
 
 #include "mxidx.h"
 #include "launch.hpp"
@@ -851,6 +854,77 @@ int idx_attn_prompt(const void* q, int64_t q_row_stride, int64_t q_head_stride, 
                             v, S > 1 ? v_row_stride : dv, v_head_stride, S, Hk, seq_lens, query_lens, B, max_seq_len,
                             causal != 0, scale, out, out_row_stride, out_head_stride, lse};
   return launched(mxidx::launch_attn_prompt(a, dk, dv, workspace, stream));
+}
+
+}  // extern "C"
+
+namespace {
+
+// An argument of a call out of its 8-byte word; false: it does not fit.
+template <class T>
+bool from_word(int64_t word, T& x) {
+  if constexpr (std::is_pointer_v<T>) {
+    x = reinterpret_cast<T>(word);
+  } else if constexpr (std::is_floating_point_v<T>) {
+    double d;
+    std::memcpy(&d, &word, 8);
+    x = (T)d;
+  } else {
+    x = (T)word;
+    // a size has no sign, and nothing fits it twice
+    return (int64_t)x == word && (std::is_signed_v<T> || word >= 0);
+  }
+  return true;
+}
+
+template <class... A, size_t... i>
+int apply(int (*call)(A...), const char* words, std::index_sequence<i...>) {
+  std::tuple<A...> args;
+  const auto word = [&](size_t k) {
+    int64_t w;
+    std::memcpy(&w, words + 8 * k, 8);
+    return w;
+  };
+  if (!(from_word(word(i), std::get<i>(args)) && ...)) return IDX_ERR_ARG;
+  return call(std::get<i>(args)...);
+}
+
+template <auto call>
+struct Entry;
+template <class... A, int (*call)(A...)>
+struct Entry<call> {
+  static constexpr int kCount = sizeof...(A);
+  static int run(const char* words) { return apply(call, words, std::make_index_sequence<sizeof...(A)>()); }
+};
+
+struct EntryRow {
+  const char* name;
+  int count;
+  int (*run)(const char*);
+};
+#define MXIDX_ENTRY(f) {#f, Entry<f>::kCount, Entry<f>::run}
+const EntryRow kEntries[] = {
+    MXIDX_ENTRY(idx_step_map),        MXIDX_ENTRY(idx_norm_rope),
+    MXIDX_ENTRY(idx_latent_insert),   MXIDX_ENTRY(idx_latent_insert_mxfp4),
+    MXIDX_ENTRY(idx_latent_gather_mxfp4), MXIDX_ENTRY(idx_attn_paged),
+    MXIDX_ENTRY(idx_attn_paged_mxfp4), MXIDX_ENTRY(idx_attn_prompt),
+};
+#undef MXIDX_ENTRY
+constexpr int kEntryCount = sizeof(kEntries) / sizeof(kEntries[0]);
+
+}  // namespace
+
+extern "C" {
+
+int idx_entry(const char* name) {
+  for (int i = 0; name && i < kEntryCount; ++i)
+    if (std::strcmp(name, kEntries[i].name) == 0) return i;
+  return -1;
+}
+
+int idx_call(int entry, const void* words, int count) {
+  if (entry < 0 || entry >= kEntryCount || !words || count != kEntries[entry].count) return IDX_ERR_ARG;
+  return kEntries[entry].run(static_cast<const char*>(words));
 }
 
 }  // extern "C"
