@@ -110,6 +110,7 @@ typedef enum { IDX_BF16 = 0, IDX_F32 = 1 } idx_dtype;
 #define IDX_ATTN_MAX_PAGES ((1 << 26) - 1024)   /* row numbers are 32-bit in the kernel */
 #define IDX_ATTN_MAX_TOKENS 0x7ffffe00           /* places of a row: tiles beyond it still count in 32 bits */
 #define IDX_ATTN_MAX_ROWS (1 << 22)              /* and a launch has fewer than 2^32 lanes */
+#define IDX_PROMPT_MAX_SEQS 1024                 /* requests of a call: each workgroup looks its own up among them */
 #define IDX_PROMPT_MAX_STRIDE (1 << 23)          /* elements from one key or value row to the next */
 #define IDX_PROMPT_MAX_WORKSPACE (36ll << 20)    /* enough for every idx_attn_prompt call */
 #define IDX_GATHER_MAX_TOKENS (1 << 29)          /* of a sequence: a workgroup of 256 lanes a page */
@@ -758,7 +759,7 @@ int idx_attn_paged_mxfp4(const void* q, int64_t q_row_stride, int64_t q_head_str
  *   seq_lens, query_lens: [B] int32, as for idx_step_map: request b has seq_lens[b] tokens, the last
  *        query_lens[b] of them this call's rows (0: none).  Its rows begin at row
  *        sum(query_lens[:b]) of q, its keys and values at row sum(seq_lens[:b]) of k and v.
- *        Negative lengths count as 0.  Row i of a request stands at position seq_lens[b] -
+ *        Negative lengths count as 0; B <= IDX_PROMPT_MAX_SEQS.  Row i of a request stands at position seq_lens[b] -
  *        query_lens[b] + i (below 0 where it has more rows than tokens: with causal it sees none).
  *   causal: not 0: a row sees its request's tokens up to its own position; 0: all of them.
  *   q:   [T, Hq, dk] bf16, row (t, h) at q + t*q_row_stride + h*q_head_stride; rows behind the last

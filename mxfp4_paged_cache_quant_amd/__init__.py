@@ -1376,7 +1376,7 @@ def attn_prompt(q, k, v, seq_lens, query_lens, scale, causal=True, max_seq_len=N
     v [S, Hk, dv] (bf16, (dk, dv) one of PROMPT_DIMS, Hq a multiple of Hk): returns (out bf16
     [T, Hq, dv], lse fp32 [T, Hq]).
 
-    seq_lens / query_lens i32 [B], as step_map's: request b's seq_lens[b] tokens follow the requests'
+    seq_lens / query_lens i32 [B], B up to 1024, as step_map's: request b's seq_lens[b] tokens follow the requests'
     before it in k and v, the last query_lens[b] of them are its rows in q.  ``causal``: a row
     sees the tokens up to its own (else all of its request's).  Rows behind the last request's
     are zeros (lse -inf) in a new out and stay as they were in a given one.  ``max_seq_len``

@@ -195,3 +195,9 @@ def test_wrappers_refuse_host_tensors():
     with pytest.raises(mx.MxidxError):
         mx.attn_prompt(z((2, 2, 128), **bf), z((2, 2, 128), **bf), z((2, 2, 128), **bf), z(1, dtype=torch.int32),
                        z(1, dtype=torch.int32), 0.1)
+
+
+def test_prompt_refuses_more_requests_than_a_workgroup_looks_through(L):
+    assert L.idx_attn_prompt(*_args(PROMPT, B=1025)) == ERR_ARG
+    assert L.idx_attn_prompt_workspace_bytes(10, 4, 2, 128, 128, 1025, 300) == 0
+    assert L.idx_attn_prompt(*_args(PROMPT, B=1024, T=0)) == OK
