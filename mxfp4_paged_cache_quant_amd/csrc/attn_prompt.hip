@@ -134,12 +134,17 @@ __device__ Found find(const PromptArgs& a, const PromptParts& parts, uint32_t wa
   const uint32_t T = (uint32_t)a.T, tok = (uint32_t)parts.tok;   // T below 2^23: sums of 64 fit 32 bits
   uint32_t row0 = 0, tile0 = 0, item0 = 0;
   int64_t key0 = 0;
-  int n, len;
+  int n, len, next_n, next_len;                        // the next 64 requests' on their way
   uint32_t row, row_end, there, tiles;
-  auto load = [&](int b0) {
+  auto fetch = [&](int b0) {
     const int b = b0 + ln;
-    n = b < a.B ? max(a.query_lens[b], 0) : 0;
-    len = b < a.B ? max(a.seq_lens[b], 0) : 0;
+    next_n = b < a.B ? a.query_lens[b] : 0;
+    next_len = b < a.B ? a.seq_lens[b] : 0;
+  };
+  auto load = [&](int b0) {
+    n = max(next_n, 0);
+    len = max(next_len, 0);
+    fetch(b0 + kWave);
     const uint32_t mine = min((uint32_t)n, T);
     row_end = wave_scan(mine) + row0;
     row = row_end - mine;
@@ -154,6 +159,7 @@ __device__ Found find(const PromptArgs& a, const PromptParts& parts, uint32_t wa
     // products' and sums' roundings, each of 2^-24, come to less than 2^-8
     float work = 0.f;
     uint32_t all = 0;
+    fetch(0);
     for (int b0 = 0; b0 < a.B; b0 += kWave) {
       load(b0);
       work += wave_sum((float)tiles * (float)key_tiles());
@@ -166,6 +172,7 @@ __device__ Found find(const PromptArgs& a, const PromptParts& parts, uint32_t wa
   }
   Found f;
   f.tile = -1;
+  fetch(0);
   for (int b0 = 0; b0 < a.B; b0 += kWave) {
     load(b0);
     const uint32_t shares = parts.shares ? max((key_tiles() + length - 1) / length, 1u) : 1u, items = tiles * shares;
