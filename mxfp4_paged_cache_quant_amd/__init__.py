@@ -1244,7 +1244,8 @@ def latent_gather_mxfp4(cache, block_table, seq_lens, cu_seq_offsets, max_seq_le
     stride = strides[0] if B > 1 else max(pages, 1)
     sp = _on(device, seq_lens, "seq_lens", torch.int32, (B,))
     op = _on(device, cu_seq_offsets, "cu_seq_offsets", torch.int64)
-    if cu_seq_offsets.dim() != 1 or cu_seq_offsets.shape[0] < B or not cu_seq_offsets.is_contiguous():
+    shape = cu_seq_offsets.shape
+    if len(shape) != 1 or shape[0] < B or not cu_seq_offsets.is_contiguous():
         raise MxidxError(f"cu_seq_offsets must be a contiguous int64 of {B} offsets or more")
     width = latent + LATENT_ROPE
     if total_tokens < 0:
@@ -1252,11 +1253,11 @@ def latent_gather_mxfp4(cache, block_table, seq_lens, cu_seq_offsets, max_seq_le
     if out is None:
         out = _empty(stream, (total_tokens, width), torch.bfloat16, device, fill=0)
     rp = _on(device, out, "out", torch.bfloat16)
-    if out.dim() != 2 or out.shape[0] < total_tokens or out.shape[1] != width or \
-            (out.stride(1) != 1 and total_tokens):
+    shape, strides = out.shape, out.stride()
+    if len(shape) != 2 or shape[0] < total_tokens or shape[1] != width or (strides[1] != 1 and total_tokens):
         raise MxidxError(f"out must be [{total_tokens}, {width}] with a contiguous last dim")
     _call("idx_latent_gather_mxfp4", device, stream, cp, num_pages, PAGE_SIZE, latent, bp, stride, sp, op,
-          B, max_seq_len, total_tokens, rp, out.stride(0))
+          B, max_seq_len, total_tokens, rp, strides[0])
     return out
 
 
@@ -1387,7 +1388,7 @@ def attn_prompt(q, k, v, seq_lens, query_lens, scale, causal=True, max_seq_len=N
     bf16 = torch.bfloat16
     qp, kp, vp = _on(device, q, "q", bf16), _on(device, k, "k", bf16), _on(device, v, "v", bf16)
     qs, ks, vs = q.shape, k.shape, v.shape
-    if len(qs) != 3 or len(ks) != 3 or len(vs) != 3 or ks[2] != qs[2] or vs[:2] != ks[:2]:
+    if len(qs) != 3 or len(ks) != 3 or len(vs) != 3 or ks[2] != qs[2] or vs[0] != ks[0] or vs[1] != ks[1]:
         raise MxidxError("q, k and v must be [T, Hq, dk], [S, Hk, dk] and [S, Hk, dv]")
     (T, Hq, dk), (S, Hk, dv) = qs, vs
     (q0, q1, q2), (k0, k1, k2), (v0, v1, v2) = q.stride(), k.stride(), v.stride()
