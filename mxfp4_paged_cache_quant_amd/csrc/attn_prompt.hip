@@ -310,6 +310,14 @@ __global__ __launch_bounds__(kWaves * kWave, kWaves == 1 ? 1 : 2) void prompt_ke
       RowCopy<VC, kWaves>::template piece<false>(i, vr, tile + kKeyA + kKeyB, vstride, 0, wave, ln);
   };
 
+  // Where a lane reads of a tile's values: lane 4j + c of a 16-lane group token 4 half + j, values 4c..4c+3 of its 16
+  // (chunk 4v and on for part v: value_swz takes from a token what its steps of 8 leave as it is).  Opaque, as a
+  // sum that the compiler spreads over steps of an address hides from it which tile a read is of, and it
+  // then waits for the next one's copies before the reads.
+  int value_at = (4 * half + ((ln & 15) >> 2)) * (kDv * 2) +
+                 (((2 * ((ln >> 4) & 1) + ((ln & 3) >> 1)) ^ value_swz<VC>((ln & 15) >> 2)) << 4) + 8 * (ln & 1);
+  asm("" : "+v"(value_at));
+
   auto compute = [&](int t, MXIDX_LDS const uint8_t* tile) __attribute__((always_inline)) {
     const int first = t * kTile;
     if (first >= wave_hi) return;                      // uniform: no slot sees the tile
@@ -373,16 +381,12 @@ __global__ __launch_bounds__(kWaves * kWave, kWaves == 1 ? 1 : 2) void prompt_ke
         l += x + y;
         w[2 * p + j / 8][(j % 8) / 2] = pack2(x, y);
       }
-    // lane 4j + c of a 16-lane group reads token 4 half + j, values 4c..4c+3 of its 16
     auto values = [&](int i, v4s (&x)[2]) __attribute__((always_inline)) {
       const int u = i / NV, v = i % NV;
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int tok = 16 * u + 8 * e + 4 * half + ((ln & 15) >> 2);
-        const int chunk = 4 * v + 2 * ((ln >> 4) & 1) + ((ln & 3) >> 1);
-        x[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((MXIDX_LDS v4s*)(
-            tile + kKeyA + kKeyB + tok * (kDv * 2) + ((chunk ^ value_swz<VC>(tok)) << 4) + 8 * (ln & 1)));
-      }
+      for (int e = 0; e < 2; ++e)
+        x[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (MXIDX_LDS v4s*)(tile + ((value_at ^ (v << 6)) + kKeyA + kKeyB + (16 * u + 8 * e) * (kDv * 2))));
     };
     v4s y[kValuesAhead][2];
 #pragma unroll

@@ -19,3 +19,25 @@ def test_codes_of_the_next_tile_are_on_their_way():
         assert "copy" in loop
         for a, b in zip(loop, loop[1:]):
             assert not (a in ("copy", "load") and b == "wait"), name
+
+
+def _waits_before_products(events):
+    """Whether a wait for every load stands between a tile's copies and its products."""
+    waited = False
+    for event in _main_loop(events):
+        if event in ("copy", "barrier"):
+            waited = False
+        elif event == "wait":
+            waited = True
+        elif event == "mfma" and waited:
+            return True
+    return False
+
+
+def test_prompt_tiles_are_on_their_way_under_both_products():
+    forms = {n: e for n, e in kernels("attn_prompt.hip").items() if n.startswith("prompt_kernel")}
+    assert len(forms) == 6
+    for name, events in forms.items():
+        loop = _main_loop(events)
+        assert "copy" in loop and "transpose" in loop
+        assert not _waits_before_products(events), name
