@@ -740,8 +740,11 @@ int idx_attn_paged(const void* q, int64_t q_row_stride, int64_t q_head_stride, i
                    float* lse, void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 /* idx_attn_paged_mxfp4 -- idx_attn_paged over the MXFP4 latent cache (idx_latent_insert_mxfp4's): the
- * same arguments, limits, workspace sizes and arithmetic, the cached rows being what their codes,
- * scales and positional values stand for (exact in bf16). */
+ * same arguments, limits and arithmetic, the cached rows being what their codes, scales and
+ * positional values stand for (exact in bf16).
+ *   workspace: as there, of idx_attn_workspace_bytes_mxfp4(...) bytes: idx_attn_workspace_bytes(...), or 0 for
+ *        windows of few tokens (up to 320, 256 and 192 of latent 128, 256 and 512), whose rows are not split. */
+size_t idx_attn_workspace_bytes_mxfp4(int64_t rows, int H, int latent, int64_t entries);
 int idx_attn_paged_mxfp4(const void* q, int64_t q_row_stride, int64_t q_head_stride, int64_t rows, int H,
                          int latent, const uint8_t* cache, int64_t num_pages, int page_size,
                          const int32_t* block_table, int64_t bt_row_stride, int B,

@@ -141,6 +141,7 @@ EXPORTS = {
     "idx_latent_gather_mxfp4": (_int, [_c_void_p, _i64, _int, _int, _c_void_p, _i64, _c_void_p,
                                        _c_void_p, _int, _i64, _i64, _c_void_p, _i64, _c_void_p]),
     "idx_attn_workspace_bytes": (ctypes.c_size_t, [_i64, _int, _int, _i64]),
+    "idx_attn_workspace_bytes_mxfp4": (ctypes.c_size_t, [_i64, _int, _int, _i64]),
     "idx_attn_workspace_max_bytes": (ctypes.c_size_t, [_i64, _int, _int, _i64]),
     "idx_attn_paged": (_int, [_c_void_p, _i64, _i64, _i64, _int, _int, _c_void_p, _i64, _int,
                               _c_void_p, _i64, _int, _c_void_p, _c_void_p, _c_void_p, _c_void_p,
@@ -1261,9 +1262,11 @@ def latent_gather_mxfp4(cache, block_table, seq_lens, cu_seq_offsets, max_seq_le
     return out
 
 
-def attn_workspace_bytes(rows, heads, latent, entries):
-    """Workspace bytes of attn_paged; entries: k with indices, else max_tokens (0: no workspace).
-    Fewer rows, heads or entries may need more."""
+def attn_workspace_bytes(rows, heads, latent, entries, mxfp4=False):
+    """Workspace bytes of attn_paged, or of attn_paged_mxfp4; entries: k with indices, else max_tokens
+    (0: no workspace).  Fewer rows, heads or entries may need more."""
+    if mxfp4:
+        return int(lib().idx_attn_workspace_bytes_mxfp4(rows, heads, latent, entries))
     return int(lib().idx_attn_workspace_bytes(rows, heads, latent, entries))
 
 
@@ -1326,7 +1329,8 @@ def _attn_paged(call, cache_of, q, cache, block_table, ke, scale, indices, ks, r
     lp = _on(device, lse, "lse", torch.float32, (rows, H))
     wp, wb = 0, 0
     if workspace is None:
-        need = attn_workspace_bytes(rows, H, latent, k if indices is not None else max_tokens)
+        need = attn_workspace_bytes(rows, H, latent, k if indices is not None else max_tokens,
+                                    call == "idx_attn_paged_mxfp4")
         if need:
             workspace = _empty(stream, need, torch.uint8, device)
     if workspace is not None:

@@ -741,7 +741,12 @@ static bool attn_sizes_ok(int64_t rows, int H, int latent, int64_t max_tokens) {
 
 size_t idx_attn_workspace_bytes(int64_t rows, int H, int latent, int64_t entries) {
   if (!attn_sizes_ok(rows, H, latent, entries)) return 0;
-  return (size_t)mxidx::attn_workspace_bytes(rows, H, latent, entries);
+  return (size_t)mxidx::attn_workspace_bytes(rows, H, latent, entries, false);
+}
+
+size_t idx_attn_workspace_bytes_mxfp4(int64_t rows, int H, int latent, int64_t entries) {
+  if (!attn_sizes_ok(rows, H, latent, entries)) return 0;
+  return (size_t)mxidx::attn_workspace_bytes(rows, H, latent, entries, true);
 }
 
 size_t idx_attn_workspace_max_bytes(int64_t rows, int H, int latent, int64_t entries) {
@@ -777,7 +782,9 @@ static int attn_paged(const void* q, int64_t q_row_stride, int64_t q_head_stride
     return IDX_ERR_ARG;
   if (max_tokens > 0 && (!block_table || !aligned(block_table, 4))) return IDX_ERR_ARG;
   if (num_pages > 0 && (!cache || !aligned(cache, 16))) return IDX_ERR_ARG;
-  const size_t need = idx_attn_workspace_bytes(rows, H, latent, indices ? k : max_tokens);
+  const int64_t entries = indices ? k : max_tokens;
+  const size_t need = mx ? idx_attn_workspace_bytes_mxfp4(rows, H, latent, entries)
+                         : idx_attn_workspace_bytes(rows, H, latent, entries);
   if (need > 0 && (!workspace || !aligned(workspace, 256) || workspace_bytes < need))
     return IDX_ERR_ARG;
   int st = gate_current();

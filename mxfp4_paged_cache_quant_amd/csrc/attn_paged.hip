@@ -902,7 +902,7 @@ int64_t split_places(int latent) { return latent <= 128 ? 2 * kCus : kCus; }
 // the second launch costs as much as the tiles that it saves (one row of 8 heads, 129 tokens, in a
 // graph and called one by one: 6.9 / 9.3 us, 8.0 / 12.1 split, latent 128; 8.6 / 9.4 and 9.8 / 11.9,
 // 256; 12.0 / 12.0 and 12.4 / 12.8, 512; of 385 tokens, latent 256, 13.4 / 13.4 and 10.2 / 11.9).
-Plan plan_of(int64_t rows, int H, int latent, int64_t entries, bool mx = false) {
+Plan plan_of(int64_t rows, int H, int latent, int64_t entries, bool mx) {
   Plan p;
   const int64_t tiles = (entries + 63) / 64, quarter = std::min<int64_t>((tiles + 3) / 4, kMaxSplits);
   const int64_t places = split_places(latent);
@@ -975,8 +975,8 @@ hipError_t launch(const AttnArgs& a, void* workspace, hipStream_t stream) {
 
 }  // namespace
 
-int64_t attn_workspace_bytes(int64_t rows, int H, int latent, int64_t entries) {
-  const Plan p = plan_of(rows, H, latent, entries);
+int64_t attn_workspace_bytes(int64_t rows, int H, int latent, int64_t entries, bool mx) {
+  const Plan p = plan_of(rows, H, latent, entries, mx);
   return p.splits == 1 ? 0 : part_bytes(rows * p.splits * p.heads, latent);
 }
 

@@ -236,7 +236,7 @@ struct AttnArgs {
   float* lse;
 };
 // Workspace bytes for rows whose windows (or lists) hold up to `entries` tokens.
-int64_t attn_workspace_bytes(int64_t rows, int H, int latent, int64_t entries);
+int64_t attn_workspace_bytes(int64_t rows, int H, int latent, int64_t entries, bool mx);
 // The same, of any call with up to so many rows, heads and entries.
 int64_t attn_workspace_max_bytes(int64_t rows, int H, int latent, int64_t entries);
 // mx: over MXFP4 pages (latent_mxfp4.hpp).
