@@ -41,7 +41,7 @@ def _functions(asm):
 
 def _event(line):
     """edge: a label or branch; mfma; copy: a load to LDS; load; transpose: a transposing LDS read; wait:
-    for every load; barrier."""
+    for every load, wait n: but for the youngest n; barrier."""
     op = line.split()[0] if line else ""
     if re.match(r"\.LBB\w+:", line) or op.startswith(("s_cbranch", "s_branch")):
         return "edge"
@@ -51,6 +51,7 @@ def _event(line):
         return "copy" if line.endswith(" lds") or "_lds_" in op else "load"
     if op.startswith("ds_read_b64_tr"):
         return "transpose"
-    if op == "s_waitcnt" and "vmcnt(0)" in line:
-        return "wait"
+    left = re.search(r"vmcnt\((\d+)\)", line) if op == "s_waitcnt" else None
+    if left:
+        return "wait" if left.group(1) == "0" else "wait " + left.group(1)
     return "barrier" if op == "s_barrier" else None

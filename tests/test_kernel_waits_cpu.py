@@ -41,3 +41,26 @@ def test_prompt_tiles_are_on_their_way_under_both_products():
         loop = _main_loop(events)
         assert "copy" in loop and "transpose" in loop
         assert not _waits_before_products(events), name
+
+
+def test_counted_waits_count_the_loads_of_codes():
+    # a step waits for all but the loads of the tile behind: as many as the compiler made of them
+    forms = {n: e for n, e in kernels("attn_paged.hip").items() if n.startswith("attn_kernel") and n.endswith("true>")}
+    for name, events in forms.items():
+        loop, found = _main_loop(events), 0
+        for at, event in enumerate(loop):
+            if event != "barrier":
+                continue
+            back = at - 1
+            while loop[back] == "edge":
+                back -= 1
+            if not loop[back].startswith("wait "):
+                continue                     # behind the loop
+            left, loads = int(loop[back].split()[1]), 0
+            while loop[back] not in ("copy", "load"):
+                back -= 1
+            while loop[back] in ("copy", "load"):
+                loads, back = loads + 1, back - 1
+            assert loads == left, (name, loads, left)
+            found += 1
+        assert found >= 1, name
