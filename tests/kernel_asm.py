@@ -41,7 +41,7 @@ def _functions(asm):
 
 def _event(line):
     """edge: a label or branch; mfma; copy: a load to LDS; load; transpose: a transposing LDS read; wait:
-    for every load, wait n: but for the youngest n; barrier."""
+    for every load, wait n: but for the youngest n; barrier; spill: a register in memory."""
     op = line.split()[0] if line else ""
     if re.match(r"\.LBB\w+:", line) or op.startswith(("s_cbranch", "s_branch")):
         return "edge"
@@ -49,6 +49,8 @@ def _event(line):
         return "mfma"
     if op.startswith(("buffer_load", "global_load")):
         return "copy" if line.endswith(" lds") or "_lds_" in op else "load"
+    if op.startswith("scratch_"):
+        return "spill"
     if op.startswith("ds_read_b64_tr"):
         return "transpose"
     left = re.search(r"vmcnt\((\d+)\)", line) if op == "s_waitcnt" else None

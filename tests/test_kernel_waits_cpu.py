@@ -64,3 +64,11 @@ def test_counted_waits_count_the_loads_of_codes():
             assert loads == left, (name, loads, left)
             found += 1
         assert found >= 1, name
+
+
+@pytest.mark.parametrize("source,forms", [("attn_paged.hip", 48), ("attn_prompt.hip", 6)])
+def test_no_register_spills_to_memory(source, forms):
+    # it would be read back behind the copies on their way
+    found = {n: e for n, e in kernels(source).items() if "mfma" in e}
+    assert len(found) == forms
+    assert not [n for n, e in found.items() if "spill" in e]
