@@ -780,7 +780,8 @@ int idx_attn_paged_mxfp4(const void* q, int64_t q_row_stride, int64_t q_head_str
  *        max_seq_len) bytes, as for idx_attn_paged; IDX_PROMPT_MAX_WORKSPACE are enough for every call.
  * Products are exact, sums and softmax statistics fp32; the weights take the second product rounded
  * to bf16, relative to the running maximum (the largest is exactly 1), the statistics unrounded; the
- * output is rounded once.  Equal calls give equal bits; the order of a row's sums depends on T, Hq, Hk, B
+ * output is rounded once.  Roundings of different weights average out; many equal ones leave up to
+ * 2^-8 of the output beside its own rounding.  Equal calls give equal bits; the order of a row's sums depends on T, Hq, Hk, B
  * and max_seq_len. */
 size_t idx_attn_prompt_workspace_bytes(int64_t T, int Hq, int Hk, int dk, int dv, int B, int64_t max_seq_len);
 int idx_attn_prompt(const void* q, int64_t q_row_stride, int64_t q_head_stride, int64_t T, int Hq, const void* k,

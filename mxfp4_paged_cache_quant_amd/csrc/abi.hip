@@ -762,7 +762,7 @@ static int attn_paged(const void* q, int64_t q_row_stride, int64_t q_head_stride
                       const int32_t* indices, int64_t idx_row_stride, int k, int64_t max_tokens,
                       float scale, void* out, int64_t out_row_stride, int64_t out_head_stride,
                       float* lse, void* workspace, size_t workspace_bytes, bool mx,
-                         hipStream_t stream) {
+                      hipStream_t stream) {
   if (!attn_sizes_ok(rows, H, latent, max_tokens) || page_size != IDX_PAGE_SIZE || num_pages < 0 ||
       num_pages > IDX_ATTN_MAX_PAGES || B < 0)
     return IDX_ERR_ARG;

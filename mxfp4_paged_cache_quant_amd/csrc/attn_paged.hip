@@ -62,6 +62,13 @@
 // 64 heads, 52.6 (57), 16 rows of 2048, 64 heads, 25.6 (24.6).  Steps: codes in registers a tile ahead
 // (20 of them spilled) 476 us for the 1024 rows; copied to LDS two tiles ahead, 32-bit addresses and
 // no spills 404; sixteen lanes' stores on all banks, and scales four a lane where registers lack, 387.
+// Two things that are left cost no time.  The first of those stores waits for the positional rows' copies,
+// which go to the same array; with arrays of their own that wait is gone and the 1024 rows take 386
+// us, the windows 107, the 16 rows 25.5.  Of the LDS's busy cycles 17% are bank conflicts, a fifth of them
+// of the codes' reads (lanes 16 apart); without those 394 and 393 us, 107 and 107.
+// Beyond 4 GiB the copies of codes take 64-bit addresses, which only the flat form of a copy to LDS has for
+// each lane, and the compiler's first wait in a step is then for all of them: 1024 rows of 2048 tokens, 64 heads 397 us
+// over 5 GB and 371 over 1, 16 heads 291 and 234; 32 windows of 6600, 128 heads 99.6 and 95.
 #include <algorithm>
 
 #include "common.hpp"
@@ -259,7 +266,7 @@ struct MxCopy {
   static constexpr int kYoungest = kSpare ? 2 * kLoads : kLoads + 1;                // instructions of load()
   static constexpr int kRawBytes = kLoads * kWave * 16;                            // of the wave
   static constexpr int SD = LB / 4;                    // dwords of a token's scales
-static constexpr int kDwords = 4 * kLoads;           // a lane's
+  static constexpr int kDwords = 4 * kLoads;           // a lane's
   static_assert(kMine % kPosPer == 0 && (kMine % kPer == 0 || kMine < kPer) && kMine * SD <= kWave, "whole instructions");
   static_assert(Page::kBytes % 256 == 0 && Page::kBytes < 65536, "a row's place fits its page's lowest bits");
 

@@ -19,14 +19,22 @@
 // 8+4h..8+4h+3 of 16), and the running maximum and sum are one register each.
 //
 // The weights go to the second product rounded to bf16 (2^-8), relative to the running maximum itself, so
-// that a token that dominates a row weighs exactly 1; l and lse take them unrounded.  The output's
-// error is 1.1-1.2 times its own rounding's.  A second part of the weights, as the attention over the
+// that a token that dominates a row weighs exactly 1; l and lse take them unrounded.  Where the roundings of
+// many different weights average out the output's error is 1.06-1.10 times its own rounding's.
+// Equal weights all round the same way: where one token has the maximum and thousands share a lower
+// score, the output is off by up to 2^-8 of itself beside its own rounding, of 2^-8 too.
+// Divided by the sum of the rounded weights it would not be (16 dot products with ones a tile more), but
+// every instruction counts here: a prompt of 16384 tokens 1247 -> 1307 us, of 8192 tokens, heads of 128, 293 -> 303, heads of
+// 64 170 -> 182, for errors of 1.05-1.09.  A second part of the weights, as the attention over the
 // cache has it, would be half as many products again where the products are what bounds the kernel.
 //
 // What bounds it: with many rows the card's power.  A prompt of 16384 tokens, 16 heads of 192 / 128,
 // takes 1.25-1.3 ms = 1,050-1,100 TFLOP/s at 1.4-1.7 GHz, where a large library product reaches
 // 1,310-1,400 (inputs of zeros: 0.9 ms); of the SIMDs' cycles 60% are MFMAs, and no LDS access
-// meets a bank conflict.  Steps: operands kept three and four steps ahead (1286 -> 1247 us; heads of
+// meets a bank conflict.  Smaller heads are bound by instruction issue: the softmax of a tile is the same
+// work beside 32 MFMAs (128) or 16 (64) as beside 40 (192 / 128), so that 6.0 and 11.4 other vector
+// instructions go with an MFMA, 4.5 there; MFMAs are busy 45% and 37% of the time at 1.9-2.0 GHz, and waves
+// wait for an issue slot 40-43% of their cycles.  Steps: operands kept three and four steps ahead (1286 -> 1247 us; heads of
 // 64, four prompts of 4000, 191 -> 169); two to four steps ahead, values read before the weights
 // are there, and a wave priority for the products: all within 1%.  Scores a tile ahead of the weights in
 // one wave (its registers are full): 298 and 303 us for a prompt of 8192 tokens, 16 heads of 128.  Eight
