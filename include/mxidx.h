@@ -110,6 +110,7 @@ typedef enum { IDX_BF16 = 0, IDX_F32 = 1 } idx_dtype;
 #define IDX_ATTN_MAX_PAGES ((1 << 26) - 1024)   /* row numbers are 32-bit in the kernel */
 #define IDX_ATTN_MAX_TOKENS 0x7ffffe00           /* places of a row: tiles beyond it still count in 32 bits */
 #define IDX_ATTN_MAX_ROWS (1 << 22)              /* and a launch has fewer than 2^32 lanes */
+#define IDX_PROMPT_MAX_HEADS 256                 /* query heads of idx_attn_prompt */
 #define IDX_PROMPT_MAX_SEQS 1024                 /* requests of a call: each workgroup looks its own up among them */
 #define IDX_PROMPT_MAX_STRIDE (1 << 23)          /* elements from one key or value row to the next */
 #define IDX_PROMPT_MAX_WORKSPACE (36ll << 20)    /* enough for every idx_attn_prompt call */
@@ -771,7 +772,7 @@ int idx_attn_paged_mxfp4(const void* q, int64_t q_row_stride, int64_t q_head_str
  *        IDX_PROMPT_MAX_STRIDE; tokens past S count as not there.  May be NULL where S is 0.
  *        The requests' tokens are finite: where some of a request's rows see a token and others do
  *        not, its value takes part in the others' products with weight 0.
- *   Hq a multiple of Hk, 1 <= Hq <= 128; (dk, dv): (64, 64), (128, 128) or (192, 128).  q, k, v 16-byte
+ *   Hq a multiple of Hk, 1 <= Hq <= IDX_PROMPT_MAX_HEADS; (dk, dv): (64, 64), (128, 128) or (192, 128).  q, k, v 16-byte
  *        aligned, strides multiples of 8.  T <= IDX_ATTN_MAX_ROWS.
  *   max_seq_len: host-side upper bound of seq_lens: later tokens are not read.
  *   out: [T, Hq, dv] bf16, strides multiples of 4, 8-byte aligned; lse: [T, Hq] fp32 or NULL.  They

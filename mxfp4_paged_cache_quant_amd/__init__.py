@@ -1378,7 +1378,7 @@ def attn_prompt_workspace(device="cuda"):
 def attn_prompt(q, k, v, seq_lens, query_lens, scale, causal=True, max_seq_len=None, out=None, lse=None,
                 workspace=None, stream=None):
     """Attention of packed requests over contiguous keys and values: q [T, Hq, dk], k [S, Hk, dk],
-    v [S, Hk, dv] (bf16, (dk, dv) one of PROMPT_DIMS, Hq a multiple of Hk): returns (out bf16
+    v [S, Hk, dv] (bf16, (dk, dv) one of PROMPT_DIMS, Hq a multiple of Hk, up to 256): returns (out bf16
     [T, Hq, dv], lse fp32 [T, Hq]).
 
     seq_lens / query_lens i32 [B], B up to 1024, as step_map's: request b's seq_lens[b] tokens follow the requests'

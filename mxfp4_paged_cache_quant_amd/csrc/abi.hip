@@ -823,7 +823,7 @@ int idx_attn_paged_mxfp4(const void* q, int64_t q_row_stride, int64_t q_head_str
 // Sizes that the kernel's grid and indexes take; T and B above 0.
 static bool prompt_sizes_ok(int64_t T, int Hq, int Hk, int dk, int dv, int64_t S, int B, int64_t max_seq_len) {
   const bool dims = (dk == 64 && dv == 64) || (dk == 128 && dv == 128) || (dk == 192 && dv == 128);
-  if (!dims || T < 0 || T > IDX_ATTN_MAX_ROWS || Hq < 1 || Hq > IDX_MAX_HEADS || Hk < 1 || Hq % Hk != 0 || S < 0 ||
+  if (!dims || T < 0 || T > IDX_ATTN_MAX_ROWS || Hq < 1 || Hq > IDX_PROMPT_MAX_HEADS || Hk < 1 || Hq % Hk != 0 || S < 0 ||
       S > ((int64_t)1 << 40) || B < 0 || B > IDX_PROMPT_MAX_SEQS || max_seq_len < 0 || max_seq_len > IDX_ATTN_MAX_TOKENS)
     return false;
   return T == 0 || B == 0 || mxidx::prompt_lanes(T, Hq, Hk, B, max_seq_len) < ((int64_t)1 << 32);
